@@ -35,6 +35,8 @@ __all__ = [
     "conv_wgrad_i8_ws", "conv_wgrad_i8_workspace_size", "conv_wgrad_i8_plain", "conv_wgrad_i8_plan", "MODE_CROSS_CORRELATION",
     "MODE_CONVOLUTION",
     "status_string", "LIB_PATH", "DT_INT8", "DT_INT32", "MAX_REDUCTION", "lib",
+    "linear", "linear_plan", "linear_backward", "linear_backward_plan", "layer_norm", "layer_norm_i8",
+    "layer_norm_backward",
 ]
 
 # CONV_I8_LIB names another build of the library (the host-sanitizer test
@@ -601,3 +603,8 @@ def conv_wgrad_i8(x: torch.Tensor, dy: torch.Tensor, dw: torch.Tensor, pre_paddi
     ws = _workspace(n, dw.device, stream)
     return conv_wgrad_i8_ws(x, dy, dw, ws, pre_padding, post_padding, stride, dilation, padding,
                             mode, stream)
+
+
+# The dense layer and layer norm (a library of their own, bound in dense.py)
+from .dense import (layer_norm, layer_norm_backward, layer_norm_i8, linear, linear_backward,  # noqa: E402
+                    linear_backward_plan, linear_plan)

@@ -1,9 +1,10 @@
-"""Build libconv_i8.so (HIP, gfx950 only) in-tree with hipcc."""
+"""Build libconv_i8.so and libdense.so (HIP, gfx950 only) in-tree with hipcc."""
 from __future__ import annotations
 
 import os
 import subprocess
 import sys
+import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,6 +19,12 @@ HEADERS = [os.path.join(CSRC, f) for f in ("kernel_common.hpp", "igemm_kernel.hp
                                                "repack_kernel.hpp")] + [
     os.path.join(INCLUDE, "conv_i8.h")]
 
+# The dense layer and layer norm: a library of their own, one object per source
+DENSE_CSRC = os.path.join(PKG, "csrc_dense")
+DENSE_LIB = os.path.join(LIB_DIR, "libdense.so")
+DENSE_SOURCES = [os.path.join(DENSE_CSRC, f) for f in ("linear.hip", "gemm_bf16.hip", "gemm_f16.hip", "gemm_i8.hip",
+                                                      "norm.hip")]
+
 HIP_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",
     "-Wall", "-Wno-unused-function", "-Wno-inline-asm",
@@ -26,23 +33,47 @@ HIP_FLAGS = [
 ]
 
 
-def build(verbose: bool = False) -> str:
-    os.makedirs(LIB_DIR, exist_ok=True)
-    tmp = LIB + ".tmp"
-    cmd = [HIPCC, *HIP_FLAGS, "-I", INCLUDE, "-I", CSRC, *SOURCES, "-o", tmp]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    r = subprocess.run(cmd, capture_output=True, text=True)
+def _run(cmds: list, verbose: bool) -> None:
+    """Runs the compiler commands side by side; raises if one fails."""
+    started = []
+    for cmd in cmds:
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        log = tempfile.TemporaryFile("w+")
+        started.append((subprocess.Popen(cmd, stdout=log, stderr=subprocess.STDOUT), log))
     # the host pass does not know the packed-fp32 feature name; drop that noise
     noise = "is not a recognized feature for this target"
-    msgs = [l for l in (r.stdout + r.stderr).splitlines() if noise not in l]
-    if r.returncode != 0:
-        raise RuntimeError("hipcc failed:\n" + "\n".join(msgs))
-    if verbose and msgs:
-        print("\n".join(msgs))
-    os.replace(tmp, LIB)
+    failed = []
+    for p, log in started:
+        rc = p.wait()
+        log.seek(0)
+        msgs = [l for l in log.read().splitlines() if noise not in l]
+        log.close()
+        if rc != 0:
+            failed += msgs
+        elif verbose and msgs:
+            print("\n".join(msgs))
+    if failed:
+        raise RuntimeError("hipcc failed:\n" + "\n".join(failed))
+
+
+def build(verbose: bool = False, dense_only: bool = False) -> str:
+    """Compiles both libraries, all sources side by side (the convolution's
+    takes minutes), or only the dense one."""
+    os.makedirs(LIB_DIR, exist_ok=True)
+    tmp, dense_tmp = LIB + ".tmp", DENSE_LIB + ".tmp"
+    objects = [os.path.join(LIB_DIR, os.path.basename(s)[:-4] + ".o") for s in DENSE_SOURCES]
+    compile_flags = [f for f in HIP_FLAGS if f != "-shared"]
+    cmds = [] if dense_only else [[HIPCC, *HIP_FLAGS, "-I", INCLUDE, "-I", CSRC, *SOURCES, "-o", tmp]]
+    cmds += [[HIPCC, *compile_flags, "-I", INCLUDE, "-I", DENSE_CSRC, "-c", s, "-o", o]
+             for s, o in zip(DENSE_SOURCES, objects)]
+    _run(cmds, verbose)
+    _run([[HIPCC, "--offload-arch=gfx950", "-fPIC", "-shared", *objects, "-o", dense_tmp]], verbose)
+    if not dense_only:
+        os.replace(tmp, LIB)
+    os.replace(dense_tmp, DENSE_LIB)
     return LIB
 
 
 if __name__ == "__main__":
-    print(build(verbose="-v" in sys.argv))
+    print(build(verbose="-v" in sys.argv, dense_only="--dense" in sys.argv))

@@ -1,0 +1,362 @@
+// Shared pieces of the dense layer's and layer norm's kernels for gfx950:
+// element types, unaligned 16-byte loads and stores, activations and their
+// slopes, direct-to-LDS loads, wave reductions and the tile order.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "dense.h"
+
+namespace dense {
+
+typedef __bf16 bf16;
+typedef _Float16 f16;
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef int v4i __attribute__((ext_vector_type(4)));
+typedef int v16i __attribute__((ext_vector_type(16)));
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) v4s lds_v4s;
+typedef __attribute__((address_space(3))) void lds_void;
+
+constexpr int kCUs = 256;
+// Buffer offset outside every resource (ranges stay below 2^31): a load from
+// it returns zeros.
+constexpr int kOutOfRange = (int)0x80000000u;
+
+template <typename T> struct Code;
+template <> struct Code<int8_t> { static constexpr int v = DENSE_INT8; };
+template <> struct Code<bf16> { static constexpr int v = DENSE_BF16; };
+template <> struct Code<f16> { static constexpr int v = DENSE_FP16; };
+template <> struct Code<float> { static constexpr int v = DENSE_FP32; };
+
+inline int dtype_size(int64_t dt)
+{
+    return dt == DENSE_INT8 ? 1 : dt == DENSE_FP32 ? 4 : dt == DENSE_BF16 || dt == DENSE_FP16 ? 2 : 0;
+}
+
+// Eight values at any element-aligned address.  gfx950 runs with unaligned
+// vector access enabled, so these are one or two 16-byte instructions whatever
+// the address; an address that is a multiple of 16 costs nothing extra.
+template <typename T>
+struct __attribute__((packed, aligned(sizeof(T)))) Pack8 {
+    T e[8];
+};
+
+template <typename T>
+__device__ __forceinline__ void load8(const T *p, float (&v)[8])
+{
+    const Pack8<T> q = *(const Pack8<T> *)p;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        v[i] = (float)q.e[i];
+}
+
+template <typename T>
+__device__ __forceinline__ void store8(T *p, const float (&v)[8])
+{
+    Pack8<T> q;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        q.e[i] = (T)v[i];
+    *(Pack8<T> *)p = q;
+}
+
+// The first n of eight values (n may be 8 or more); the others read as `fill`.
+template <typename T>
+__device__ __forceinline__ void load8n(const T *p, int n, float (&v)[8], float fill = 0.0f)
+{
+    if (n >= 8) {
+        load8(p, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = i < n ? (float)p[i] : fill;
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void store8n(T *p, int n, const float (&v)[8])
+{
+    if (n >= 8) {
+        store8(p, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n)
+                p[i] = (T)v[i];
+    }
+}
+
+// The same with the element type given at run time (uniform over the launch).
+__device__ __forceinline__ void load8n_dt(const void *p, int dt, int64_t off, int n, float (&v)[8])
+{
+    if (dt == DENSE_BF16)
+        load8n((const bf16 *)p + off, n, v);
+    else if (dt == DENSE_FP16)
+        load8n((const f16 *)p + off, n, v);
+    else
+        load8n((const float *)p + off, n, v);
+}
+
+__device__ __forceinline__ void store8n_dt(void *p, int dt, int64_t off, int n, const float (&v)[8])
+{
+    if (dt == DENSE_BF16)
+        store8n((bf16 *)p + off, n, v);
+    else if (dt == DENSE_FP16)
+        store8n((f16 *)p + off, n, v);
+    else
+        store8n((float *)p + off, n, v);
+}
+
+__device__ __forceinline__ float load_dt(const void *p, int dt, int64_t i)
+{
+    return dt == DENSE_BF16 ? (float)((const bf16 *)p)[i]
+         : dt == DENSE_FP16 ? (float)((const f16 *)p)[i]
+                            : ((const float *)p)[i];
+}
+
+__device__ __forceinline__ void store_dt(void *p, int dt, int64_t i, float v)
+{
+    if (dt == DENSE_BF16)
+        ((bf16 *)p)[i] = (bf16)v;
+    else if (dt == DENSE_FP16)
+        ((f16 *)p)[i] = (f16)v;
+    else
+        ((float *)p)[i] = v;
+}
+
+// 1 / (1 + exp(-x)) from the hardware's exp2 and reciprocal (1 ulp each; the
+// product with log2 e costs |x| 2^-24 relative, far below a 16-bit rounding).
+// exp2 overflows to infinity and its reciprocal to 0, so both tails are exact.
+__device__ __forceinline__ float sigmoid(float x)
+{
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504088896f * x));
+}
+
+constexpr float kGeluC = 0.797884560802865f;   // sqrt(2/pi)
+constexpr float kGeluA = 0.044715f;
+constexpr float kSqrtHalf = 0.707106781186548f;
+constexpr float kInvSqrt2Pi = 0.398942280401433f;
+
+// 0.5 (1 + tanh u) = sigmoid(2u), so the tanh form of gelu is z sigmoid(2u).
+__device__ __forceinline__ float gelu_tanh_gate(float z)
+{
+    return sigmoid(2.0f * kGeluC * (z + kGeluA * z * z * z));
+}
+
+// Normal distribution function through erfc, which keeps its relative
+// precision in the lower tail.
+__device__ __forceinline__ float normal_cdf(float z)
+{
+    return 0.5f * erfcf(-kSqrtHalf * z);
+}
+
+template <int ACT>
+__device__ __forceinline__ float activate(float z)
+{
+    if constexpr (ACT == DENSE_ACT_RELU)
+        return z < 0.0f ? 0.0f : z;  // keeps a NaN
+    else if constexpr (ACT == DENSE_ACT_GELU)
+        return z * normal_cdf(z);
+    else if constexpr (ACT == DENSE_ACT_GELU_TANH)
+        return z * gelu_tanh_gate(z);
+    else if constexpr (ACT == DENSE_ACT_SILU)
+        return z * sigmoid(z);
+    else
+        return z;
+}
+
+template <int ACT>
+__device__ __forceinline__ float act_slope(float z)
+{
+    if constexpr (ACT == DENSE_ACT_RELU) {
+        return z > 0.0f ? 1.0f : z == z ? 0.0f : z;
+    } else if constexpr (ACT == DENSE_ACT_GELU) {
+        return normal_cdf(z) + z * kInvSqrt2Pi * __builtin_amdgcn_exp2f(-0.72134752044448f * z * z);
+    } else if constexpr (ACT == DENSE_ACT_GELU_TANH) {
+        // p + z p (1 - p) 2u'(z); z^2 is bounded where p (1 - p) is already 0,
+        // so that it cannot overflow against it
+        const float p = gelu_tanh_gate(z);
+        const float z2 = fminf(z * z, 1.0e4f);
+        return p + z * p * (1.0f - p) * (2.0f * kGeluC) * (1.0f + 3.0f * kGeluA * z2);
+    } else if constexpr (ACT == DENSE_ACT_SILU) {
+        const float p = sigmoid(z);
+        return p * (1.0f + z * (1.0f - p));
+    } else {
+        return 1.0f;
+    }
+}
+
+template <int U>
+__device__ __forceinline__ void activate8(int act, float (&v)[U][8])
+{
+    auto all = [&](auto f) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[u][i] = f(v[u][i]);
+    };
+    if (act == DENSE_ACT_RELU)
+        all([](float z) { return activate<DENSE_ACT_RELU>(z); });
+    else if (act == DENSE_ACT_GELU)
+        all([](float z) { return activate<DENSE_ACT_GELU>(z); });
+    else if (act == DENSE_ACT_GELU_TANH)
+        all([](float z) { return activate<DENSE_ACT_GELU_TANH>(z); });
+    else if (act == DENSE_ACT_SILU)
+        all([](float z) { return activate<DENSE_ACT_SILU>(z); });
+}
+
+__device__ __forceinline__ float activate_rt(int act, float z)
+{
+    return act == DENSE_ACT_RELU        ? activate<DENSE_ACT_RELU>(z)
+         : act == DENSE_ACT_GELU        ? activate<DENSE_ACT_GELU>(z)
+         : act == DENSE_ACT_GELU_TANH   ? activate<DENSE_ACT_GELU_TANH>(z)
+         : act == DENSE_ACT_SILU        ? activate<DENSE_ACT_SILU>(z)
+                                        : z;
+}
+
+// s_waitcnt immediate (gfx9 encoding): at most VM vector-memory operations
+// outstanding, all LDS operations done.
+template <int VM>
+__device__ __forceinline__ void wait_vm_lgkm0()
+{
+    static_assert(VM >= 0 && VM < 64, "vmcnt out of range");
+    __builtin_amdgcn_s_waitcnt((VM & 15) | ((VM >> 4) << 14) | (7 << 4) | (0 << 8));
+}
+
+// Buffer resource (gfx9 layout): base address, stride 0, byte range, 32-bit
+// data format.  Built from uniform values.
+__device__ __forceinline__ v4i make_rsrc(const void *p, int range)
+{
+    const unsigned long long a = (unsigned long long)p;
+    v4i d;
+    d.x = (int)(unsigned)a;
+    d.y = (int)((a >> 32) & 0xFFFFu);
+    d.z = range;
+    d.w = 0x00020000;
+    return d;
+}
+
+// 16 bytes per lane from buffer offset `voff` straight into LDS: lane i's
+// bytes land at lds + 16*i.  An offset outside the range writes zeros.  The
+// compiler does not see these loads, so the kernel counts them itself with
+// s_waitcnt vmcnt.
+__device__ __forceinline__ void load16_to_lds(v4i rsrc, unsigned lds_addr, int voff)
+{
+    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :: "s"(lds_addr), "v"(voff), "s"(rsrc) : "memory", "m0");
+}
+
+__device__ __forceinline__ unsigned lds_address(const void *p)
+{
+    return (unsigned)(unsigned long long)(lds_void *)p;
+}
+
+template <int WIDTH>
+__device__ __forceinline__ float wave_sum(float v)
+{
+#pragma unroll
+    for (int o = WIDTH / 2; o >= 1; o >>= 1)
+        v += __shfl_xor(v, o, 64);
+    return v;
+}
+
+template <int WIDTH>
+__device__ __forceinline__ float wave_max(float v)
+{
+#pragma unroll
+    for (int o = WIDTH / 2; o >= 1; o >>= 1)
+        v = fmaxf(v, __shfl_xor(v, o, 64));
+    return v;
+}
+
+// Workgroups are dealt round-robin to the 8 XCDs; each XCD gets one contiguous
+// run of tiles.
+__device__ __forceinline__ int xcd_tile(int bid, int tiles)
+{
+    const int per = tiles >> 3, rem = tiles & 7;
+    const int xcd = bid & 7, idx = bid >> 3;
+    return xcd * per + min(xcd, rem) + idx;
+}
+
+// Epilogue of one product (linear's, or a plain store for the gradients).
+struct Epilogue {
+    void *out;
+    const void *residual;
+    void *preact;
+    const void *bias;
+    const float *x_scale, *w_scale;
+    int64_t ldo, ldr, ldp;  // row strides in elements
+    int out_dt;             // of out, residual and preact
+    int bias_dt;
+    int act;
+};
+
+// The epilogue of U chunks of eight columns n .. n+cnt-1, chunk u in row
+// m + u*step: v holds the products' sums, ws and bs the columns' scales and
+// biases.  Rows from M on are skipped.  All residuals are loaded first, so that
+// their latencies overlap.
+template <bool SCALED, int U>
+__device__ __forceinline__ void finish8(const Epilogue &e, int64_t m, int step, int64_t M, int64_t n, int cnt,
+                                        float (&v)[U][8], const float (&bs)[8], const float (&ws)[8])
+{
+    float r[U][8];
+    if (e.residual) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (m + u * step < M)
+                load8n_dt(e.residual, e.out_dt, (m + u * step) * e.ldr + n, cnt, r[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        if constexpr (SCALED) {
+            const float xs = e.x_scale && m + u * step < M ? e.x_scale[m + u * step] : 1.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[u][i] = __builtin_fmaf(v[u][i], xs * ws[i], bs[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[u][i] += bs[i];
+        }
+    }
+    if (e.preact) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (m + u * step < M)
+                store8n_dt(e.preact, e.out_dt, (m + u * step) * e.ldp + n, cnt, v[u]);
+    }
+    activate8(e.act, v);
+    if (e.residual) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[u][i] += r[u][i];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (m + u * step < M)
+            store8n_dt(e.out, e.out_dt, (m + u * step) * e.ldo + n, cnt, v[u]);
+}
+
+// Scales and biases of columns n .. n+cnt-1 (ones and zeros where absent).
+__device__ __forceinline__ void column_params(const Epilogue &e, int64_t n, int cnt, float (&bs)[8], float (&ws)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        bs[i] = 0.0f;
+        ws[i] = 1.0f;
+    }
+    if (e.bias)
+        load8n_dt(e.bias, e.bias_dt, n, cnt, bs);
+    if (e.w_scale)
+        load8n(e.w_scale + n, cnt, ws);
+}
+
+}  // namespace dense

@@ -1,0 +1,279 @@
+// Layer norm's C entries: argument checks, the choice of kernel, the launches.
+#include <string.h>
+
+#include "host_common.hpp"
+#include "norm_kernel.hpp"
+#include "rows_kernel.hpp"
+
+namespace dense {
+namespace {
+
+constexpr int64_t kWsAlign = 256;
+// Longest row that stays in registers, forward and backward.
+constexpr int64_t kNormRow = 65536;
+constexpr int64_t kBackRow = 16384;
+
+conv_i8_status_t check_stat(dense_vec_t *v, int64_t n)
+{
+    DENSE_TRY(check_vec(v, n));
+    return v->dtype == DENSE_NONE || v->dtype == DENSE_FP32 ? CONV_I8_OK : CONV_I8_ERR_DTYPE;
+}
+
+conv_i8_status_t analyze(const dense_layer_norm_t *args, dense_layer_norm_t *d)
+{
+    if (!args)
+        return CONV_I8_ERR_NULL;
+    *d = *args;
+    DENSE_TRY(check_mat(&d->x, false));
+    DENSE_TRY(check_mat(&d->y, true));
+    const int64_t dt = d->x.dtype, M = d->x.rows, D = d->x.cols;
+    if (!is_float(dt) || (d->y.dtype != dt && d->y.dtype != DENSE_INT8))
+        return CONV_I8_ERR_DTYPE;
+    if (D < 1)
+        return CONV_I8_ERR_DIMS;
+    if (d->y.rows != M || d->y.cols != D)
+        return CONV_I8_ERR_OUT_DIMS;
+    if (d->x.col_stride != 1)
+        return CONV_I8_ERR_STRIDES;
+    DENSE_TRY(check_vec(&d->weight, D));
+    DENSE_TRY(check_vec(&d->bias, D));
+    for (const dense_vec_t *v : {&d->weight, &d->bias})
+        if (v->dtype != DENSE_NONE && v->dtype != dt)
+            return CONV_I8_ERR_DTYPE;
+    DENSE_TRY(check_stat(&d->mean, M));
+    DENSE_TRY(check_stat(&d->rstd, M));
+    DENSE_TRY(check_stat(&d->scale, M));
+    if ((d->scale.dtype != DENSE_NONE) != (d->y.dtype == DENSE_INT8))
+        return CONV_I8_ERR_PARAM;
+    if (!(d->eps >= 0.0))
+        return CONV_I8_ERR_PARAM;
+    return CONV_I8_OK;
+}
+
+template <typename T, int P, int V, bool Q8>
+void launch_one(const NormArgs &a, hipStream_t s)
+{
+    constexpr int rows = norm_threads(P) / P;
+    hipLaunchKernelGGL((norm_kernel<T, P, V, Q8>), dim3((unsigned)ceil_div(a.M, rows)), dim3(norm_threads(P)), 0, s, a);
+}
+
+template <typename T, bool Q8>
+void launch_norm(const NormArgs &a, hipStream_t s)
+{
+    const int D = a.D;
+    // a wave per row while that gives each CU a few waves, else a workgroup per row
+    const bool few = a.M < 4 * kCUs;
+    if (D <= 512)
+        launch_one<T, 64, 1, Q8>(a, s);
+    else if (D <= 1024 && !few)
+        launch_one<T, 64, 2, Q8>(a, s);
+    else if (D <= 2048)
+        few ? launch_one<T, 256, 1, Q8>(a, s) : launch_one<T, 64, 4, Q8>(a, s);
+    else if (D <= 4096)
+        launch_one<T, 256, 2, Q8>(a, s);
+    else if (D <= 8192)
+        launch_one<T, 256, 4, Q8>(a, s);
+    else if (D <= 16384)
+        launch_one<T, 1024, 2, Q8>(a, s);
+    else if (D <= kNormRow)
+        launch_one<T, 1024, 8, Q8>(a, s);
+    else
+        hipLaunchKernelGGL((norm_long_kernel<T, Q8>), dim3((unsigned)a.M), dim3(1024), 0, s, a);
+}
+
+struct BackPlan {
+    dense_layer_norm_backward_t d;
+    int64_t M, D;
+    bool sums;
+    int wgs = 0;         // workgroups that walk the rows, or row blocks of a long row's sums
+    int64_t part_ld = 0, ws_bytes = 0;
+};
+
+constexpr int back_threads(int64_t D) { return D <= 512 ? 64 : D <= 8192 ? 256 : 1024; }
+
+conv_i8_status_t analyze(const dense_layer_norm_backward_t *args, BackPlan *p)
+{
+    if (!args)
+        return CONV_I8_ERR_NULL;
+    p->d = *args;
+    dense_layer_norm_backward_t &d = p->d;
+    DENSE_TRY(check_mat(&d.dy, false));
+    DENSE_TRY(check_mat(&d.x, false));
+    DENSE_TRY(check_mat(&d.dx, true));
+    const int64_t dt = d.x.dtype;
+    p->M = d.x.rows;
+    p->D = d.x.cols;
+    if (!is_float(dt) || d.dy.dtype != dt || d.dx.dtype != dt)
+        return CONV_I8_ERR_DTYPE;
+    if (p->D < 1 || d.dy.rows != p->M || d.dy.cols != p->D)
+        return CONV_I8_ERR_DIMS;
+    if (d.dx.rows != p->M || d.dx.cols != p->D)
+        return CONV_I8_ERR_OUT_DIMS;
+    if (d.x.col_stride != 1 || d.dy.col_stride != 1)
+        return CONV_I8_ERR_STRIDES;
+    DENSE_TRY(check_vec(&d.weight, p->D));
+    DENSE_TRY(check_vec(&d.dweight, p->D));
+    DENSE_TRY(check_vec(&d.dbias, p->D));
+    for (const dense_vec_t *v : {&d.weight, &d.dweight, &d.dbias})
+        if (v->dtype != DENSE_NONE && v->dtype != dt)
+            return CONV_I8_ERR_DTYPE;
+    if (d.mean.dtype == DENSE_NONE || d.rstd.dtype == DENSE_NONE)
+        return CONV_I8_ERR_NULL;
+    DENSE_TRY(check_stat(&d.mean, p->M));
+    DENSE_TRY(check_stat(&d.rstd, p->M));
+    if ((d.dweight.dtype == DENSE_NONE) != (d.dbias.dtype == DENSE_NONE))
+        return CONV_I8_ERR_PARAM;
+    p->sums = d.dweight.dtype != DENSE_NONE;
+    p->part_ld = round_up(p->D, 8);
+    if (p->D > kBackRow) {
+        const int64_t blocks = p->M < 64 ? p->M : 64;
+        p->wgs = (int)(p->M > 0 ? ceil_div(p->M, ceil_div(p->M, blocks)) : 0);
+    } else {
+        // two workgroups a CU, and at least four rows for each group of threads
+        const int rows = norm_threads(back_threads(p->D)) / back_threads(p->D);
+        const int64_t want = ceil_div(p->M, 4 * rows);
+        p->wgs = (int)(want < 2 * kCUs ? want : 2 * kCUs);
+    }
+    p->ws_bytes = p->sums ? round_up((int64_t)p->wgs * 2 * p->part_ld * 4, kWsAlign) : 0;
+    return CONV_I8_OK;
+}
+
+template <typename T, int P, int V>
+void launch_back_one(const NormBackArgs &a, int wgs, hipStream_t s)
+{
+    if (a.part)
+        hipLaunchKernelGGL((norm_backward_kernel<T, P, V, true>), dim3((unsigned)wgs), dim3(norm_threads(P)), 0, s, a);
+    else
+        hipLaunchKernelGGL((norm_backward_kernel<T, P, V, false>), dim3((unsigned)wgs), dim3(norm_threads(P)), 0, s, a);
+}
+
+template <typename T>
+void launch_back(const NormBackArgs &a, int wgs, hipStream_t s)
+{
+    const int D = a.D;
+    if (D <= 512)
+        launch_back_one<T, 64, 1>(a, wgs, s);
+    else if (D <= 2048)
+        launch_back_one<T, 256, 1>(a, wgs, s);
+    else if (D <= 4096)
+        launch_back_one<T, 256, 2>(a, wgs, s);
+    else if (D <= 8192)
+        launch_back_one<T, 256, 4>(a, wgs, s);
+    else if (D <= kBackRow)
+        launch_back_one<T, 1024, 2>(a, wgs, s);
+    else {
+        hipLaunchKernelGGL(norm_backward_long_kernel<T>, dim3((unsigned)a.M), dim3(1024), 0, s, a);
+        if (a.part)
+            hipLaunchKernelGGL(norm_backward_sums_kernel<T>, dim3((unsigned)ceil_div(D, 2048), (unsigned)wgs), dim3(256),
+                               0, s, a, (int)ceil_div(a.M, wgs));
+    }
+}
+
+}  // namespace
+}  // namespace dense
+
+using namespace dense;
+
+extern "C" {
+
+conv_i8_status_t dense_layer_norm(const dense_layer_norm_t *args, void *stream)
+{
+    dense_layer_norm_t d;
+    DENSE_TRY(analyze(args, &d));
+    if (d.x.rows == 0)
+        return CONV_I8_OK;
+    NormArgs a;
+    memset(&a, 0, sizeof a);
+    a.x = d.x.ptr;
+    a.weight = d.weight.ptr;
+    a.bias = d.bias.ptr;
+    a.y = const_cast<void *>(d.y.ptr);
+    a.ldx = d.x.row_stride;
+    a.ldy = d.y.row_stride;
+    a.M = (int)d.x.rows;
+    a.D = (int)d.x.cols;
+    a.eps = (float)d.eps;
+    a.d = (float)a.D;
+    a.mean = (float *)const_cast<void *>(d.mean.ptr);
+    a.rstd = (float *)const_cast<void *>(d.rstd.ptr);
+    a.scale = (float *)const_cast<void *>(d.scale.ptr);
+    const bool q8 = d.y.dtype == DENSE_INT8;
+    hipStream_t s = (hipStream_t)stream;
+    if (d.x.dtype == DENSE_BF16)
+        q8 ? launch_norm<bf16, true>(a, s) : launch_norm<bf16, false>(a, s);
+    else if (d.x.dtype == DENSE_FP16)
+        q8 ? launch_norm<f16, true>(a, s) : launch_norm<f16, false>(a, s);
+    else
+        q8 ? launch_norm<float, true>(a, s) : launch_norm<float, false>(a, s);
+    return hipGetLastError() == hipSuccess ? CONV_I8_OK : CONV_I8_ERR_HIP;
+}
+
+conv_i8_status_t dense_layer_norm_backward_workspace_size(const dense_layer_norm_backward_t *args, size_t *bytes)
+{
+    if (!bytes)
+        return CONV_I8_ERR_NULL;
+    BackPlan p;
+    DENSE_TRY(analyze(args, &p));
+    *bytes = (size_t)p.ws_bytes;
+    return CONV_I8_OK;
+}
+
+conv_i8_status_t dense_layer_norm_backward(const dense_layer_norm_backward_t *args, void *workspace, size_t bytes,
+                                           void *stream)
+{
+    BackPlan p;
+    DENSE_TRY(analyze(args, &p));
+    if (p.ws_bytes > 0) {
+        if (bytes < (size_t)p.ws_bytes || ((uintptr_t)workspace & (kWsAlign - 1)) != 0)
+            return CONV_I8_ERR_WORKSPACE;
+        if (!workspace)
+            return CONV_I8_ERR_NULL;
+    }
+    NormBackArgs a;
+    memset(&a, 0, sizeof a);
+    a.dy = p.d.dy.ptr;
+    a.x = p.d.x.ptr;
+    a.weight = p.d.weight.ptr;
+    a.mean = (const float *)p.d.mean.ptr;
+    a.rstd = (const float *)p.d.rstd.ptr;
+    a.dx = const_cast<void *>(p.d.dx.ptr);
+    a.lddy = p.d.dy.row_stride;
+    a.ldx = p.d.x.row_stride;
+    a.lddx = p.d.dx.row_stride;
+    a.M = (int)p.M;
+    a.D = (int)p.D;
+    a.d = (float)a.D;
+    a.part = p.sums ? (float *)workspace : nullptr;
+    a.part_ld = p.part_ld;
+    hipStream_t s = (hipStream_t)stream;
+    const int64_t dt = p.d.x.dtype;
+    if (p.M > 0) {
+        if (dt == DENSE_BF16)
+            launch_back<bf16>(a, p.wgs, s);
+        else if (dt == DENSE_FP16)
+            launch_back<f16>(a, p.wgs, s);
+        else
+            launch_back<float>(a, p.wgs, s);
+        if (hipGetLastError() != hipSuccess)
+            return CONV_I8_ERR_HIP;
+    }
+    if (p.sums) {
+        ColSumArgs c;
+        memset(&c, 0, sizeof c);
+        c.part = a.part;
+        c.ld = 2 * p.part_ld;
+        c.rows = p.M > 0 ? p.wgs : 0;  // none: zeros
+        c.cols = (int)(2 * p.part_ld);
+        c.split = (int)p.part_ld;
+        c.valid = (int)p.D;
+        c.out0 = const_cast<void *>(p.d.dweight.ptr);
+        c.out1 = const_cast<void *>(p.d.dbias.ptr);
+        c.dt = (int)dt;
+        hipLaunchKernelGGL(colsum_kernel<>, dim3((unsigned)ceil_div(c.cols, 32)), dim3(256), 0, s, c);
+        if (hipGetLastError() != hipSuccess)
+            return CONV_I8_ERR_HIP;
+    }
+    return CONV_I8_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,156 @@
+// Memory-bound passes around the products: copies of operands into the form
+// the product kernel reads in place, the gradient of the activation with the
+// column sums of the bias gradient, and the reduction of those sums.
+#pragma once
+
+#include "dense_common.hpp"
+
+namespace dense {
+
+// One operand copied to rows of 16-byte chunks: dst row r holds `cols`
+// elements of src row r and zeros up to the chunk's end.
+struct PackJob {
+    const void *src;
+    void *dst;
+    int64_t rows, cols;      // elements
+    int64_t rs, cs;          // source strides in elements
+    int64_t chunks;          // 16-byte chunks per destination row
+    int64_t items;           // rows * chunks, 0 for an unused job
+};
+
+struct PackArgs {
+    PackJob job[2];
+    int first;               // workgroups of job 0
+};
+
+// One thread copies one chunk; both operands of a product go in one launch.
+// U is an unsigned integer of the element's size.
+template <typename U>
+__global__ __launch_bounds__(256) void pack_kernel(const PackArgs a)
+{
+    constexpr int E = 16 / sizeof(U);
+    struct __attribute__((packed, aligned(sizeof(U)))) Piece { U e[E]; };
+    const bool second = (int)blockIdx.x >= a.first;
+    const PackJob &j = a.job[second];
+    const int64_t i = (int64_t)(second ? blockIdx.x - a.first : blockIdx.x) * 256 + threadIdx.x;
+    if (i >= j.items)
+        return;
+    const int64_t r = i / j.chunks, c = (i - r * j.chunks) * E;
+    const U *s = (const U *)j.src + r * j.rs + c * j.cs;
+    Piece p;
+    if (j.cs == 1 && c + E <= j.cols) {
+        p = *(const Piece *)s;
+    } else {
+#pragma unroll
+        for (int k = 0; k < E; ++k)
+            p.e[k] = c + k < j.cols ? s[k * j.cs] : U(0);
+    }
+    *(v4i *)((U *)j.dst + i * E) = __builtin_bit_cast(v4i, p);
+}
+
+// g = dy act'(z), written with a row pitch of whole 16-byte chunks (zeros past
+// N), and column sums of the unrounded g over a block of rows.
+struct ActGradArgs {
+    const void *dy, *z;       // z null: g = dy
+    int64_t ldy, ldz;
+    int M, N;
+    int rows;                 // rows per workgroup
+    void *g;                  // null: only the column sums
+    int64_t ldg;
+    float *colsum;            // [row block][sum_ld], or null
+    int64_t sum_ld;
+};
+
+// A wave takes 512 columns (eight per lane) of every fourth row of its block,
+// so that each load is one contiguous 1 KiB; the four waves' column sums are
+// added through LDS in order.
+template <typename T, int ACT>
+__global__ __launch_bounds__(256) void act_grad_kernel(const ActGradArgs a)
+{
+    __shared__ float red[4][512];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int n = blockIdx.x * 512 + lane * 8;
+    const int cnt = a.N - n;
+    const int m0 = blockIdx.y * a.rows, m1 = min(a.M, m0 + a.rows);
+    float sum[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        sum[i] = 0.0f;
+    if (cnt > 0) {
+#pragma unroll 4
+        for (int m = m0 + wave; m < m1; m += 4) {
+            float v[8];
+            load8n((const T *)a.dy + m * a.ldy + n, cnt, v);
+            if constexpr (ACT != DENSE_ACT_NONE) {
+                float z[8];
+                load8n((const T *)a.z + m * a.ldz + n, cnt, z);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    v[i] *= act_slope<ACT>(z[i]);
+            }
+            if (a.g)
+                store8((T *)a.g + m * a.ldg + n, v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                sum[i] += v[i];
+        }
+    }
+    if (!a.colsum)
+        return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        red[wave][lane * 8 + i] = sum[i];
+    __syncthreads();
+    for (int c = threadIdx.x; c < 512; c += 256)
+        if (blockIdx.x * 512 + c < a.N)
+            a.colsum[blockIdx.y * a.sum_ld + blockIdx.x * 512 + c] =
+                (red[0][c] + red[1][c]) + (red[2][c] + red[3][c]);
+}
+
+// out[c] = sum over r of part[r][c], rows in a fixed order: eight groups of
+// threads take every eighth row of 32 columns and are added through LDS.
+// Columns [0, split) go to out0 and [split, cols) to out1, the first `valid`
+// of each.
+struct ColSumArgs {
+    const float *part;
+    int64_t ld;
+    int rows, cols;
+    int split, valid;
+    void *out0, *out1;
+    int dt;
+};
+
+template <int COLS = 32>
+__global__ __launch_bounds__(256) void colsum_kernel(const ColSumArgs a)
+{
+    constexpr int G = 256 / COLS;
+    __shared__ float red[G][COLS + 1];
+    const int c = threadIdx.x % COLS, grp = threadIdx.x / COLS;
+    const int col = blockIdx.x * COLS + c;
+    const bool second = col >= a.split;
+    const int oc = second ? col - a.split : col;
+    const bool live = col < a.cols && oc < a.valid;
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (live) {
+        const float *p = a.part + col;
+        int r = grp;
+        for (; r + 3 * G < a.rows; r += 4 * G) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                s[k] += p[(r + G * k) * a.ld];
+        }
+        for (; r < a.rows; r += G)
+            s[0] += p[r * a.ld];
+    }
+    red[grp][c] = (s[0] + s[1]) + (s[2] + s[3]);
+    __syncthreads();
+    if (grp == 0 && live) {
+        float v = 0.0f;
+#pragma unroll
+        for (int k = 0; k < G; ++k)
+            v += red[k][c];
+        store_dt(second ? a.out1 : a.out0, a.dt, oc, v);
+    }
+}
+
+}  // namespace dense

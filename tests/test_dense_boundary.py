@@ -1,0 +1,268 @@
+"""The dense layer's and layer norm's entries on the CPU: every declared symbol
+is exported, bad arguments are refused on the host before any device is
+touched, and plans and workspaces are what the sizes ask for."""
+import ctypes
+import os
+import re
+
+import pytest
+import torch
+
+import int8_convolution_forward_amd as ci8
+from int8_convolution_forward_amd import dense
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+I8, BF16, FP16, FP32 = 1, 3, 4, 5
+FAKE = 0x1000000  # aligned, never dereferenced: every call below ends before device work
+
+
+def mat(r, c, dt, rs=None, cs=1, ptr=FAKE):
+    return (ptr, r, c, c if rs is None else rs, cs, dt)
+
+
+def vec(n, dt, ptr=FAKE):
+    return (ptr, n, dt)
+
+
+NM, NV = dense._NO_MAT, dense._NO_VEC
+
+
+def linear(x=mat(64, 32, BF16), w=mat(48, 32, BF16), y=mat(64, 48, BF16), residual=NM, preact=NM, bias=NV, xs=NV, ws=NV,
+           act=0):
+    return dense._pack_linear(*x, *w, *y, *residual, *preact, *bias, *xs, *ws, act)
+
+
+def backward(dy=mat(64, 48, BF16), x=mat(64, 32, BF16), w=mat(48, 32, BF16), z=NM, dx=mat(64, 32, BF16),
+             dw=mat(48, 32, BF16), db=vec(48, BF16), act=0):
+    return dense._pack_linear_backward(*dy, *x, *w, *z, *dx, *dw, *db, act)
+
+
+def norm(x=mat(8, 32, BF16), y=mat(8, 32, BF16), weight=NV, bias=NV, mean=NV, rstd=NV, scale=NV, eps=1e-5):
+    return dense._pack_norm(*x, *y, *weight, *bias, *mean, *rstd, *scale, eps)
+
+
+def norm_backward(dy=mat(8, 32, BF16), x=mat(8, 32, BF16), dx=mat(8, 32, BF16), weight=NV, mean=vec(8, FP32),
+                  rstd=vec(8, FP32), dw=vec(32, BF16), db=vec(32, BF16)):
+    return dense._pack_norm_backward(*dy, *x, *dx, *weight, *mean, *rstd, *dw, *db)
+
+
+def size(entry, args):
+    n = ctypes.c_size_t()
+    code = getattr(dense.lib, entry + "_workspace_size")(args, n)
+    return ci8.STATUS[code], n.value
+
+
+def test_every_declared_symbol_is_exported():
+    text = re.sub(r"/\*.*?\*/", "", open(os.path.join(ROOT, "include", "dense.h")).read(), flags=re.S)
+    names = set(re.findall(r"^\s*conv_i8_status_t\s+(dense_\w+)\s*\(", text, flags=re.M))
+    assert names == set(dense._ENTRIES)
+    for n in names:
+        assert hasattr(dense.lib, n), n
+
+
+def test_structures_match_the_header():
+    """The packed sizes are those of the C structures (8-byte members only)."""
+    assert len(linear()) == 8 * (5 * 6 + 3 * 3 + 1)
+    assert len(backward()) == 8 * (6 * 6 + 3 + 1)
+    assert len(norm()) == 8 * (2 * 6 + 5 * 3 + 1)
+    assert len(norm_backward()) == 8 * (3 * 6 + 5 * 3)
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(x=mat(64, 32, FP32), w=mat(48, 32, FP32), y=mat(64, 48, FP32)), "DTYPE"),
+    (dict(x=mat(64, 32, 99)), "DTYPE"),
+    (dict(w=mat(48, 32, FP16)), "DTYPE"),
+    (dict(y=mat(64, 48, FP16)), "DTYPE"),
+    (dict(y=mat(64, 48, I8)), "DTYPE"),
+    (dict(x=mat(64, 33, BF16)), "CHANNELS"),
+    (dict(y=mat(63, 48, BF16)), "OUT_DIMS"),
+    (dict(y=mat(64, 47, BF16)), "OUT_DIMS"),
+    (dict(x=mat(-1, 32, BF16)), "DIMS"),
+    (dict(x=mat(64, 32, BF16, rs=-32)), "STRIDES"),
+    (dict(x=mat(64, 32, BF16, cs=-1)), "STRIDES"),
+    (dict(y=mat(64, 48, BF16, rs=47)), "STRIDES"),
+    (dict(y=mat(64, 48, BF16, rs=1, cs=64)), "STRIDES"),
+    (dict(y=mat(64, 48, BF16, rs=0)), "STRIDES"),
+    (dict(residual=mat(64, 48, FP32)), "DTYPE"),
+    (dict(residual=mat(64, 40, BF16)), "OUT_DIMS"),
+    (dict(residual=mat(64, 48, BF16, rs=1, cs=64)), "STRIDES"),
+    (dict(preact=mat(64, 48, BF16, rs=40)), "STRIDES"),
+    (dict(bias=vec(47, BF16)), "DIMS"),
+    (dict(bias=vec(48, I8)), "DTYPE"),
+    (dict(bias=vec(48, BF16, ptr=0)), "NULL"),
+    (dict(xs=vec(64, FP32)), "DTYPE"),
+    (dict(act=5), "PARAM"),
+    (dict(act=-1), "PARAM"),
+    (dict(x=mat(64, 32, BF16, ptr=0)), "NULL"),
+    (dict(y=mat(64, 48, BF16, ptr=0)), "NULL"),
+    (dict(x=mat(64, 32, BF16, ptr=FAKE + 1)), "PARAM"),
+    (dict(x=mat(64, 131072, I8), w=mat(48, 131072, I8)), "RANGE"),
+    (dict(x=mat(64, 32, I8), w=mat(48, 32, I8), xs=vec(64, BF16)), "DTYPE"),
+    (dict(x=mat(64, 32, I8), w=mat(48, 32, I8), xs=vec(63, FP32)), "DIMS"),
+    (dict(x=mat(64, 1 << 24, BF16), w=mat(48, 1 << 24, BF16)), "UNSUPPORTED"),
+    (dict(x=mat(1 << 31, 32, BF16), y=mat(1 << 31, 48, BF16)), "UNSUPPORTED"),
+])
+def test_linear_refusals(over, status):
+    args = linear(**over)
+    want = "CONV_I8_ERR_" + status
+    assert size("dense_linear", args)[0] == want
+    assert ci8.STATUS[dense.lib.dense_linear(args, None, 0, None)] == want
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(dy=mat(64, 48, I8)), "DTYPE"),
+    (dict(x=mat(64, 32, FP16)), "DTYPE"),
+    (dict(x=mat(63, 32, BF16)), "DIMS"),
+    (dict(w=mat(48, 31, BF16)), "CHANNELS"),
+    (dict(w=mat(47, 32, BF16)), "DIMS"),
+    (dict(dy=mat(64, 48, BF16, rs=1, cs=64)), "STRIDES"),
+    (dict(act=1), "NULL"),
+    (dict(act=1, z=mat(64, 47, BF16)), "DIMS"),
+    (dict(act=1, z=mat(64, 48, FP16)), "DTYPE"),
+    (dict(act=9), "PARAM"),
+    (dict(dx=mat(64, 31, BF16)), "OUT_DIMS"),
+    (dict(dx=mat(64, 32, FP32)), "DTYPE"),
+    (dict(dw=mat(48, 32, BF16, rs=8)), "STRIDES"),
+    (dict(dw=mat(47, 32, BF16)), "OUT_DIMS"),
+    (dict(db=vec(47, BF16)), "DIMS"),
+    (dict(db=vec(48, FP32)), "DTYPE"),
+])
+def test_linear_backward_refusals(over, status):
+    args = backward(**over)
+    want = "CONV_I8_ERR_" + status
+    assert size("dense_linear_backward", args)[0] == want
+    assert ci8.STATUS[dense.lib.dense_linear_backward(args, None, 0, None)] == want
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(x=mat(8, 32, I8), y=mat(8, 32, I8)), "DTYPE"),
+    (dict(y=mat(8, 32, FP32)), "DTYPE"),
+    (dict(x=mat(8, 0, BF16), y=mat(8, 0, BF16)), "DIMS"),
+    (dict(y=mat(8, 31, BF16)), "OUT_DIMS"),
+    (dict(x=mat(8, 32, BF16, rs=1, cs=8)), "STRIDES"),
+    (dict(y=mat(8, 32, BF16, rs=31)), "STRIDES"),
+    (dict(weight=vec(31, BF16)), "DIMS"),
+    (dict(weight=vec(32, FP32)), "DTYPE"),
+    (dict(mean=vec(8, BF16)), "DTYPE"),
+    (dict(rstd=vec(7, FP32)), "DIMS"),
+    (dict(y=mat(8, 32, I8)), "PARAM"),
+    (dict(scale=vec(8, FP32)), "PARAM"),
+    (dict(eps=-1.0), "PARAM"),
+    (dict(eps=float("nan")), "PARAM"),
+])
+def test_norm_refusals(over, status):
+    assert ci8.STATUS[dense.lib.dense_layer_norm(norm(**over), None)] == "CONV_I8_ERR_" + status
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(dy=mat(8, 32, FP32)), "DTYPE"),
+    (dict(dy=mat(7, 32, BF16)), "DIMS"),
+    (dict(dx=mat(8, 31, BF16)), "OUT_DIMS"),
+    (dict(x=mat(8, 32, BF16, rs=1, cs=8)), "STRIDES"),
+    (dict(mean=NV), "NULL"),
+    (dict(rstd=vec(8, BF16)), "DTYPE"),
+    (dict(weight=vec(32, FP16)), "DTYPE"),
+    (dict(dw=NV), "PARAM"),
+    (dict(db=vec(31, BF16)), "DIMS"),
+])
+def test_norm_backward_refusals(over, status):
+    args = norm_backward(**over)
+    want = "CONV_I8_ERR_" + status
+    assert size("dense_layer_norm_backward", args)[0] == want
+    assert ci8.STATUS[dense.lib.dense_layer_norm_backward(args, None, 0, None)] == want
+
+
+def test_null_arguments():
+    n = ctypes.c_size_t()
+    for name in ("dense_linear", "dense_linear_backward", "dense_layer_norm_backward"):
+        assert ci8.STATUS[getattr(dense.lib, name)(None, None, 0, None)] == "CONV_I8_ERR_NULL"
+        assert ci8.STATUS[getattr(dense.lib, name + "_workspace_size")(None, n)] == "CONV_I8_ERR_NULL"
+    assert ci8.STATUS[dense.lib.dense_layer_norm(None, None)] == "CONV_I8_ERR_NULL"
+
+
+def test_workspace_is_checked():
+    """Odd rows need copies; a workspace that is short or misaligned is refused."""
+    args = linear(x=mat(64, 33, BF16), w=mat(48, 33, BF16))
+    status, need = size("dense_linear", args)
+    assert status == "CONV_I8_OK" and need >= (64 + 48) * 33 * 2
+    for ws, n in ((FAKE, need - 1), (FAKE + 64, need), (None, need)):
+        assert dense.lib.dense_linear(args, ws, n, None) != 0
+    args = norm_backward()
+    status, need = size("dense_layer_norm_backward", args)
+    assert status == "CONV_I8_OK" and need >= 2 * 32 * 4
+    assert ci8.STATUS[dense.lib.dense_layer_norm_backward(args, FAKE, need - 1, None)] == "CONV_I8_ERR_WORKSPACE"
+    assert size("dense_layer_norm_backward", norm_backward(dw=NV, db=NV)) == ("CONV_I8_OK", 0)
+
+
+def test_empty_problems_are_ok_without_device_work():
+    assert dense.lib.dense_linear(linear(x=mat(0, 32, BF16, ptr=0), y=mat(0, 48, BF16, ptr=0)), None, 0, None) == 0
+    assert dense.lib.dense_layer_norm(norm(x=mat(0, 32, BF16, ptr=0), y=mat(0, 32, BF16, ptr=0)), None) == 0
+    args = norm_backward(dy=mat(0, 32, BF16, ptr=0), x=mat(0, 32, BF16, ptr=0), dx=mat(0, 32, BF16, ptr=0),
+                         mean=vec(0, FP32), rstd=vec(0, FP32), dw=NV, db=NV)
+    assert dense.lib.dense_layer_norm_backward(args, None, 0, None) == 0
+
+
+def plan(args):
+    buf = ctypes.create_string_buffer(512)
+    assert dense.lib.dense_linear_plan(args, buf, 512) == 0
+    return buf.value.decode()
+
+
+def test_plans():
+    assert plan(linear(x=mat(1, 64, BF16), y=mat(1, 48, BF16), w=mat(48, 64, BF16))).startswith("kernel=skinny")
+    assert "aligned=0" in plan(linear(x=mat(1, 33, BF16), y=mat(1, 48, BF16), w=mat(48, 33, BF16)))
+    p = plan(linear(x=mat(512, 64, BF16), y=mat(512, 256, BF16), w=mat(256, 64, BF16)))
+    assert "a=rows b=rows" in p
+    p = plan(linear(x=mat(512, 64, BF16), y=mat(512, 256, BF16), w=mat(256, 64, BF16, rs=1, cs=256)))
+    assert "a=rows b=cols" in p and "packed" not in p
+    p = plan(linear(x=mat(512, 64, I8), y=mat(512, 256, BF16), w=mat(256, 64, I8, rs=1, cs=256)))
+    assert "b=rows_packed" in p
+    p = plan(linear(x=mat(512, 65, BF16), y=mat(512, 256, BF16), w=mat(256, 65, BF16)))
+    assert "a=rows_packed b=rows_packed" in p
+    buf = ctypes.create_string_buffer(4)
+    assert ci8.STATUS[dense.lib.dense_linear_plan(linear(), buf, 4)] == "CONV_I8_ERR_PARAM"
+
+
+def test_forced_tiles_and_splits(monkeypatch):
+    args = linear(x=mat(512, 1024, BF16), y=mat(512, 256, BF16), w=mat(256, 1024, BF16))
+    for name, tiles in (("256x256", 2), ("256x128", 4), ("128x128", 8), ("64x64", 32)):
+        monkeypatch.setenv("CONV_I8_DENSE_TILE", name)
+        assert f"tile={name} tiles={tiles} " in plan(args)
+        monkeypatch.setenv("CONV_I8_DENSE_TILE", name + "/4")
+        assert f"tile={name} tiles={tiles} split=4" in plan(args)
+    status, need = size("dense_linear", args)
+    assert need == 4 * 512 * 256 * 4
+
+
+def test_a_split_covers_every_stage():
+    """Stages per split are even and together reach the end, whatever the sizes."""
+    for k in range(32, 4097, 96):
+        p = ci8.plan_fields(plan(linear(x=mat(64, k, BF16), y=mat(64, 48, BF16), w=mat(48, k, BF16))))
+        assert int(p["stages"]) == -(-k // 32)
+        assert 1 <= int(p["split"]) <= 64
+
+
+def cpu_calls():
+    x, w = torch.zeros(4, 16, dtype=torch.bfloat16), torch.zeros(8, 16, dtype=torch.bfloat16)
+    s = torch.zeros(4)
+    return {
+        "linear": lambda: ci8.linear(x, w),
+        "linear_backward": lambda: ci8.linear_backward(torch.zeros(4, 8, dtype=torch.bfloat16), x, w),
+        "layer_norm": lambda: ci8.layer_norm(x),
+        "layer_norm_i8": lambda: ci8.layer_norm_i8(x),
+        "layer_norm_backward": lambda: ci8.layer_norm_backward(x, x, None, s, s),
+    }
+
+
+@pytest.mark.parametrize("name", list(cpu_calls()))
+def test_wrappers_refuse_host_tensors(monkeypatch, name):
+    monkeypatch.setattr(dense, "lib", None)
+    with pytest.raises(ValueError, match="expected a GPU tensor"):
+        cpu_calls()[name]()
+
+
+def test_wrappers_refuse_non_tensors():
+    with pytest.raises(TypeError):
+        ci8.linear([1.0], torch.zeros(2, 2))
+    with pytest.raises(TypeError):
+        ci8.layer_norm(None)
