@@ -129,6 +129,23 @@ __device__ __forceinline__ void store_dt(void *p, int dt, int64_t i, float v)
         ((float *)p)[i] = v;
 }
 
+// 16x16 matrix product of 64 bytes of the inner dimension: lane l gives row
+// l % 16 of each operand at bytes 16 (l / 16), and holds column l % 16 (the
+// second operand's row), rows 4 (l / 16) .. +3 of the result.
+template <typename T> struct Acc4 { typedef v4f type; };
+template <> struct Acc4<int8_t> { typedef v4i type; };
+
+template <typename T>
+__device__ __forceinline__ typename Acc4<T>::type mfma16(v4i a, v4i b, typename Acc4<T>::type c)
+{
+    if constexpr (sizeof(T) == 1)
+        return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
+    else if constexpr (__is_same(T, bf16))
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), c, 0, 0, 0);
+}
+
 // 1 / (1 + exp(-x)) from the hardware's exp2 and reciprocal (1 ulp each; the
 // product with log2 e costs |x| 2^-24 relative, far below a 16-bit rounding).
 // exp2 overflows to infinity and its reciprocal to 0, so both tails are exact.
@@ -242,14 +259,21 @@ __device__ __forceinline__ v4i make_rsrc(const void *p, int range)
     return d;
 }
 
-// 16 bytes per lane from buffer offset `voff` straight into LDS: lane i's
-// bytes land at lds + 16*i.  An offset outside the range writes zeros.  The
-// compiler does not see these loads, so the kernel counts them itself with
-// s_waitcnt vmcnt.
-__device__ __forceinline__ void load16_to_lds(v4i rsrc, unsigned lds_addr, int voff)
+// A load of 16 bytes per lane from buffer offset `voff` straight into LDS, lane
+// i's bytes to M0 + 16*i, and the write of M0 that comes before it (with at
+// least one other instruction between them: M0 needs a wait state).  An offset
+// outside the range writes zeros.  The compiler does not see these loads, so
+// the kernel counts them itself with s_waitcnt vmcnt; nothing between the two
+// may use M0.
+template <int OFFSET>
+__device__ __forceinline__ void set_lds_target(unsigned lds_base)
 {
-    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                 :: "s"(lds_addr), "v"(voff), "s"(rsrc) : "memory", "m0");
+    asm volatile("s_add_u32 m0, %0, %1" :: "s"(lds_base), "n"(OFFSET) : "m0", "scc");
+}
+
+__device__ __forceinline__ void load16_to_lds(v4i rsrc, int voff)
+{
+    asm volatile("buffer_load_dwordx4 %0, %1, 0 offen lds" :: "v"(voff), "s"(rsrc) : "memory");
 }
 
 __device__ __forceinline__ unsigned lds_address(const void *p)

@@ -56,56 +56,87 @@ struct GemmArgs {
 
 template <int N> struct Size { static constexpr int value = N; };
 
-template <typename T> struct Acc { typedef v16f type; };
-template <> struct Acc<int8_t> { typedef v16i type; };
+// f(Size<0>) .. f(Size<N-1>)
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void for_each(F f)
+{
+    if constexpr (I < N) {
+        f(Size<I>{});
+        for_each<N, I + 1>(f);
+    }
+}
 
+// acc += the 16x16 product, in place in accumulation registers.  Written as an
+// instruction because the register allocator otherwise gives the result other
+// registers than the addend and copies all of them around the loop.  The
+// compiler then knows nothing of its latency: operands come from LDS reads
+// (which it does wait for), one accumulator's instructions are FM*FN apart, and
+// the kernel waits itself before it reads the sums (mfma_drain).
 template <typename T>
-__device__ __forceinline__ typename Acc<T>::type mfma32(v4i a, v4i b, typename Acc<T>::type c)
+__device__ __forceinline__ void mfma16_acc(v4i a, v4i b, typename Acc4<T>::type &c)
 {
     if constexpr (sizeof(T) == 1)
-        return __builtin_amdgcn_mfma_i32_32x32x32_i8(a, b, c, 0, 0, 0);
+        asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
     else if constexpr (__is_same(T, bf16))
-        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
+        asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
     else
-        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), c, 0, 0, 0);
+        asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
 }
 
-// Rows form: chunk permutation of a 64-byte row.
+// More wait states than a result of the instruction above needs.
+__device__ __forceinline__ void mfma_drain()
+{
+    asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+}
+
+// Rows form: chunk permutation of a row of SB bytes.  16 rows that read one
+// chunk cover the 64 banks once: four 64-byte or two 128-byte rows make up the
+// banks' 256 bytes, and the permutation differs between those that coincide.
+template <int SB>
 __device__ __forceinline__ int row_swizzle(int row, int chunk)
 {
-    return chunk ^ (((row >> 1) ^ (row >> 2)) & 3);
+    return SB == 64 ? chunk ^ (((row >> 1) ^ (row >> 2)) & 3) : chunk ^ ((row >> 1) & 7);
 }
 
-// Columns form: 64-byte group permutation of inner row kr.  The four rows of
-// a transposing read must fall into different bank groups: rows of 256 bytes
-// and more all start at bank 0, two 128-byte rows cover the banks once.
+// Columns form: permutation of inner row kr's 32-byte groups.  32 lanes of a
+// transposing read take 32 bytes each of the eight rows k0 .. k0+3 and
+// k0+8 .. k0+11, which must cover the banks once: rows of 256 bytes and more
+// all start at bank 0, two 128-byte rows cover the banks once.
 template <int TD>
 __device__ __forceinline__ int col_swizzle(int kr)
 {
-    return TD >= 128 ? kr & 3 : (kr >> 1) & 1;
+    return TD >= 128 ? (kr & 3) | ((kr >> 1) & 4) : ((kr >> 1) & 1) | ((kr >> 2) & 2);
 }
 
+// SB: bytes of the inner dimension per stage, 64 or 128; NSA, NSB: slots of the
+// operands' rings, NSB or NSB + 1 and NSB; LH: loads per thread of a stage that
+// go out in the half that frees their slots (the others in the half after it);
 // OCC: workgroups a CU is to hold at a time (one wave of each per SIMD)
-template <typename T, int TM, int TN, int WGM, int WGN, int NS, int OCC, bool ASTR, bool BSTR>
+template <typename T, int TM, int TN, int WGM, int WGN, int SB, int NSA, int NSB, int LH, int OCC, bool ASTR, bool BSTR>
 __global__ __launch_bounds__(64 * WGM * WGN, OCC) void gemm_kernel(const GemmArgs g)
 {
     constexpr int NW = WGM * WGN;
     constexpr int ES = sizeof(T);
-    constexpr int BKE = 64 / ES;                // inner elements per stage
-    constexpr int AL = TM / (NW * 16), BL = TN / (NW * 16), LPS = AL + BL;
-    constexpr int A_BYTES = TM * 64, STAGE = (TM + TN) * 64;
+    constexpr int H = SB / 64;                  // halves of a stage, one matrix instruction deep each
+    constexpr int BKE = SB / ES;                // inner elements per stage
+    constexpr int RPB = 1024 / SB;              // rows-form rows per 1 KiB block
+    constexpr int AL = TM / (NW * RPB), BL = TN / (NW * RPB), LPS = AL + BL;
+    constexpr int A_BYTES = TM * SB, B_BYTES = TN * SB;
     constexpr int WM = TM / WGM, WN = TN / WGN;
-    constexpr int FM = WM / 32, FN = WN / 32;
-    constexpr int NMF = 2 * FM * FN;            // matrix instructions per stage
-    constexpr int NRD = 2 * (FM + FN);          // fragment reads per stage
-    static_assert(AL >= 1 && BL >= 1 && FM >= 1 && FN >= 1, "tile too small");
-    static_assert(NS >= 2 && (NS - 1) * LPS < 64, "pipeline depth");
+    constexpr int FM = WM / 16, FN = WN / 16;
+    constexpr int NMF = FM * FN;                // matrix instructions per half
+    constexpr int NRD = FM + FN;                // fragment reads per half
+    static_assert(AL >= 1 && BL >= 1 && FM >= 2 && FN >= 2, "tile too small");
+    static_assert(NSB >= 2 && (NSA == NSB || (NSA == 3 && NSB == 2)), "ring slots");
+    static_assert((NSA - 1) * AL + (NSB - 1) * BL < 64, "pipeline depth");
+    static_assert(LH <= LPS && (H > 1 || LH == LPS), "loads of a stage");
+    constexpr int RING = NSA * A_BYTES + NSB * B_BYTES, A_RING = NSA * A_BYTES;
     static_assert(!(ASTR || BSTR) || ES == 2, "transposing reads take 16-bit values");
 
     // epilogue slab of one wave: 32 rows of WN values, padded by 4
     constexpr int SP = WN + 4;
     constexpr int SLAB = 32 * SP * 4;
-    constexpr int LDS_BYTES = NS * STAGE > NW * SLAB ? NS * STAGE : NW * SLAB;
+    constexpr int LDS_BYTES = RING > NW * SLAB ? RING : NW * SLAB;
     __shared__ __attribute__((aligned(1024))) uint8_t smem[LDS_BYTES];
 
     const int tid = threadIdx.x;
@@ -128,17 +159,17 @@ __global__ __launch_bounds__(64 * WGM * WGN, OCC) void gemm_kernel(const GemmArg
 
     // ---- load geometry: load i of this wave fills the 1 KiB LDS block
     // i*NW+wave of its operand's part of the stage
-    const int row0 = wave * 16 + (lane >> 2);
-    const int j = row_swizzle(row0, lane & 3);  // the same for every i
+    const int row0 = wave * RPB + lane / (SB / 16);
+    const int j = row_swizzle<SB>(row0, lane % (SB / 16));  // the same for every i
     auto rows_off = [&](int i, int first, int dim, int64_t ld) {
-        const int r = row0 + i * NW * 16;
+        const int r = row0 + i * NW * RPB;
         return first + r < dim ? r * (int)ld + j * 16 : kOutOfRange;
     };
     auto cols_off = [&](auto td, int i, int first, int dim, int64_t ld) {
         constexpr int TD = decltype(td)::value;
         constexpr int CPR = TD / 8;             // chunks per inner row
         const int kr = (i * NW + wave) * (64 / CPR) + lane / CPR;
-        const int c = (lane % CPR) ^ (col_swizzle<TD>(kr) << 2);
+        const int c = (lane % CPR) ^ (col_swizzle<TD>(kr) << 1);
         return first + c * 8 < dim ? kr * (int)ld + c * 16 : kOutOfRange;
     };
     typedef Size<TM> TMc;
@@ -151,150 +182,251 @@ __global__ __launch_bounds__(64 * WGM * WGN, OCC) void gemm_kernel(const GemmArg
     for (int i = 0; i < BL; ++i)
         b_off[i] = BSTR ? cols_off(TNc{}, i, n0, g.N, g.ldb) : rows_off(i, n0, g.N, g.ldb);
 
-    // bases of the tile at the next stage to load
-    const uint8_t *a_base = g.a + (ASTR ? (int64_t)m0 * ES + (int64_t)stage0 * BKE * g.lda
-                                        : m0 * g.lda + (int64_t)stage0 * 64);
-    const uint8_t *b_base = g.b + (BSTR ? (int64_t)n0 * ES + (int64_t)stage0 * BKE * g.ldb
-                                        : n0 * g.ldb + (int64_t)stage0 * 64);
-    const int64_t a_step = ASTR ? BKE * g.lda : 64, b_step = BSTR ? BKE * g.ldb : 64;
-
+    // The operands' streams: buffer resource and ring slot of the next stage to
+    // load.  `full` is the range of a whole stage: without limit in rows form
+    // (offsets past an edge were set out of range above), up to the last chunk
+    // of the last inner row in columns form, where a range also ends the last,
+    // partial stage.
     const unsigned smem_lds = lds_address(smem);
-    int issued = stage0;
-    v4i a_rsrc, b_rsrc;
-    unsigned lbase = 0;
-    bool chunk_live = false;  // rows form: this lane's chunk lies inside the inner dimension
+    const int a_cols = min(TM, (g.M - m0 + 7) & ~7) * ES, b_cols = min(TN, (g.N - n0 + 7) & ~7) * ES;
+    const int a_full = ASTR ? (BKE - 1) * (int)g.lda + a_cols : 0x7fffffff;
+    const int b_full = BSTR ? (BKE - 1) * (int)g.ldb + b_cols : 0x7fffffff;
+    const int64_t a_step = ASTR ? BKE * g.lda : SB, b_step = BSTR ? BKE * g.ldb : SB;
+    // the stage in which the inner dimension ends before the stage does
+    const int tail = (ASTR || BSTR ? g.K % BKE : g.kbytes % SB) ? g.nstages - 1 : -1;
+    const int tail_k = g.K - tail * BKE;    // inner elements of it
+    v4i a_rsrc = make_rsrc(g.a + (ASTR ? (int64_t)m0 * ES + stage0 * a_step : m0 * g.lda + stage0 * a_step), a_full);
+    v4i b_rsrc = make_rsrc(g.b + (BSTR ? (int64_t)n0 * ES + stage0 * b_step : n0 * g.ldb + stage0 * b_step), b_full);
+    int a_next = stage0, b_next = stage0, a_fill = 0, b_fill = 0;
+    unsigned a_lds = smem_lds + wave * 1024, b_lds = smem_lds + A_RING + wave * 1024;
 
-    // Loads of the next stage go to ring slot `slot`.  A stage past the end
-    // loads zeros, so that every iteration issues the same number of loads.
-    auto begin_stage = [&](int slot) {
-        const bool live = issued < stage_end;
-        // columns form: the range ends with the last inner row of the stage
-        // and the last 16-byte chunk of it inside the matrix
-        const int krows = live ? min(BKE, g.K - issued * BKE) : 0;
-        a_rsrc = make_rsrc(a_base, ASTR ? (krows > 0 ? (krows - 1) * (int)g.lda + min(TM, (g.M - m0 + 7) & ~7) * ES : 0)
-                                        : (live ? 0x7fffffff : 0));
-        b_rsrc = make_rsrc(b_base, BSTR ? (krows > 0 ? (krows - 1) * (int)g.ldb + min(TN, (g.N - n0 + 7) & ~7) * ES : 0)
-                                        : (live ? 0x7fffffff : 0));
-        chunk_live = issued * 64 + j * 16 < g.kbytes;
-        lbase = smem_lds + slot * STAGE + wave * 1024;
+    // Before a stage's first load: its range (a stage past the end loads zeros,
+    // so that every iteration issues the same number of loads), and in the tail
+    // stage what lies past the inner dimension set out of range -- for good,
+    // since nothing is loaded after it.
+    auto open_a = [&]() {
+        a_rsrc.z = a_next < stage_end ? a_full : 0;
+        if (a_next == tail) {
+            if constexpr (ASTR) {
+                a_rsrc.z = a_next < stage_end ? (tail_k - 1) * (int)g.lda + a_cols : 0;
+            } else {
+                const bool in = a_next * SB + j * 16 < g.kbytes;
+#pragma unroll
+                for (int i = 0; i < AL; ++i)
+                    a_off[i] = in ? a_off[i] : kOutOfRange;
+            }
+        }
     };
-    auto dma_one = [&](int i) {
-        if (i < AL)
-            load16_to_lds(a_rsrc, lbase + i * NW * 1024, ASTR || chunk_live ? a_off[i] : kOutOfRange);
+    auto open_b = [&]() {
+        b_rsrc.z = b_next < stage_end ? b_full : 0;
+        if (b_next == tail) {
+            if constexpr (BSTR) {
+                b_rsrc.z = b_next < stage_end ? (tail_k - 1) * (int)g.ldb + b_cols : 0;
+            } else {
+                const bool in = b_next * SB + j * 16 < g.kbytes;
+#pragma unroll
+                for (int i = 0; i < BL; ++i)
+                    b_off[i] = in ? b_off[i] : kOutOfRange;
+            }
+        }
+    };
+    // After its last load: the base and the slot of the next one.
+    auto advance = [&](v4i &r, int64_t step) {
+        const uint64_t base = ((uint64_t)(unsigned)r.y << 32 | (unsigned)r.x) + step;
+        r.x = (int)(unsigned)base;
+        r.y = (int)(base >> 32);
+    };
+    auto next_a = [&]() {
+        ++a_next;
+        a_fill = a_fill + 1 == NSA ? 0 : a_fill + 1;
+        a_lds = smem_lds + wave * 1024 + a_fill * A_BYTES;
+    };
+    auto next_b = [&]() {
+        ++b_next;
+        b_fill = b_fill + 1 == NSB ? 0 : b_fill + 1;
+        b_lds = smem_lds + A_RING + wave * 1024 + b_fill * B_BYTES;
+    };
+    // Loads 0 .. BL-1 of a stage are B's: with one slot less, it is needed sooner.
+    auto aim = [&](auto ic) {
+        constexpr int i = decltype(ic)::value;
+        if constexpr (i < BL)
+            set_lds_target<i * NW * 1024>(b_lds);
+        else if constexpr (i < LPS)
+            set_lds_target<(i - BL) * NW * 1024>(a_lds);
+    };
+    auto load_one = [&](auto ic) {
+        constexpr int i = decltype(ic)::value;
+        if constexpr (i < BL)
+            load16_to_lds(b_rsrc, b_off[i]);
         else
-            load16_to_lds(b_rsrc, lbase + A_BYTES + (i - AL) * NW * 1024,
-                          BSTR || chunk_live ? b_off[i - AL] : kOutOfRange);
-    };
-    auto end_stage = [&]() {
-        ++issued;
-        a_base += a_step;
-        b_base += b_step;
+            load16_to_lds(a_rsrc, a_off[i - BL]);
     };
 
     const int wm = (wave / WGN) * WM;
     const int wn = (wave % WGN) * WN;
 
-    typename Acc<T>::type acc[FM][FN];
+    typename Acc4<T>::type acc[FM][FN];
 #pragma unroll
     for (int x = 0; x < FM; ++x)
 #pragma unroll
         for (int y = 0; y < FN; ++y)
-            acc[x][y] = typename Acc<T>::type{};
+            acc[x][y] = typename Acc4<T>::type{};
 
-    // fragments, double-buffered in registers: [0, FM) from A, [FM, FM+FN) from B
-    v4i frag[2][2][FM + FN];
-    auto read_rows = [&](const uint8_t *base, int first, int ks) {
-        const int row = first + (lane & 31);
-        return *(const v4i *)&base[row * 64 + row_swizzle(row, ks * 2 + (lane >> 5)) * 16];
+    // fragments of a half, double-buffered in registers: [0, FN) from B,
+    // [FN, FN+FM) from A
+    v4i frag[2][FN + FM];
+    auto read_rows = [&](const uint8_t *base, int first, int half) {
+        const int row = first + (lane & 15);
+        return *(const v4i *)&base[row * SB + row_swizzle<SB>(row, half * 4 + (lane >> 4)) * 16];
     };
-    auto read_cols = [&](auto td, const uint8_t *base, int first, int ks) {
+    auto read_cols = [&](auto td, const uint8_t *base, int first, int half) {
         constexpr int TD = decltype(td)::value;
         const int jj = lane & 15;
-        const int col = first + ((lane >> 4) & 1) * 16 + (jj & 3) * 4;
+        const int col = first + (jj & 3) * 4;
         v4s r[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int kr = ks * 16 + (lane >> 5) * 8 + h * 4 + (jj >> 2);
-            const uint8_t *p = base + kr * (TD * 2) + (((col >> 3) ^ (col_swizzle<TD>(kr) << 2)) << 4) + (col & 7) * 2;
+            const int kr = half * 32 + (lane >> 4) * 8 + h * 4 + (jj >> 2);
+            const uint8_t *p = base + kr * (TD * 2) + (((col >> 3) ^ (col_swizzle<TD>(kr) << 1)) << 4) + (col & 7) * 2;
             r[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)p);
         }
         return __builtin_bit_cast(v4i, __builtin_shufflevector(r[0], r[1], 0, 1, 2, 3, 4, 5, 6, 7));
     };
-    auto read_one = [&](int buf, int slot, int i) {
-        const int ks = i / (FM + FN), f = i % (FM + FN);
-        const uint8_t *base = smem + slot * STAGE;
-        if (f < FM) {
-            if constexpr (ASTR)
-                frag[buf][ks][f] = read_cols(TMc{}, base, wm + f * 32, ks);
-            else
-                frag[buf][ks][f] = read_rows(base, wm + f * 32, ks);
-        } else {
+    auto read_one = [&](int buf, int a_slot, int b_slot, int half, int i) {
+        if (i < FN) {
+            const uint8_t *base = smem + A_RING + b_slot * B_BYTES;
             if constexpr (BSTR)
-                frag[buf][ks][f] = read_cols(TNc{}, base + A_BYTES, wn + (f - FM) * 32, ks);
+                frag[buf][i] = read_cols(TNc{}, base, wn + i * 16, half);
             else
-                frag[buf][ks][f] = read_rows(base + A_BYTES, wn + (f - FM) * 32, ks);
+                frag[buf][i] = read_rows(base, wn + i * 16, half);
+        } else {
+            const uint8_t *base = smem + a_slot * A_BYTES;
+            if constexpr (ASTR)
+                frag[buf][i] = read_cols(TMc{}, base, wm + (i - FN) * 16, half);
+            else
+                frag[buf][i] = read_rows(base, wm + (i - FN) * 16, half);
         }
     };
     auto mfma_one = [&](int buf, int i) {
-        const int ks = i / (FM * FN), x = (i / FN) % FM, y = i % FN;
-        acc[x][y] = mfma32<T>(frag[buf][ks][FM + y], frag[buf][ks][x], acc[x][y]);
+        const int x = i / FN, y = i % FN;
+        mfma16_acc<T>(frag[buf][y], frag[buf][FN + x], acc[x][y]);
     };
 
-    // One stage: the matrix instructions of stage `it` (fragments in registers
-    // `buf`) are interleaved with the loads of stage it+NS into the slot that
-    // stage `it` vacated and the fragment reads of stage it+1.  The first ones
-    // need only registers and go out before the wait and the barrier.
-    constexpr int NOTHER = LPS + NRD;
+    // A half: its matrix instructions (fragments in registers `buf`) with the
+    // reads of the next half's fragments and the loads between them.  In the
+    // last half of a stage the next half is the next stage's first: a wait and
+    // a barrier come before its reads, and after them this stage's slots are
+    // free, so the loads of the stage NSB (NSA) ahead go there, the last
+    // LPS - LH of them in the next stage's first half.  The first PRE matrix
+    // instructions need only registers and go out before the wait.
+    //
+    // The order is pinned instruction by instruction.  A wave is alone on its
+    // SIMD (or shares it with one other), a matrix instruction lasts 16 cycles
+    // and every other instruction takes 4 to issue: more than three of them
+    // between two matrix instructions leave the matrix unit idle.  So reads,
+    // loads, the writes of M0 and the scalar work of a new stage go into
+    // different gaps.
     constexpr int PRE = NMF / 4;
-    int cur_slot = 0;
-    auto body = [&](int buf) {
-#pragma unroll
-        for (int i = 0; i < PRE; ++i)
-            mfma_one(buf, i);
-        __builtin_amdgcn_sched_barrier(0);
-        wait_vm_lgkm0<(NS - 2) * LPS>();
-        __builtin_amdgcn_s_barrier();
-        __builtin_amdgcn_sched_barrier(0);
-        begin_stage(cur_slot);
-        const int nslot = cur_slot + 1 == NS ? 0 : cur_slot + 1;
-#pragma unroll
-        for (int i = PRE; i < NMF; ++i) {
-            mfma_one(buf, i);
-#pragma unroll
-            for (int o = (i - PRE) * NOTHER / (NMF - PRE); o < (i - PRE + 1) * NOTHER / (NMF - PRE); ++o) {
-                if (o < LPS)
-                    dma_one(o);
-                else
-                    read_one(buf ^ 1, nslot, o - LPS);
+    int a_slot = 0, b_slot = 0;
+    auto half = [&](auto bufc, auto hc) __attribute__((always_inline)) {
+        constexpr int buf = decltype(bufc)::value, h = decltype(hc)::value;
+        constexpr bool last = h == H - 1;
+        constexpr int first = last ? PRE : 0;   // matrix instructions before reads may start
+        constexpr int np = NMF - first, nr = np * 3 / 4 > 0 ? np * 3 / 4 : 1;
+        constexpr int l0 = last ? 0 : LH, nl = last ? LH : h == 0 ? LPS - LH : 0;
+        const int an = a_slot + 1 == NSA ? 0 : a_slot + 1, bn = b_slot + 1 == NSB ? 0 : b_slot + 1;
+        for_each<NMF>([&](auto ic) __attribute__((always_inline)) {
+            constexpr int i = decltype(ic)::value;
+            if constexpr (last && i == PRE) {
+                wait_vm_lgkm0<(NSA - 2) * AL + (NSB - 2) * BL>();
+                __builtin_amdgcn_s_barrier();
+                __builtin_amdgcn_sched_barrier(0);
             }
+            mfma_one(buf, i);
+            if constexpr (last && i < PRE) {
+                // the stage whose loads start after the barrier
+                constexpr int step = PRE / 6 > 0 ? PRE / 6 : 1;
+                if constexpr (i == 0)
+                    advance(b_rsrc, b_step);
+                if constexpr (i == (step < PRE ? step : 0))
+                    next_b();
+                if constexpr (i == (2 * step < PRE ? 2 * step : 0))
+                    open_b();
+                if constexpr (i == (3 * step < PRE ? 3 * step : 0))
+                    advance(a_rsrc, a_step);
+                if constexpr (i == (4 * step < PRE ? 4 * step : 0))
+                    next_a();
+                if constexpr (i == (5 * step < PRE ? 5 * step : 0))
+                    open_a();
+            }
+            if constexpr (i == (first > 0 ? first - 1 : 0) && nl > 0)
+                aim(Size<l0>{});
+            if constexpr (i >= first) {
+                constexpr int p = i - first;
+                constexpr int r0 = p * NRD / nr < NRD ? p * NRD / nr : NRD;
+                constexpr int r1 = (p + 1) * NRD / nr < NRD ? (p + 1) * NRD / nr : NRD;
+                for_each<r1 - r0>([&](auto oc) __attribute__((always_inline)) {
+                    read_one(buf ^ 1, last ? an : a_slot, last ? bn : b_slot, last ? 0 : h + 1, r0 + decltype(oc)::value);
+                });
+                constexpr int d0 = p * nl / np, d1 = (p + 1) * nl / np;
+                for_each<d1 - d0>([&](auto oc) __attribute__((always_inline)) {
+                    constexpr int o = l0 + d0 + decltype(oc)::value;
+                    load_one(Size<o>{});
+                    if constexpr (o + 1 < l0 + nl)
+                        aim(Size<o + 1>{});
+                });
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        });
+        if constexpr (last) {
+            a_slot = an;
+            b_slot = bn;
         }
-        end_stage();
-        cur_slot = nslot;
-        __builtin_amdgcn_sched_barrier(0);
     };
 
-    // An odd count runs one extra stage of zeros, so that the loop body holds
-    // two stages, one per fragment buffer, without a branch.
-    const int nloop = (max(stage_end - stage0, 0) + 1) & ~1;
+    // Fragment buffers alternate by half.  With one half per stage the loop
+    // body holds two stages, and an odd count runs an extra stage of zeros.
+    const int nloop = H == 1 ? (max(stage_end - stage0, 0) + 1) & ~1 : max(stage_end - stage0, 0);
     if (nloop > 0) {
-#pragma unroll
-        for (int s = 0; s < NS; ++s) {
-            begin_stage(s);
-#pragma unroll
-            for (int i = 0; i < LPS; ++i)
-                dma_one(i);
-            end_stage();
+        // The rings filled in the order of the loop: stage by stage, B before
+        // A, and A's extra slot first of all
+        auto load_part = [&](auto from, auto to) __attribute__((always_inline)) {
+            for_each<decltype(to)::value - decltype(from)::value>([&](auto ic) __attribute__((always_inline)) {
+                typedef Size<decltype(from)::value + decltype(ic)::value> I;
+                aim(I{});
+                asm volatile("s_nop 0");
+                load_one(I{});
+            });
+        };
+        if constexpr (NSA > NSB) {
+            open_a();
+            load_part(Size<BL>{}, Size<LPS>{});
+            advance(a_rsrc, a_step);
+            next_a();
         }
-        wait_vm_lgkm0<(NS - 1) * LPS>();
+        for_each<NSB>([&](auto sc) __attribute__((always_inline)) {
+            if constexpr (decltype(sc)::value > 0) {
+                advance(b_rsrc, b_step);
+                next_b();
+                advance(a_rsrc, a_step);
+                next_a();
+            }
+            open_b();
+            open_a();
+            load_part(Size<0>{}, Size<(decltype(sc)::value < NSB - 1 ? LPS : LH)>{});
+        });
+        // everything but the loads after stage 0's
+        wait_vm_lgkm0<(NSB - 2) * LPS + LH + (NSA > NSB ? AL : 0)>();
         __builtin_amdgcn_s_barrier();
 #pragma unroll
         for (int i = 0; i < NRD; ++i)
-            read_one(0, 0, i);
-        for (int it = 0; it < nloop; it += 2) {
-            body(0);
-            body(1);
+            read_one(0, 0, 0, 0, i);
+        for (int it = 0; it < nloop; it += H == 1 ? 2 : 1) {
+            half(Size<0>{}, Size<0>{});
+            half(Size<1>{}, Size<H - 1>{});
         }
-        wait_vm_lgkm0<0>();  // the trailing loads of zeros still write to the ring
+        wait_vm_lgkm0<0>();  // the trailing loads of zeros still write to the rings
+        mfma_drain();
     }
     __syncthreads();
 
@@ -311,19 +443,16 @@ __global__ __launch_bounds__(64 * WGM * WGN, OCC) void gemm_kernel(const GemmArg
     auto finish_slab = [&](auto xc) __attribute__((always_inline)) {
         constexpr int x = decltype(xc)::value;
 #pragma unroll
-        for (int y = 0; y < FN; ++y)
+        for (int x2 = 0; x2 < 2; ++x2)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                typename Acc<T>::type &v = acc[x][y];
+            for (int y = 0; y < FN; ++y) {
+                const typename Acc4<T>::type v = acc[2 * x + x2][y];
                 v4f o;
-                if constexpr (ES == 1) {
-                    // partial sums stay integers (their bits travel as floats)
-                    const v4i iv = {v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
-                    o = g.part ? __builtin_bit_cast(v4f, iv) : v4f{(float)iv.x, (float)iv.y, (float)iv.z, (float)iv.w};
-                } else {
-                    o = v4f{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
-                }
-                *(v4f *)&slab[(lane & 31) * SP + y * 32 + 8 * q + 4 * (lane >> 5)] = o;
+                if constexpr (ES == 1)  // partial sums stay integers (their bits travel as floats)
+                    o = g.part ? __builtin_bit_cast(v4f, v) : v4f{(float)v.x, (float)v.y, (float)v.z, (float)v.w};
+                else
+                    o = v;
+                *(v4f *)&slab[(x2 * 16 + (lane & 15)) * SP + y * 16 + 4 * (lane >> 4)] = o;
             }
         // one wave's LDS operations run in order: only the compiler must not
         // move the reads up
@@ -360,11 +489,11 @@ __global__ __launch_bounds__(64 * WGM * WGN, OCC) void gemm_kernel(const GemmArg
         __builtin_amdgcn_wave_barrier();
         __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
     };
-    static_assert(FM == 1 || FM == 2 || FM == 4, "slabs");
+    static_assert(FM == 2 || FM == 4 || FM == 8, "slabs");
     finish_slab(Size<0>{});
-    if constexpr (FM >= 2)
+    if constexpr (FM >= 4)
         finish_slab(Size<1>{});
-    if constexpr (FM >= 4) {
+    if constexpr (FM >= 8) {
         finish_slab(Size<2>{});
         finish_slab(Size<3>{});
     }

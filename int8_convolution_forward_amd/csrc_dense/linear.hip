@@ -119,12 +119,12 @@ constexpr TileCost kCost[kTiles] = {
     {0.06f, 0.15f, 2.0f},
 };
 
-double gemm_cost(int tile, int64_t M, int64_t N, int64_t nstages, int splits)
+double gemm_cost(int tile, int64_t M, int64_t N, int64_t kbytes, int splits)
 {
     const Tile &t = kTile[tile];
     const TileCost &c = kCost[tile];
     const int64_t wgs = ceil_div(M, t.tm) * ceil_div(N, t.tn) * splits;
-    const double stages = (double)ceil_div(nstages, splits);
+    const double stages = (double)ceil_div(kbytes, 64 * splits);
     const int64_t per_cu = ceil_div(wgs, kCUs);
     const double rounds = (double)ceil_div(per_cu, t.occ);
     double us = rounds * (stages * c.alone + c.fixed);
@@ -140,7 +140,6 @@ const char *forced_tile() { return getenv("CONV_I8_DENSE_TILE"); }
 
 void plan_gemm(int64_t M, int64_t N, int64_t K, int es, GemmPlan *p)
 {
-    const int64_t nstages = ceil_div(K * es, 64);
     int best = 0, best_s = 1;
     double least = 1e30;
     const char *force = forced_tile();  // "256x128" or "256x128/4": a tile and a split for tests and sweeps
@@ -153,11 +152,12 @@ void plan_gemm(int64_t M, int64_t N, int64_t K, int es, GemmPlan *p)
             only_split = force[len] == '/' ? atoi(force + len + 1) : 0;
         }
         const int64_t tiles = ceil_div(M, kTile[t].tm) * ceil_div(N, kTile[t].tn);
+        const int64_t nstages = ceil_div(K * es, kTile[t].sb);
         for (int s = 1; s <= 64; s *= 2) {
             const int use = only_split > 0 ? (only_split < 64 ? only_split : 64) : s;
             if (use > 1 && (nstages < 4 * use || (only_split == 0 && tiles * use > 2 * kCUs * kTile[t].occ)))
                 break;
-            const double us = gemm_cost(t, M, N, nstages, use);
+            const double us = gemm_cost(t, M, N, K * es, use);
             if (us < least) {
                 least = us;
                 best = t;
@@ -170,6 +170,7 @@ void plan_gemm(int64_t M, int64_t N, int64_t K, int es, GemmPlan *p)
     p->tile = best;
     p->tiles_m = (int)ceil_div(M, kTile[best].tm);
     p->tiles_n = (int)ceil_div(N, kTile[best].tn);
+    const int64_t nstages = ceil_div(K * es, kTile[best].sb);
     p->nstages = (int)nstages;
     p->kchunk = nstages > 0 ? (int)round_up(ceil_div(nstages, best_s), 2) : 0;
     p->splits = nstages > 0 ? (int)ceil_div(nstages, p->kchunk) : 1;

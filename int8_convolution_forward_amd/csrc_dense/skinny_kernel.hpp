@@ -22,20 +22,6 @@ struct SkinnyArgs {
     Epilogue epi;
 };
 
-template <typename T> struct Acc4 { typedef v4f type; };
-template <> struct Acc4<int8_t> { typedef v4i type; };
-
-template <typename T>
-__device__ __forceinline__ typename Acc4<T>::type mfma16(v4i a, v4i b, typename Acc4<T>::type c)
-{
-    if constexpr (sizeof(T) == 1)
-        return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
-    else if constexpr (__is_same(T, bf16))
-        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
-    else
-        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), c, 0, 0, 0);
-}
-
 // 16 bytes at any address that is a multiple of the element size
 template <typename T>
 struct __attribute__((packed, aligned(sizeof(T)))) Piece16 {
