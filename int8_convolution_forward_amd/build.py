@@ -4,6 +4,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import sysconfig
 import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -24,6 +25,9 @@ DENSE_CSRC = os.path.join(PKG, "csrc_dense")
 DENSE_LIB = os.path.join(LIB_DIR, "libdense.so")
 DENSE_SOURCES = [os.path.join(DENSE_CSRC, f) for f in ("linear.hip", "gemm_bf16.hip", "gemm_f16.hip", "gemm_i8.hip",
                                                       "norm.hip")]
+# ... and the Python module that hands tensors to it (host code only)
+DENSE_BIND_SOURCE = os.path.join(DENSE_CSRC, "bind.cpp")
+DENSE_BIND = os.path.join(LIB_DIR, "_dense.so")
 
 HIP_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",
@@ -54,17 +58,30 @@ def _run(cmds: list, verbose: bool) -> None:
         elif verbose and msgs:
             print("\n".join(msgs))
     if failed:
-        raise RuntimeError("hipcc failed:\n" + "\n".join(failed))
+        raise RuntimeError("the compiler failed:\n" + "\n".join(failed))
+
+
+def bind_command(out: str) -> list:
+    import torch
+
+    base = os.path.dirname(torch.__file__)
+    include = [os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
+               "/opt/rocm/include", sysconfig.get_paths()["include"], INCLUDE]
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1",
+            "-DUSE_ROCM=1", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            *[f for i in include for f in ("-I", i)], DENSE_BIND_SOURCE, "-o", out, "-L", os.path.join(base, "lib"),
+            "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_hip"]
 
 
 def build(verbose: bool = False, dense_only: bool = False) -> str:
     """Compiles both libraries, all sources side by side (the convolution's
     takes minutes), or only the dense one."""
     os.makedirs(LIB_DIR, exist_ok=True)
-    tmp, dense_tmp = LIB + ".tmp", DENSE_LIB + ".tmp"
+    tmp, dense_tmp, bind_tmp = (f + ".tmp" for f in (LIB, DENSE_LIB, DENSE_BIND))
     objects = [os.path.join(LIB_DIR, os.path.basename(s)[:-4] + ".o") for s in DENSE_SOURCES]
     compile_flags = [f for f in HIP_FLAGS if f != "-shared"]
     cmds = [] if dense_only else [[HIPCC, *HIP_FLAGS, "-I", INCLUDE, "-I", CSRC, *SOURCES, "-o", tmp]]
+    cmds.append(bind_command(bind_tmp))
     cmds += [[HIPCC, *compile_flags, "-I", INCLUDE, "-I", DENSE_CSRC, "-c", s, "-o", o]
              for s, o in zip(DENSE_SOURCES, objects)]
     _run(cmds, verbose)
@@ -72,6 +89,7 @@ def build(verbose: bool = False, dense_only: bool = False) -> str:
     if not dense_only:
         os.replace(tmp, LIB)
     os.replace(dense_tmp, DENSE_LIB)
+    os.replace(bind_tmp, DENSE_BIND)
     return LIB
 
 

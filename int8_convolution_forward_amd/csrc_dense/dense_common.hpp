@@ -129,6 +129,18 @@ __device__ __forceinline__ void store_dt(void *p, int dt, int64_t i, float v)
         ((float *)p)[i] = v;
 }
 
+template <int N> struct Size { static constexpr int value = N; };
+
+// f(Size<0>) .. f(Size<N-1>)
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void for_each(F f)
+{
+    if constexpr (I < N) {
+        f(Size<I>{});
+        for_each<N, I + 1>(f);
+    }
+}
+
 // 16x16 matrix product of 64 bytes of the inner dimension: lane l gives row
 // l % 16 of each operand at bytes 16 (l / 16), and holds column l % 16 (the
 // second operand's row), rows 4 (l / 16) .. +3 of the result.
@@ -237,6 +249,15 @@ __device__ __forceinline__ float activate_rt(int act, float z)
                                         : z;
 }
 
+// Chunk permutation of an LDS row of SB bytes.  16 rows that read one
+// chunk cover the 64 banks once: four 64-byte or two 128-byte rows make up the
+// banks' 256 bytes, and the permutation differs between those that coincide.
+template <int SB>
+__device__ __forceinline__ int row_swizzle(int row, int chunk)
+{
+    return SB == 64 ? chunk ^ (((row >> 1) ^ (row >> 2)) & 3) : chunk ^ ((row >> 1) & 7);
+}
+
 // s_waitcnt immediate (gfx9 encoding): at most VM vector-memory operations
 // outstanding, all LDS operations done.
 template <int VM>
@@ -244,6 +265,12 @@ __device__ __forceinline__ void wait_vm_lgkm0()
 {
     static_assert(VM >= 0 && VM < 64, "vmcnt out of range");
     __builtin_amdgcn_s_waitcnt((VM & 15) | ((VM >> 4) << 14) | (7 << 4) | (0 << 8));
+}
+
+// All LDS operations done, any number of vector-memory operations outstanding.
+__device__ __forceinline__ void wait_lgkm0()
+{
+    __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4) | (0 << 8));
 }
 
 // Buffer resource (gfx9 layout): base address, stride 0, byte range, 32-bit

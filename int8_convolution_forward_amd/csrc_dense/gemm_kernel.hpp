@@ -54,18 +54,6 @@ struct GemmArgs {
     Epilogue epi;
 };
 
-template <int N> struct Size { static constexpr int value = N; };
-
-// f(Size<0>) .. f(Size<N-1>)
-template <int N, int I = 0, typename F>
-__device__ __forceinline__ void for_each(F f)
-{
-    if constexpr (I < N) {
-        f(Size<I>{});
-        for_each<N, I + 1>(f);
-    }
-}
-
 // acc += the 16x16 product, in place in accumulation registers.  Written as an
 // instruction because the register allocator otherwise gives the result other
 // registers than the addend and copies all of them around the loop.  The
@@ -87,15 +75,6 @@ __device__ __forceinline__ void mfma16_acc(v4i a, v4i b, typename Acc4<T>::type 
 __device__ __forceinline__ void mfma_drain()
 {
     asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
-}
-
-// Rows form: chunk permutation of a row of SB bytes.  16 rows that read one
-// chunk cover the 64 banks once: four 64-byte or two 128-byte rows make up the
-// banks' 256 bytes, and the permutation differs between those that coincide.
-template <int SB>
-__device__ __forceinline__ int row_swizzle(int row, int chunk)
-{
-    return SB == 64 ? chunk ^ (((row >> 1) ^ (row >> 2)) & 3) : chunk ^ ((row >> 1) & 7);
 }
 
 // Columns form: permutation of inner row kr's 32-byte groups.  32 lanes of a

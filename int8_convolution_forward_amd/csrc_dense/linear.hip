@@ -290,11 +290,15 @@ conv_i8_status_t analyze(const dense_linear_t *args, LinearPlan *p)
     const bool x_rows = d.x.col_stride == 1 || p->K <= 1, w_rows = d.w.col_stride == 1 || p->K <= 1;
     p->skinny = p->M <= kSkinnyRows && x_rows && w_rows && !forced_tile();
     if (p->skinny) {
-        p->aligned = (((uintptr_t)d.x.ptr | (uintptr_t)d.w.ptr) & 15) == 0 &&
+        p->aligned = (((uintptr_t)d.x.ptr | (uintptr_t)d.w.ptr) & 15) == 0 && p->K * es % 16 == 0 &&
                      (p->M <= 1 || d.x.row_stride * es % 16 == 0) && (p->N <= 1 || d.w.row_stride * es % 16 == 0);
-        // more waves share a row block's inner dimension where there are few row blocks
-        const int64_t blocks = ceil_div(p->N, 16);
-        p->waves = blocks >= 4 * kCUs ? 4 : blocks >= kCUs ? 8 : 16;
+        // load offsets are 31-bit: 32 rows from a workgroup's first
+        if (p->M > 1 && d.x.row_stride * es > kMaxRowBytes)
+            p->aligned = false;
+        if (p->N > 1 && d.w.row_stride * es > kMaxRowBytes)
+            p->aligned = false;
+        // blocks of 128 bytes of the inner dimension for every wave, or fewer waves
+        p->waves = !p->aligned ? 8 : p->K * es < 16 * 128 ? 4 : p->M <= 16 ? 16 : 8;
         return CONV_I8_OK;
     }
     p->a.src = d.x.ptr;
@@ -337,25 +341,31 @@ Epilogue epilogue_of(const dense_linear_t &d)
     return e;
 }
 
-template <typename T, int G, bool ALIGNED>
-void launch_skinny_w(const SkinnyArgs &s, int waves, hipStream_t stream)
-{
-    const dim3 grid((unsigned)ceil_div(s.N, 16)), block(64u * waves);
-    if (waves == 4)
-        hipLaunchKernelGGL((skinny_kernel<T, G, 4, ALIGNED>), grid, block, 0, stream, s);
-    else if (waves == 8)
-        hipLaunchKernelGGL((skinny_kernel<T, G, 8, ALIGNED>), grid, block, 0, stream, s);
-    else
-        hipLaunchKernelGGL((skinny_kernel<T, G, 16, ALIGNED>), grid, block, 0, stream, s);
-}
-
 template <typename T>
 bool launch_skinny(const SkinnyArgs &s, const LinearPlan &p, hipStream_t stream)
 {
-    if (p.M <= 16)
-        p.aligned ? launch_skinny_w<T, 1, true>(s, p.waves, stream) : launch_skinny_w<T, 1, false>(s, p.waves, stream);
-    else
-        p.aligned ? launch_skinny_w<T, 2, true>(s, p.waves, stream) : launch_skinny_w<T, 2, false>(s, p.waves, stream);
+    const dim3 one((unsigned)ceil_div(s.N, 16)), two((unsigned)ceil_div(s.N, 32));
+    if (!p.aligned) {
+        if (p.M <= 16)
+            hipLaunchKernelGGL((skinny_direct_kernel<T, 1, 8>), one, dim3(512), 0, stream, s);
+        else
+            hipLaunchKernelGGL((skinny_direct_kernel<T, 2, 8>), one, dim3(512), 0, stream, s);
+    } else if (p.M <= 4) {
+        if (p.waves == 4)
+            hipLaunchKernelGGL((skinny_kernel<T, 1, 1, 4, 4, false>), one, dim3(256), 0, stream, s);
+        else
+            hipLaunchKernelGGL((skinny_kernel<T, 1, 1, 16, 2, false>), one, dim3(1024), 0, stream, s);
+    } else if (p.M <= 16) {
+        if (p.waves == 4)
+            hipLaunchKernelGGL((skinny_kernel<T, 1, 1, 4, 4, true>), one, dim3(256), 0, stream, s);
+        else
+            hipLaunchKernelGGL((skinny_kernel<T, 1, 1, 16, 2, true>), one, dim3(1024), 0, stream, s);
+    } else {
+        if (p.waves == 4)
+            hipLaunchKernelGGL((skinny_kernel<T, 2, 2, 4, 2, true>), two, dim3(256), 0, stream, s);
+        else
+            hipLaunchKernelGGL((skinny_kernel<T, 2, 2, 8, 2, true>), two, dim3(512), 0, stream, s);
+    }
     return hipGetLastError() == hipSuccess;
 }
 
@@ -615,8 +625,8 @@ conv_i8_status_t run_backward(const BackwardPlan &p, void *ws, hipStream_t strea
 
 int describe(const GemmPlan &p, const Operand &a, const Operand &b, char *buf, size_t len)
 {
-    return snprintf(buf, len, "tile=%s tiles=%d split=%d stages=%d a=%s%s b=%s%s", kTile[p.tile].name,
-                    p.tiles_m * p.tiles_n, p.splits, p.nstages, a.cols ? "cols" : "rows", a.packed ? "_packed" : "",
+    return snprintf(buf, len, "tile=%s tiles=%d split=%d stages=%d per_split=%d a=%s%s b=%s%s",
+                    kTile[p.tile].name, p.tiles_m * p.tiles_n, p.splits, p.nstages, p.kchunk, a.cols ? "cols" : "rows", a.packed ? "_packed" : "",
                     b.cols ? "cols" : "rows", b.packed ? "_packed" : "");
 }
 
