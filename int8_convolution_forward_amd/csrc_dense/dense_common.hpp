@@ -38,78 +38,80 @@ inline int dtype_size(int64_t dt)
     return dt == DENSE_INT8 ? 1 : dt == DENSE_FP32 ? 4 : dt == DENSE_BF16 || dt == DENSE_FP16 ? 2 : 0;
 }
 
-// Eight values at any element-aligned address.  gfx950 runs with unaligned
-// vector access enabled, so these are one or two 16-byte instructions whatever
-// the address; an address that is a multiple of 16 costs nothing extra.
-template <typename T>
-struct __attribute__((packed, aligned(sizeof(T)))) Pack8 {
-    T e[8];
+// C values at any element-aligned address.  gfx950 runs with unaligned vector
+// access enabled, so 16 bytes are one instruction whatever the address; an
+// address that is a multiple of 16 costs nothing extra.
+template <typename T, int C>
+struct __attribute__((packed, aligned(sizeof(T)))) Pack {
+    T e[C];
 };
 
-template <typename T>
-__device__ __forceinline__ void load8(const T *p, float (&v)[8])
+template <typename T, int C>
+__device__ __forceinline__ void load_all(const T *p, float (&v)[C])
 {
-    const Pack8<T> q = *(const Pack8<T> *)p;
+    const Pack<T, C> q = *(const Pack<T, C> *)p;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < C; ++i)
         v[i] = (float)q.e[i];
 }
 
-template <typename T>
-__device__ __forceinline__ void store8(T *p, const float (&v)[8])
+template <typename T, int C>
+__device__ __forceinline__ void store_all(T *p, const float (&v)[C])
 {
-    Pack8<T> q;
+    Pack<T, C> q;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < C; ++i)
         q.e[i] = (T)v[i];
-    *(Pack8<T> *)p = q;
+    *(Pack<T, C> *)p = q;
 }
 
-// The first n of eight values (n may be 8 or more); the others read as `fill`.
-template <typename T>
-__device__ __forceinline__ void load8n(const T *p, int n, float (&v)[8], float fill = 0.0f)
+// The first n of C values (n may be C or more); the others read as `fill`.
+template <typename T, int C>
+__device__ __forceinline__ void load_n(const T *p, int n, float (&v)[C], float fill = 0.0f)
 {
-    if (n >= 8) {
-        load8(p, v);
+    if (n >= C) {
+        load_all(p, v);
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < C; ++i)
             v[i] = i < n ? (float)p[i] : fill;
     }
 }
 
-template <typename T>
-__device__ __forceinline__ void store8n(T *p, int n, const float (&v)[8])
+template <typename T, int C>
+__device__ __forceinline__ void store_n(T *p, int n, const float (&v)[C])
 {
-    if (n >= 8) {
-        store8(p, v);
+    if (n >= C) {
+        store_all(p, v);
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < C; ++i)
             if (i < n)
                 p[i] = (T)v[i];
     }
 }
 
 // The same with the element type given at run time (uniform over the launch).
-__device__ __forceinline__ void load8n_dt(const void *p, int dt, int64_t off, int n, float (&v)[8])
+template <int C>
+__device__ __forceinline__ void load_n_dt(const void *p, int dt, int64_t off, int n, float (&v)[C])
 {
     if (dt == DENSE_BF16)
-        load8n((const bf16 *)p + off, n, v);
+        load_n((const bf16 *)p + off, n, v);
     else if (dt == DENSE_FP16)
-        load8n((const f16 *)p + off, n, v);
+        load_n((const f16 *)p + off, n, v);
     else
-        load8n((const float *)p + off, n, v);
+        load_n((const float *)p + off, n, v);
 }
 
-__device__ __forceinline__ void store8n_dt(void *p, int dt, int64_t off, int n, const float (&v)[8])
+template <int C>
+__device__ __forceinline__ void store_n_dt(void *p, int dt, int64_t off, int n, const float (&v)[C])
 {
     if (dt == DENSE_BF16)
-        store8n((bf16 *)p + off, n, v);
+        store_n((bf16 *)p + off, n, v);
     else if (dt == DENSE_FP16)
-        store8n((f16 *)p + off, n, v);
+        store_n((f16 *)p + off, n, v);
     else
-        store8n((float *)p + off, n, v);
+        store_n((float *)p + off, n, v);
 }
 
 __device__ __forceinline__ float load_dt(const void *p, int dt, int64_t i)
@@ -220,14 +222,14 @@ __device__ __forceinline__ float act_slope(float z)
     }
 }
 
-template <int U>
-__device__ __forceinline__ void activate8(int act, float (&v)[U][8])
+template <int U, int C>
+__device__ __forceinline__ void activate_all(int act, float (&v)[U][C])
 {
     auto all = [&](auto f) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < C; ++i)
                 v[u][i] = f(v[u][i]);
     };
     if (act == DENSE_ACT_RELU)
@@ -346,33 +348,34 @@ struct Epilogue {
     int out_dt;             // of out, residual and preact
     int bias_dt;
     int act;
+    int tile_offsets;       // 256 rows of every matrix above span less than 2^31 bytes
 };
 
-// The epilogue of U chunks of eight columns n .. n+cnt-1, chunk u in row
+// The epilogue of U chunks of C columns, of which n .. n+cnt-1 exist, chunk u in row
 // m + u*step: v holds the products' sums, ws and bs the columns' scales and
 // biases.  Rows from M on are skipped.  All residuals are loaded first, so that
 // their latencies overlap.
-template <bool SCALED, int U>
-__device__ __forceinline__ void finish8(const Epilogue &e, int64_t m, int step, int64_t M, int64_t n, int cnt,
-                                        float (&v)[U][8], const float (&bs)[8], const float (&ws)[8])
+template <bool SCALED, int U, int C>
+__device__ __forceinline__ void finish(const Epilogue &e, int64_t m, int step, int64_t M, int64_t n, int cnt,
+                                       float (&v)[U][C], const float (&bs)[C], const float (&ws)[C])
 {
-    float r[U][8];
+    float r[U][C];
     if (e.residual) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (m + u * step < M)
-                load8n_dt(e.residual, e.out_dt, (m + u * step) * e.ldr + n, cnt, r[u]);
+                load_n_dt(e.residual, e.out_dt, (m + u * step) * e.ldr + n, cnt, r[u]);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         if constexpr (SCALED) {
             const float xs = e.x_scale && m + u * step < M ? e.x_scale[m + u * step] : 1.0f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < C; ++i)
                 v[u][i] = __builtin_fmaf(v[u][i], xs * ws[i], bs[i]);
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < C; ++i)
                 v[u][i] += bs[i];
         }
     }
@@ -380,34 +383,35 @@ __device__ __forceinline__ void finish8(const Epilogue &e, int64_t m, int step, 
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (m + u * step < M)
-                store8n_dt(e.preact, e.out_dt, (m + u * step) * e.ldp + n, cnt, v[u]);
+                store_n_dt(e.preact, e.out_dt, (m + u * step) * e.ldp + n, cnt, v[u]);
     }
-    activate8(e.act, v);
+    activate_all(e.act, v);
     if (e.residual) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < C; ++i)
                 v[u][i] += r[u][i];
     }
 #pragma unroll
     for (int u = 0; u < U; ++u)
         if (m + u * step < M)
-            store8n_dt(e.out, e.out_dt, (m + u * step) * e.ldo + n, cnt, v[u]);
+            store_n_dt(e.out, e.out_dt, (m + u * step) * e.ldo + n, cnt, v[u]);
 }
 
 // Scales and biases of columns n .. n+cnt-1 (ones and zeros where absent).
-__device__ __forceinline__ void column_params(const Epilogue &e, int64_t n, int cnt, float (&bs)[8], float (&ws)[8])
+template <int C>
+__device__ __forceinline__ void column_params(const Epilogue &e, int64_t n, int cnt, float (&bs)[C], float (&ws)[C])
 {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < C; ++i) {
         bs[i] = 0.0f;
         ws[i] = 1.0f;
     }
     if (e.bias)
-        load8n_dt(e.bias, e.bias_dt, n, cnt, bs);
+        load_n_dt(e.bias, e.bias_dt, n, cnt, bs);
     if (e.w_scale)
-        load8n(e.w_scale + n, cnt, ws);
+        load_n(e.w_scale + n, cnt, ws);
 }
 
 }  // namespace dense

@@ -2,19 +2,21 @@
 // dense layer's epilogue, operands BF16, FP16 (32-bit float sums) or INT8
 // (32-bit integer sums).
 //
-// A workgroup of four waves computes a TM x TN tile.  Both operands stream
-// from memory straight into a ring of NS LDS stages (buffer_load ... lds, 16
-// bytes a lane, no staging registers), NS-1 stages ahead of the one that is
-// multiplied; one barrier per stage publishes the stage that landed and
-// retires the slot the next loads overwrite.  A stage is 64 bytes of the inner
-// dimension: 32 BF16/FP16 or 64 INT8 values, two matrix instructions deep.
+// A workgroup of four waves computes a TM x TN tile.  Both operands stream from
+// memory straight into rings of LDS stages (buffer_load ... lds, 16 bytes a
+// lane, no staging registers); one barrier per stage publishes the stage that
+// landed and retires the slots the next loads overwrite.  A stage is 128 bytes
+// of the inner dimension: 64 BF16/FP16 or 128 INT8 values.  (Stages of 64 bytes
+// make twice the requests to the cache for the same data: 709 us against 605
+// for 8192^3 BF16 zeros.  The 256x256 tile has three slots for A and two for B,
+// which fills the 160 KB: two for both leave 100 us of waits there.)
 //
 // An operand is stored in one of two ways:
-//  * rows (STR false): the inner dimension is contiguous.  LDS holds 64-byte
-//    rows whose 16-byte chunks are permuted by row bits 1..2, so that the 32
-//    rows a fragment read touches spread over all banks.
+//  * rows (STR false): the inner dimension is contiguous.  LDS holds 128-byte
+//    rows whose 16-byte chunks are permuted so that the 16 rows a fragment read
+//    touches cover the banks once.
 //  * columns (STR true, 16-bit types): the inner dimension has the stride.
-//    LDS holds one row of TM (TN) values per inner index, 64-byte groups
+//    LDS holds one row of TM (TN) values per inner index, 32-byte groups
 //    permuted by the row's low bits; fragments come from transposing reads
 //    (ds_read_tr16_b64: lane i of a 16-lane group gets value i % 4 of the
 //    four 8-byte pieces that lanes 4b + i/4 address).
@@ -27,16 +29,22 @@
 // row's end (others are copied into that form first).  Bases advance by 64-bit
 // scalar adds, so only offsets within one tile have to fit 31 bits.
 //
-// Matrix operands are passed as (B, A): a lane then holds one row m and four
-// consecutive columns n at a time.  The epilogue turns 32-row slabs of the
-// wave's tile through its own part of LDS, so that every lane loads, computes
-// and stores eight consecutive columns (16 bytes) and a wave writes whole
-// 256-byte row segments.
+// Epilogue.  A lane holds one of 16 columns of each 16x16 block.  With B in rows
+// form, lane i reads the fragment of block y from column FN i + y of the wave's
+// part of B (FN blocks of 16 columns), so that it ends up with FN consecutive
+// columns of a row and sixteen lanes with the row's whole segment of the wave's
+// tile: bias, activation, residual and stores are 16 bytes a lane (FN = 8) and
+// 256 contiguous bytes a row, straight from the accumulators.  Tiles at an edge,
+// partial sums, 32-bit outputs and B in columns form (whose transposing reads
+// cannot give that order) turn through LDS.
 #pragma once
 
 #include "dense_common.hpp"
 
 namespace dense {
+
+// Bytes of the inner dimension per stage: two halves, one matrix instruction deep each
+constexpr int kStageBytes = 128;
 
 struct GemmArgs {
     const uint8_t *a, *b;
@@ -60,15 +68,23 @@ struct GemmArgs {
 // compiler then knows nothing of its latency: operands come from LDS reads
 // (which it does wait for), one accumulator's instructions are FM*FN apart, and
 // the kernel waits itself before it reads the sums (mfma_drain).
-template <typename T>
+// VGPR: the sums lie in ordinary registers instead.
+template <typename T, bool VGPR>
 __device__ __forceinline__ void mfma16_acc(v4i a, v4i b, typename Acc4<T>::type &c)
 {
-    if constexpr (sizeof(T) == 1)
-        asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
-    else if constexpr (__is_same(T, bf16))
-        asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
-    else
-        asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+#define DENSE_MFMA(NAME)                                                             \
+    if constexpr (VGPR)                                                              \
+        asm volatile("v_mfma_" NAME " %0, %1, %2, %0" : "+v"(c) : "v"(a), "v"(b));   \
+    else                                                                             \
+        asm volatile("v_mfma_" NAME " %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b))
+    if constexpr (sizeof(T) == 1) {
+        DENSE_MFMA("i32_16x16x64_i8");
+    } else if constexpr (__is_same(T, bf16)) {
+        DENSE_MFMA("f32_16x16x32_bf16");
+    } else {
+        DENSE_MFMA("f32_16x16x32_f16");
+    }
+#undef DENSE_MFMA
 }
 
 // More wait states than a result of the instruction above needs.
@@ -87,16 +103,132 @@ __device__ __forceinline__ int col_swizzle(int kr)
     return TD >= 128 ? (kr & 3) | ((kr >> 1) & 4) : ((kr >> 1) & 1) | ((kr >> 2) & 2);
 }
 
-// SB: bytes of the inner dimension per stage, 64 or 128; NSA, NSB: slots of the
-// operands' rings, NSB or NSB + 1 and NSB; LH: loads per thread of a stage that
-// go out in the half that frees their slots (the others in the half after it);
-// OCC: workgroups a CU is to hold at a time (one wave of each per SIMD)
-template <typename T, int TM, int TN, int WGM, int WGN, int SB, int NSA, int NSB, int LH, int OCC, bool ASTR, bool BSTR>
+// B in rows form, in the order of the epilogue: a fragment read takes the rows
+// FN i + y, i = 0 .. 15, all of one parity.  Two 128-byte rows make up the
+// banks' 256 bytes, so the 16 slots of a pair of rows are permuted together, by
+// the pair's number in units of the pairs a read skips.
+template <int FN>
+__device__ __forceinline__ int pair_swizzle(int pair, int slot)
+{
+    return slot ^ ((pair / (FN / 2)) & 15);
+}
+
+template <typename T> struct Type { typedef T type; };
+
+// C values as the bits of 16-bit output type O, and back
+template <typename O, int C> struct Bits { typedef O vec __attribute__((ext_vector_type(C))); };
+template <int C> struct Words;
+template <> struct Words<8> { typedef v4i type; };
+template <> struct Words<4> { typedef int type __attribute__((ext_vector_type(2))); };
+template <> struct Words<2> { typedef int type; };
+
+template <int C>
+__device__ __forceinline__ void buffer_store(typename Words<C>::type v, __amdgpu_buffer_rsrc_t r, int voff, int soff)
+{
+    if constexpr (C == 8)
+        __builtin_amdgcn_raw_buffer_store_b128(v, r, voff, soff, 0);
+    else if constexpr (C == 4)
+        __builtin_amdgcn_raw_buffer_store_b64(v, r, voff, soff, 0);
+    else
+        __builtin_amdgcn_raw_buffer_store_b32(v, r, voff, soff, 0);
+}
+
+template <int C>
+__device__ __forceinline__ typename Words<C>::type buffer_load(__amdgpu_buffer_rsrc_t r, int voff, int soff)
+{
+    if constexpr (C == 8)
+        return __builtin_amdgcn_raw_buffer_load_b128(r, voff, soff, 0);
+    else if constexpr (C == 4)
+        return __builtin_amdgcn_raw_buffer_load_b64(r, voff, soff, 0);
+    else
+        return __builtin_amdgcn_raw_buffer_load_b32(r, voff, soff, 0);
+}
+
+// The epilogue of a wave's whole 16 FM x 16 FN tile at (m, n), values of 16-bit
+// type O, straight from the accumulators: lane l holds rows 16 x + 4 (l / 16) + u
+// and columns (l % 16) FN + y.
+template <typename T, typename O, int ACT, int FM, int FN>
+__device__ __forceinline__ void finish_whole(const Epilogue &e, typename Acc4<T>::type (&acc)[FM][FN], int m, int n,
+                                             int lane)
+{
+    typedef typename Words<FN>::type words;
+    typedef typename Bits<O, FN>::vec vec;
+    const int col = (lane & 15) * FN, row = 4 * (lane >> 4);
+    float bs[FN], ws[FN];
+    column_params(e, n + col, FN, bs, ws);
+    auto view = [&](const void *p, int64_t ld) {
+        return __builtin_amdgcn_make_buffer_rsrc((O *)const_cast<void *>(p) + m * ld + n, (short)0, 0x7fffffff, 0x00020000);
+    };
+    // residuals of four blocks of rows at a time (64 registers)
+    constexpr int RG = FM < 4 ? FM : 4;
+    words res[RG][4];
+    const __amdgpu_buffer_rsrc_t rsd = view(e.residual, e.ldr);
+    const int vr = (row * (int)e.ldr + col) * 2;
+    const __amdgpu_buffer_rsrc_t out = view(e.out, e.ldo), pre = view(e.preact, e.ldp);
+    const int vo = (row * (int)e.ldo + col) * 2, vp = (row * (int)e.ldp + col) * 2;
+    for_each<FM>([&](auto xc) __attribute__((always_inline)) {
+        constexpr int x = decltype(xc)::value;
+        if constexpr (x % RG == 0) {
+            if (e.residual)
+#pragma unroll
+                for (int i = 0; i < RG; ++i)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        res[i][u] = buffer_load<FN>(rsd, vr, (16 * (x + i) + u) * (int)e.ldr * 2);
+        }
+        float xs[4] = {1.0f, 1.0f, 1.0f, 1.0f};
+        if constexpr (sizeof(T) == 1) {
+            if (e.x_scale)
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    xs[u] = e.x_scale[m + 16 * x + row + u];
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            float z[FN];
+#pragma unroll
+            for (int y = 0; y < FN; ++y) {
+                if constexpr (sizeof(T) == 1)
+                    z[y] = __builtin_fmaf((float)acc[x][y][u], xs[u] * ws[y], bs[y]);
+                else
+                    z[y] = acc[x][y][u] + bs[y];
+            }
+            if (e.preact) {
+                vec b;
+#pragma unroll
+                for (int y = 0; y < FN; ++y)
+                    b[y] = (O)z[y];
+                buffer_store<FN>(__builtin_bit_cast(words, b), pre, vp, (16 * x + u) * (int)e.ldp * 2);
+            }
+#pragma unroll
+            for (int y = 0; y < FN; ++y)
+                z[y] = activate<ACT>(z[y]);
+            if (e.residual) {
+                const vec b = __builtin_bit_cast(vec, res[x % RG][u]);
+#pragma unroll
+                for (int y = 0; y < FN; ++y)
+                    z[y] += (float)b[y];
+            }
+            vec b;
+#pragma unroll
+            for (int y = 0; y < FN; ++y)
+                b[y] = (O)z[y];
+            buffer_store<FN>(__builtin_bit_cast(words, b), out, vo, (16 * x + u) * (int)e.ldo * 2);
+        }
+        __builtin_amdgcn_sched_barrier(0);  // one block at a time, or the values of several are held at once
+    });
+}
+
+// NSA, NSB: slots of the operands' rings, NSB or NSB + 1 and NSB; LH: loads per
+// thread of a stage that go out in the half that frees their slots (the others
+// in the half after it); OCC: workgroups a CU is to hold at a time (one wave of
+// each per SIMD)
+template <typename T, int TM, int TN, int WGM, int WGN, int NSA, int NSB, int LH, int OCC, bool ASTR, bool BSTR>
 __global__ __launch_bounds__(64 * WGM * WGN, OCC) void gemm_kernel(const GemmArgs g)
 {
     constexpr int NW = WGM * WGN;
     constexpr int ES = sizeof(T);
-    constexpr int H = SB / 64;                  // halves of a stage, one matrix instruction deep each
+    constexpr int SB = kStageBytes;
     constexpr int BKE = SB / ES;                // inner elements per stage
     constexpr int RPB = 1024 / SB;              // rows-form rows per 1 KiB block
     constexpr int AL = TM / (NW * RPB), BL = TN / (NW * RPB), LPS = AL + BL;
@@ -108,13 +240,13 @@ __global__ __launch_bounds__(64 * WGM * WGN, OCC) void gemm_kernel(const GemmArg
     static_assert(AL >= 1 && BL >= 1 && FM >= 2 && FN >= 2, "tile too small");
     static_assert(NSB >= 2 && (NSA == NSB || (NSA == 3 && NSB == 2)), "ring slots");
     static_assert((NSA - 1) * AL + (NSB - 1) * BL < 64, "pipeline depth");
-    static_assert(LH <= LPS && (H > 1 || LH == LPS), "loads of a stage");
+    static_assert(LH <= LPS, "loads of a stage");
     constexpr int RING = NSA * A_BYTES + NSB * B_BYTES, A_RING = NSA * A_BYTES;
     static_assert(!(ASTR || BSTR) || ES == 2, "transposing reads take 16-bit values");
 
-    // epilogue slab of one wave: 32 rows of WN values, padded by 4
+    // epilogue slab of one wave: up to 64 rows of WN values, padded by 4
     constexpr int SP = WN + 4;
-    constexpr int SLAB = 32 * SP * 4;
+    constexpr int SLAB = (WM < 64 ? WM : 64) * SP * 4;
     constexpr int LDS_BYTES = RING > NW * SLAB ? RING : NW * SLAB;
     __shared__ __attribute__((aligned(1024))) uint8_t smem[LDS_BYTES];
 
@@ -140,9 +272,17 @@ __global__ __launch_bounds__(64 * WGM * WGN, OCC) void gemm_kernel(const GemmArg
     // i*NW+wave of its operand's part of the stage
     const int row0 = wave * RPB + lane / (SB / 16);
     const int j = row_swizzle<SB>(row0, lane % (SB / 16));  // the same for every i
-    auto rows_off = [&](int i, int first, int dim, int64_t ld) {
+    auto a_rows_off = [&](int i) {
         const int r = row0 + i * NW * RPB;
-        return first + r < dim ? r * (int)ld + j * 16 : kOutOfRange;
+        return m0 + r < g.M ? r * (int)g.lda + j * 16 : kOutOfRange;
+    };
+    auto b_slot_of = [&](int i) {               // row * 8 + chunk that belongs at this lane's place
+        const int pair = (i * NW + wave) * (RPB / 2) + (lane >> 4);
+        return pair * 16 + pair_swizzle<FN>(pair, lane & 15);
+    };
+    auto b_rows_off = [&](int i) {
+        const int rc = b_slot_of(i), r = rc >> 3;
+        return n0 + r < g.N ? r * (int)g.ldb + (rc & 7) * 16 : kOutOfRange;
     };
     auto cols_off = [&](auto td, int i, int first, int dim, int64_t ld) {
         constexpr int TD = decltype(td)::value;
@@ -156,10 +296,10 @@ __global__ __launch_bounds__(64 * WGM * WGN, OCC) void gemm_kernel(const GemmArg
     int a_off[AL], b_off[BL];
 #pragma unroll
     for (int i = 0; i < AL; ++i)
-        a_off[i] = ASTR ? cols_off(TMc{}, i, m0, g.M, g.lda) : rows_off(i, m0, g.M, g.lda);
+        a_off[i] = ASTR ? cols_off(TMc{}, i, m0, g.M, g.lda) : a_rows_off(i);
 #pragma unroll
     for (int i = 0; i < BL; ++i)
-        b_off[i] = BSTR ? cols_off(TNc{}, i, n0, g.N, g.ldb) : rows_off(i, n0, g.N, g.ldb);
+        b_off[i] = BSTR ? cols_off(TNc{}, i, n0, g.N, g.ldb) : b_rows_off(i);
 
     // The operands' streams: buffer resource and ring slot of the next stage to
     // load.  `full` is the range of a whole stage: without limit in rows form
@@ -202,10 +342,9 @@ __global__ __launch_bounds__(64 * WGM * WGN, OCC) void gemm_kernel(const GemmArg
             if constexpr (BSTR) {
                 b_rsrc.z = b_next < stage_end ? (tail_k - 1) * (int)g.ldb + b_cols : 0;
             } else {
-                const bool in = b_next * SB + j * 16 < g.kbytes;
 #pragma unroll
                 for (int i = 0; i < BL; ++i)
-                    b_off[i] = in ? b_off[i] : kOutOfRange;
+                    b_off[i] = b_next * SB + (b_slot_of(i) & 7) * 16 < g.kbytes ? b_off[i] : kOutOfRange;
             }
         }
     };
@@ -258,6 +397,10 @@ __global__ __launch_bounds__(64 * WGM * WGN, OCC) void gemm_kernel(const GemmArg
         const int row = first + (lane & 15);
         return *(const v4i *)&base[row * SB + row_swizzle<SB>(row, half * 4 + (lane >> 4)) * 16];
     };
+    auto read_b_rows = [&](const uint8_t *base, int y, int half) {
+        const int row = wn + (lane & 15) * FN + y;
+        return *(const v4i *)&base[(row >> 1) * 256 + pair_swizzle<FN>(row >> 1, (row & 1) * 8 + half * 4 + (lane >> 4)) * 16];
+    };
     auto read_cols = [&](auto td, const uint8_t *base, int first, int half) {
         constexpr int TD = decltype(td)::value;
         const int jj = lane & 15;
@@ -277,7 +420,7 @@ __global__ __launch_bounds__(64 * WGM * WGN, OCC) void gemm_kernel(const GemmArg
             if constexpr (BSTR)
                 frag[buf][i] = read_cols(TNc{}, base, wn + i * 16, half);
             else
-                frag[buf][i] = read_rows(base, wn + i * 16, half);
+                frag[buf][i] = read_b_rows(base, i, half);
         } else {
             const uint8_t *base = smem + a_slot * A_BYTES;
             if constexpr (ASTR)
@@ -286,9 +429,16 @@ __global__ __launch_bounds__(64 * WGM * WGN, OCC) void gemm_kernel(const GemmArg
                 frag[buf][i] = read_rows(base, wm + (i - FN) * 16, half);
         }
     };
-    auto mfma_one = [&](int buf, int i) {
-        const int x = i / FN, y = i % FN;
-        mfma16_acc<T>(frag[buf][y], frag[buf][FN + x], acc[x][y]);
+    // A wave of the 256x256 tile has 256 sums, all the accumulation registers there
+    // are; one row of blocks is kept in ordinary ones, since with none to spare the
+    // allocator moves sums about inside the loop.
+    auto mfma_one = [&](int buf, auto ic) __attribute__((always_inline)) {
+        constexpr int x = decltype(ic)::value / FN, y = decltype(ic)::value % FN;
+        constexpr bool vgpr = FM * FN == 64 && x == FM - 1;
+        if constexpr (BSTR)
+            mfma16_acc<T, vgpr>(frag[buf][y], frag[buf][FN + x], acc[x][y]);
+        else
+            mfma16_acc<T, vgpr>(frag[buf][FN + x], frag[buf][y], acc[x][y]);
     };
 
     // A half: its matrix instructions (fragments in registers `buf`) with the
@@ -307,12 +457,12 @@ __global__ __launch_bounds__(64 * WGM * WGN, OCC) void gemm_kernel(const GemmArg
     // different gaps.
     constexpr int PRE = NMF / 4;
     int a_slot = 0, b_slot = 0;
-    auto half = [&](auto bufc, auto hc) __attribute__((always_inline)) {
-        constexpr int buf = decltype(bufc)::value, h = decltype(hc)::value;
-        constexpr bool last = h == H - 1;
+    auto half = [&](auto hc) __attribute__((always_inline)) {
+        constexpr int h = decltype(hc)::value, buf = h;
+        constexpr bool last = h == 1;
         constexpr int first = last ? PRE : 0;   // matrix instructions before reads may start
         constexpr int np = NMF - first, nr = np * 3 / 4 > 0 ? np * 3 / 4 : 1;
-        constexpr int l0 = last ? 0 : LH, nl = last ? LH : h == 0 ? LPS - LH : 0;
+        constexpr int l0 = last ? 0 : LH, nl = last ? LH : LPS - LH;
         const int an = a_slot + 1 == NSA ? 0 : a_slot + 1, bn = b_slot + 1 == NSB ? 0 : b_slot + 1;
         for_each<NMF>([&](auto ic) __attribute__((always_inline)) {
             constexpr int i = decltype(ic)::value;
@@ -321,7 +471,7 @@ __global__ __launch_bounds__(64 * WGM * WGN, OCC) void gemm_kernel(const GemmArg
                 __builtin_amdgcn_s_barrier();
                 __builtin_amdgcn_sched_barrier(0);
             }
-            mfma_one(buf, i);
+            mfma_one(buf, ic);
             if constexpr (last && i < PRE) {
                 // the stage whose loads start after the barrier
                 constexpr int step = PRE / 6 > 0 ? PRE / 6 : 1;
@@ -363,9 +513,7 @@ __global__ __launch_bounds__(64 * WGM * WGN, OCC) void gemm_kernel(const GemmArg
         }
     };
 
-    // Fragment buffers alternate by half.  With one half per stage the loop
-    // body holds two stages, and an odd count runs an extra stage of zeros.
-    const int nloop = H == 1 ? (max(stage_end - stage0, 0) + 1) & ~1 : max(stage_end - stage0, 0);
+    const int nloop = max(stage_end - stage0, 0);
     if (nloop > 0) {
         // The rings filled in the order of the loop: stage by stage, B before
         // A, and A's extra slot first of all
@@ -400,50 +548,89 @@ __global__ __launch_bounds__(64 * WGM * WGN, OCC) void gemm_kernel(const GemmArg
 #pragma unroll
         for (int i = 0; i < NRD; ++i)
             read_one(0, 0, 0, 0, i);
-        for (int it = 0; it < nloop; it += H == 1 ? 2 : 1) {
-            half(Size<0>{}, Size<0>{});
-            half(Size<1>{}, Size<H - 1>{});
+        for (int it = 0; it < nloop; ++it) {
+            half(Size<0>{});
+            half(Size<1>{});
         }
         wait_vm_lgkm0<0>();  // the trailing loads of zeros still write to the rings
         mfma_drain();
     }
     __syncthreads();
 
-    // ---- epilogue: 32-row slabs through the wave's own LDS -----------------
+    // ---- epilogue, whole tile, 16-bit output, B in rows form: straight from the
+    // accumulators, one piece of code per activation without branches inside
+    const Epilogue &e = g.epi;
+    if constexpr (!BSTR) {
+        // row strides that reach past a tile's 31-bit offsets take the other path
+        const bool whole = !g.part && m0 + TM <= g.M && n0 + TN <= g.N && e.tile_offsets;
+        if (whole && (ES == 2 ? e.out_dt == Code<T>::v : e.out_dt != DENSE_FP32)) {
+            auto run = [&](auto act, auto out) __attribute__((always_inline)) {
+                typedef typename decltype(out)::type O;
+                finish_whole<T, O, decltype(act)::value, FM, FN>(e, acc, m0 + wm, n0 + wn, lane);
+            };
+            auto by_act = [&](auto out) __attribute__((always_inline)) {
+                if (e.act == DENSE_ACT_NONE)
+                    run(Size<DENSE_ACT_NONE>{}, out);
+                else if (e.act == DENSE_ACT_RELU)
+                    run(Size<DENSE_ACT_RELU>{}, out);
+                else if (e.act == DENSE_ACT_GELU)
+                    run(Size<DENSE_ACT_GELU>{}, out);
+                else if (e.act == DENSE_ACT_GELU_TANH)
+                    run(Size<DENSE_ACT_GELU_TANH>{}, out);
+                else
+                    run(Size<DENSE_ACT_SILU>{}, out);
+            };
+            if constexpr (ES == 2) {
+                by_act(Type<T>{});
+            } else if (e.out_dt == DENSE_BF16) {
+                by_act(Type<bf16>{});
+            } else {
+                by_act(Type<f16>{});
+            }
+            return;
+        }
+    }
+
+    // ---- epilogue, anything else: the sums go to the wave's own part of LDS, up
+    // to 64 rows at a time, and one loop takes them from there row by row
     float *slab = (float *)(smem + wave * SLAB);
-    constexpr int CPR = WN / 8;                 // 8-column chunks per slab row
+    constexpr int CPR = WN / 8;                 // 8-column chunks per row
     static_assert(64 % CPR == 0, "a lane keeps its columns over all rows");
     const int cc = (lane % CPR) * 8;
     const int n = n0 + wn + cc;
     const int cnt = g.N - n;                    // columns of this chunk inside the matrix (8 or more: all)
     float bs[8], ws[8];
     if (!g.part && cnt > 0)
-        column_params(g.epi, n, cnt, bs, ws);
-    auto finish_slab = [&](auto xc) __attribute__((always_inline)) {
-        constexpr int x = decltype(xc)::value;
+        column_params(e, n, cnt, bs, ws);
+    for_each<(FM + 3) / 4>([&](auto sc) __attribute__((always_inline)) {
+        constexpr int x0 = decltype(sc)::value * 4, XS = FM - x0 < 4 ? FM - x0 : 4;
+        for_each<XS * FN>([&](auto bc) __attribute__((always_inline)) {
+            constexpr int x = decltype(bc)::value / FN, y = decltype(bc)::value % FN;
+            const typename Acc4<T>::type v = acc[x0 + x][y];
+            v4f o;
+            if constexpr (ES == 1)  // partial sums stay integers (their bits travel as floats)
+                o = g.part ? __builtin_bit_cast(v4f, v) : v4f{(float)v.x, (float)v.y, (float)v.z, (float)v.w};
+            else
+                o = v;
+            if constexpr (BSTR) {
+                *(v4f *)&slab[(x * 16 + (lane & 15)) * SP + y * 16 + 4 * (lane >> 4)] = o;
+            } else {
 #pragma unroll
-        for (int x2 = 0; x2 < 2; ++x2)
-#pragma unroll
-            for (int y = 0; y < FN; ++y) {
-                const typename Acc4<T>::type v = acc[2 * x + x2][y];
-                v4f o;
-                if constexpr (ES == 1)  // partial sums stay integers (their bits travel as floats)
-                    o = g.part ? __builtin_bit_cast(v4f, v) : v4f{(float)v.x, (float)v.y, (float)v.z, (float)v.w};
-                else
-                    o = v;
-                *(v4f *)&slab[(x2 * 16 + (lane & 15)) * SP + y * 16 + 4 * (lane >> 4)] = o;
+                for (int u = 0; u < 4; ++u)
+                    slab[(x * 16 + 4 * (lane >> 4) + u) * SP + (lane & 15) * FN + y] = o[u];
             }
+        });
         // one wave's LDS operations run in order: only the compiler must not
         // move the reads up
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
         __builtin_amdgcn_wave_barrier();
         __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
         constexpr int RS = 64 / CPR;            // rows apart of a lane's chunks
-        constexpr int ITS = 32 / RS, U = ITS < 4 ? ITS : 4;
+        constexpr int ITS = XS * 16 / RS, U = ITS < 4 ? ITS : 4;
 #pragma unroll 1
         for (int it = 0; it < ITS; it += U) {
             const int r = it * RS + lane / CPR;
-            const int m = m0 + wm + x * 32 + r;
+            const int m = m0 + wm + x0 * 16 + r;
             float v[U][8];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -461,21 +648,13 @@ __global__ __launch_bounds__(64 * WGM * WGN, OCC) void gemm_kernel(const GemmArg
                         *(v4f *)(p + 4) = *(v4f *)&v[u][4];
                     }
             } else {
-                finish8<ES == 1, U>(g.epi, m, RS, g.M, n, cnt, v, bs, ws);
+                finish<ES == 1, U, 8>(e, m, RS, g.M, n, cnt, v, bs, ws);
             }
         }
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
         __builtin_amdgcn_wave_barrier();
         __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-    };
-    static_assert(FM == 2 || FM == 4 || FM == 8, "slabs");
-    finish_slab(Size<0>{});
-    if constexpr (FM >= 4)
-        finish_slab(Size<1>{});
-    if constexpr (FM >= 8) {
-        finish_slab(Size<2>{});
-        finish_slab(Size<3>{});
-    }
+    });
 }
 
 // Sum of a split product's partial copies, in the order of the splits, and the
@@ -516,7 +695,7 @@ __global__ __launch_bounds__(256) void split_finish_kernel(const GemmArgs g, int
     }
     float bs[8], ws[8];
     column_params(g.epi, n, g.N - n, bs, ws);
-    finish8<INT, 1>(g.epi, m, 1, g.M, n, g.N - n, v, bs, ws);
+    finish<INT, 1>(g.epi, m, 1, g.M, n, g.N - n, v, bs, ws);
 }
 
 }  // namespace dense

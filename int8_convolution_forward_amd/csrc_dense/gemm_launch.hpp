@@ -8,17 +8,15 @@ namespace dense {
 
 struct Tile {
     int tm, tn;
-    int sb;           // bytes of the inner dimension per stage
     int occ;          // workgroups per CU
     const char *name;
 };
 
-constexpr int kTiles = 4;
+constexpr int kTiles = 3;
 constexpr Tile kTile[kTiles] = {
-    {256, 256, 128, 1, "256x256"},
-    {256, 128, 64, 2, "256x128"},
-    {128, 128, 128, 2, "128x128"},
-    {64, 64, 128, 3, "64x64"},
+    {256, 256, 1, "256x256"},
+    {128, 128, 2, "128x128"},
+    {64, 64, 3, "64x64"},
 };
 
 // One launch of tile `tile` with the operands in rows or columns form (INT8:
@@ -32,10 +30,9 @@ bool launch_gemm_form(int tile, const GemmArgs &g, int splits, hipStream_t strea
 {
     const dim3 grid((unsigned)g.tiles, (unsigned)splits), block(256);
     switch (tile) {
-    case 0: hipLaunchKernelGGL((gemm_kernel<T, 256, 256, 2, 2, 128, 3, 2, 7, 1, ASTR, BSTR>), grid, block, 0, stream, g); break;
-    case 1: hipLaunchKernelGGL((gemm_kernel<T, 256, 128, 2, 2, 64, 3, 3, 6, 2, ASTR, BSTR>), grid, block, 0, stream, g); break;
-    case 2: hipLaunchKernelGGL((gemm_kernel<T, 128, 128, 2, 2, 128, 2, 2, 6, 2, ASTR, BSTR>), grid, block, 0, stream, g); break;
-    case 3: hipLaunchKernelGGL((gemm_kernel<T, 64, 64, 2, 2, 128, 3, 3, 4, 3, ASTR, BSTR>), grid, block, 0, stream, g); break;
+    case 0: hipLaunchKernelGGL((gemm_kernel<T, 256, 256, 2, 2, 3, 2, 7, 1, ASTR, BSTR>), grid, block, 0, stream, g); break;
+    case 1: hipLaunchKernelGGL((gemm_kernel<T, 128, 128, 2, 2, 2, 2, 6, 2, ASTR, BSTR>), grid, block, 0, stream, g); break;
+    case 2: hipLaunchKernelGGL((gemm_kernel<T, 64, 64, 2, 2, 3, 3, 4, 3, ASTR, BSTR>), grid, block, 0, stream, g); break;
     default: return false;
     }
     return hipGetLastError() == hipSuccess;

@@ -68,7 +68,7 @@ __global__ __launch_bounds__(norm_threads(P)) void norm_kernel(const NormArgs a)
     float v[V][8];
 #pragma unroll
     for (int i = 0; i < V; ++i)
-        load8n(x + (i * P + t) * 8, a.D - (i * P + t) * 8, v[i]);
+        load_n(x + (i * P + t) * 8, a.D - (i * P + t) * 8, v[i]);
 
     float s = 0.0f;
 #pragma unroll
@@ -108,9 +108,9 @@ __global__ __launch_bounds__(norm_threads(P)) void norm_kernel(const NormArgs a)
             b[k] = 0.0f;
         }
         if (a.weight)
-            load8n((const T *)a.weight + c, cnt, w);
+            load_n((const T *)a.weight + c, cnt, w);
         if (a.bias)
-            load8n((const T *)a.bias + c, cnt, b);
+            load_n((const T *)a.bias + c, cnt, b);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             v[i][k] = __builtin_fmaf(v[i][k] * rstd, w[k], b[k]);
@@ -121,7 +121,7 @@ __global__ __launch_bounds__(norm_threads(P)) void norm_kernel(const NormArgs a)
             }
         }
         if constexpr (!Q8)
-            store8n((T *)a.y + m * a.ldy + c, cnt, v[i]);
+            store_n((T *)a.y + m * a.ldy + c, cnt, v[i]);
     }
     if constexpr (Q8) {
         float inv;
@@ -162,7 +162,7 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(const NormArgs a)
     float s = 0.0f;
     for (int64_t c = t * 8; c < a.D; c += 8192) {
         float v[8];
-        load8n(x + c, (int)(a.D - c), v);
+        load_n(x + c, (int)(a.D - c), v);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
             s += v[k];
@@ -171,7 +171,7 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(const NormArgs a)
     s = 0.0f;
     for (int64_t c = t * 8; c < a.D; c += 8192) {
         float v[8];
-        load8n(x + c, (int)(a.D - c), v, mean);
+        load_n(x + c, (int)(a.D - c), v, mean);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
             s = __builtin_fmaf(v[k] - mean, v[k] - mean, s);
@@ -190,11 +190,11 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(const NormArgs a)
             w[k] = 1.0f;
             b[k] = 0.0f;
         }
-        load8n(x + c, cnt, v);
+        load_n(x + c, cnt, v);
         if (a.weight)
-            load8n((const T *)a.weight + c, cnt, w);
+            load_n((const T *)a.weight + c, cnt, w);
         if (a.bias)
-            load8n((const T *)a.bias + c, cnt, b);
+            load_n((const T *)a.bias + c, cnt, b);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
             v[k] = __builtin_fmaf((v[k] - mean) * rstd, w[k], b[k]);
@@ -213,7 +213,7 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(const NormArgs a)
                 nan |= u != u;
             }
         } else {
-            store8n((T *)a.y + m * a.ldy + c, cnt, v);
+            store_n((T *)a.y + m * a.ldy + c, cnt, v);
         }
     }
     if constexpr (Q8) {
@@ -260,7 +260,7 @@ __global__ __launch_bounds__(norm_threads(P)) void norm_backward_kernel(const No
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         if (a.weight) {
-            load8n((const T *)a.weight + (i * P + t) * 8, a.D - (i * P + t) * 8, w[i]);
+            load_n((const T *)a.weight + (i * P + t) * 8, a.D - (i * P + t) * 8, w[i]);
         } else {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
@@ -281,8 +281,8 @@ __global__ __launch_bounds__(norm_threads(P)) void norm_backward_kernel(const No
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int c = (i * P + t) * 8;
-            load8n((const T *)a.x + m * a.ldx + c, a.D - c, xh[i]);
-            load8n((const T *)a.dy + m * a.lddy + c, a.D - c, dy[i]);
+            load_n((const T *)a.x + m * a.ldx + c, a.D - c, xh[i]);
+            load_n((const T *)a.dy + m * a.lddy + c, a.D - c, dy[i]);
         }
         float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
@@ -324,7 +324,7 @@ __global__ __launch_bounds__(norm_threads(P)) void norm_backward_kernel(const No
 #pragma unroll
             for (int k = 0; k < 8; ++k)
                 o[k] = rstd * (dy[i][k] * w[i][k] - s1 - xh[i][k] * s2);
-            store8n((T *)a.dx + m * a.lddx + c, a.D - c, o);
+            store_n((T *)a.dx + m * a.lddx + c, a.D - c, o);
         }
     }
     if constexpr (SUMS) {
@@ -357,8 +357,8 @@ __global__ __launch_bounds__(norm_threads(P)) void norm_backward_kernel(const No
             for (int i = 0; i < V; ++i) {
                 const int c = (i * P + t) * 8;
                 float *p = a.part + (int64_t)blockIdx.x * 2 * a.part_ld + c;
-                store8n(p, a.D - c, sw[i]);
-                store8n(p + a.part_ld, a.D - c, sb[i]);
+                store_n(p, a.D - c, sw[i]);
+                store_n(p + a.part_ld, a.D - c, sb[i]);
             }
         }
     }
@@ -375,13 +375,13 @@ __global__ __launch_bounds__(1024) void norm_backward_long_kernel(const NormBack
     const float mean = a.mean[m], rstd = a.rstd[m];
     auto load = [&](int64_t c, int cnt, float (&xh)[8], float (&cv)[8]) {
         float w[8];
-        load8n(x + c, cnt, xh, mean);
-        load8n(g + c, cnt, cv);
+        load_n(x + c, cnt, xh, mean);
+        load_n(g + c, cnt, cv);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
             w[k] = 1.0f;
         if (a.weight)
-            load8n((const T *)a.weight + c, cnt, w);
+            load_n((const T *)a.weight + c, cnt, w);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             xh[k] = (xh[k] - mean) * rstd;
@@ -406,7 +406,7 @@ __global__ __launch_bounds__(1024) void norm_backward_long_kernel(const NormBack
 #pragma unroll
         for (int k = 0; k < 8; ++k)
             cv[k] = rstd * (cv[k] - s1 - xh[k] * s2);
-        store8n((T *)a.dx + m * a.lddx + c, (int)(a.D - c), cv);
+        store_n((T *)a.dx + m * a.lddx + c, (int)(a.D - c), cv);
     }
 }
 
@@ -423,8 +423,8 @@ __global__ __launch_bounds__(256) void norm_backward_sums_kernel(const NormBackA
     for (int64_t m = (int64_t)blockIdx.y * rows; m < m1; ++m) {
         const float mean = a.mean[m], rstd = a.rstd[m];
         float xv[8], g[8];
-        load8n((const T *)a.x + m * a.ldx + c, cnt, xv);
-        load8n((const T *)a.dy + m * a.lddy + c, cnt, g);
+        load_n((const T *)a.x + m * a.ldx + c, cnt, xv);
+        load_n((const T *)a.dy + m * a.lddy + c, cnt, g);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             sw[k] = __builtin_fmaf(g[k], (xv[k] - mean) * rstd, sw[k]);
@@ -432,8 +432,8 @@ __global__ __launch_bounds__(256) void norm_backward_sums_kernel(const NormBackA
         }
     }
     float *p = a.part + (int64_t)blockIdx.y * 2 * a.part_ld + c;
-    store8n(p, cnt, sw);
-    store8n(p + a.part_ld, cnt, sb);
+    store_n(p, cnt, sw);
+    store_n(p + a.part_ld, cnt, sb);
 }
 
 }  // namespace dense

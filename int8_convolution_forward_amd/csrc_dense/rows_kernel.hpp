@@ -80,16 +80,16 @@ __global__ __launch_bounds__(256) void act_grad_kernel(const ActGradArgs a)
 #pragma unroll 4
         for (int m = m0 + wave; m < m1; m += 4) {
             float v[8];
-            load8n((const T *)a.dy + m * a.ldy + n, cnt, v);
+            load_n((const T *)a.dy + m * a.ldy + n, cnt, v);
             if constexpr (ACT != DENSE_ACT_NONE) {
                 float z[8];
-                load8n((const T *)a.z + m * a.ldz + n, cnt, z);
+                load_n((const T *)a.z + m * a.ldz + n, cnt, z);
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     v[i] *= act_slope<ACT>(z[i]);
             }
             if (a.g)
-                store8((T *)a.g + m * a.ldg + n, v);
+                store_all((T *)a.g + m * a.ldg + n, v);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 sum[i] += v[i];
