@@ -55,6 +55,55 @@ __device__ __forceinline__ void load_all(const T *p, float (&v)[C])
         v[i] = (float)q.e[i];
 }
 
+// Eight values as they lie in memory, so that what is on its way takes the
+// registers of its type and not of 32-bit values.
+template <typename T>
+struct Raw8 {
+    v4i w[sizeof(T) / 2];
+};
+
+// Values c .. c+7 of a row of D >= 8.  Past the end, and for a partial group, it
+// reads the last eight of the row, which widen_part puts in their place: a load
+// has no condition per lane, so nothing waits for it before it is used.
+template <typename T>
+__device__ __forceinline__ Raw8<T> load_raw(const T *row, int c, int D)
+{
+    return __builtin_bit_cast(Raw8<T>, *(const Pack<T, 8> *)(row + min(c, D - 8)));
+}
+
+template <typename T>
+__device__ __forceinline__ void widen(const Raw8<T> &r, float (&v)[8])
+{
+    typedef T vec __attribute__((ext_vector_type(8)));
+    const vec q = __builtin_bit_cast(vec, r);
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        v[k] = (float)q[k];
+}
+
+// The same where only D - c of the values may exist: the others become zero.
+// TAIL: D may be other than a multiple of eight.
+template <bool TAIL, typename T>
+__device__ __forceinline__ void widen_part(const Raw8<T> &r, int c, int D, float (&v)[8])
+{
+    widen(r, v);
+    const int n = D - c;
+    if constexpr (TAIL) {
+        if (n < 8) {
+            asm volatile("");  // keeps the branch: as selects, every lane would pay for them
+            const int by = 8 - n;  // down by so many places
+#pragma unroll
+            for (int b = 4; b >= 1; b >>= 1)
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    v[k] = by & b ? (k + b < 8 ? v[k + b] : 0.0f) : v[k];
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        v[k] = n > 0 ? v[k] : 0.0f;
+}
+
 template <typename T, int C>
 __device__ __forceinline__ void store_all(T *p, const float (&v)[C])
 {
@@ -170,13 +219,17 @@ __device__ __forceinline__ float sigmoid(float x)
 
 constexpr float kGeluC = 0.797884560802865f;   // sqrt(2/pi)
 constexpr float kGeluA = 0.044715f;
+constexpr float kGeluE1 = -2.302208198144325f;  // -2 sqrt(2/pi) log2 e
+constexpr float kGeluE3 = -0.102943239579983f;  // kGeluA times it
 constexpr float kSqrtHalf = 0.707106781186548f;
 constexpr float kInvSqrt2Pi = 0.398942280401433f;
 
 // 0.5 (1 + tanh u) = sigmoid(2u), so the tanh form of gelu is z sigmoid(2u).
-__device__ __forceinline__ float gelu_tanh_gate(float z)
+// z2 is z^2; the constants of u and of the exponential are one, because the
+// epilogue's arithmetic is not hidden by anything (7 operations a value).
+__device__ __forceinline__ float gelu_tanh_gate(float z, float z2)
 {
-    return sigmoid(2.0f * kGeluC * (z + kGeluA * z * z * z));
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * __builtin_fmaf(z2, kGeluE3, kGeluE1)));
 }
 
 // Normal distribution function through erfc, which keeps its relative
@@ -194,7 +247,7 @@ __device__ __forceinline__ float activate(float z)
     else if constexpr (ACT == DENSE_ACT_GELU)
         return z * normal_cdf(z);
     else if constexpr (ACT == DENSE_ACT_GELU_TANH)
-        return z * gelu_tanh_gate(z);
+        return z * gelu_tanh_gate(z, z * z);
     else if constexpr (ACT == DENSE_ACT_SILU)
         return z * sigmoid(z);
     else
@@ -211,9 +264,9 @@ __device__ __forceinline__ float act_slope(float z)
     } else if constexpr (ACT == DENSE_ACT_GELU_TANH) {
         // p + z p (1 - p) 2u'(z); z^2 is bounded where p (1 - p) is already 0,
         // so that it cannot overflow against it
-        const float p = gelu_tanh_gate(z);
         const float z2 = fminf(z * z, 1.0e4f);
-        return p + z * p * (1.0f - p) * (2.0f * kGeluC) * (1.0f + 3.0f * kGeluA * z2);
+        const float p = gelu_tanh_gate(z, z2);
+        return __builtin_fmaf(z * p * (1.0f - p), __builtin_fmaf(z2, 6.0f * kGeluC * kGeluA, 2.0f * kGeluC), p);
     } else if constexpr (ACT == DENSE_ACT_SILU) {
         const float p = sigmoid(z);
         return p * (1.0f + z * (1.0f - p));

@@ -12,6 +12,8 @@ constexpr int64_t kWsAlign = 256;
 // Longest row that stays in registers, forward and backward.
 constexpr int64_t kNormRow = 65536;
 constexpr int64_t kBackRow = 16384;
+// Rows outside these, or of fewer than eight columns, are read again for each step.
+inline bool back_in_registers(int64_t D) { return D >= 8 && D <= kBackRow; }
 
 conv_i8_status_t check_stat(dense_vec_t *v, int64_t n)
 {
@@ -50,11 +52,23 @@ conv_i8_status_t analyze(const dense_layer_norm_t *args, dense_layer_norm_t *d)
     return CONV_I8_OK;
 }
 
+// Two rows for each thread group once there are more than 1024 workgroups: the
+// second one's loads then overlap the first one's work, and the card still
+// balances itself (16384 x 4096 BF16: 48.6 us, one row each 55.9, sixteen 52.3).
+// Wide groups (512 threads) hold fewer workgroups on a CU and take more rows.
 template <typename T, int P, int V, bool Q8>
 void launch_one(const NormArgs &a, hipStream_t s)
 {
     constexpr int rows = norm_threads(P) / P;
-    hipLaunchKernelGGL((norm_kernel<T, P, V, Q8>), dim3((unsigned)ceil_div(a.M, rows)), dim3(norm_threads(P)), 0, s, a);
+    constexpr bool hold = P <= 512;
+    int64_t wgs = ceil_div(a.M, rows);
+    if (hold && wgs > 1024)
+        wgs = P > 256 || wgs <= 2048 ? 1024 : ceil_div(wgs, 2);
+    const dim3 grid((unsigned)wgs), block(norm_threads(P));
+    if (a.D % 8 == 0)
+        hipLaunchKernelGGL((norm_kernel<T, P, V, hold, false, Q8>), grid, block, 0, s, a);
+    else
+        hipLaunchKernelGGL((norm_kernel<T, P, V, hold, true, Q8>), grid, block, 0, s, a);
 }
 
 template <typename T, bool Q8>
@@ -63,7 +77,9 @@ void launch_norm(const NormArgs &a, hipStream_t s)
     const int D = a.D;
     // a wave per row while that gives each CU a few waves, else a workgroup per row
     const bool few = a.M < 4 * kCUs;
-    if (D <= 512)
+    if (D < 8 || D > kNormRow)
+        hipLaunchKernelGGL((norm_long_kernel<T, Q8>), dim3((unsigned)a.M), dim3(1024), 0, s, a);
+    else if (D <= 512)
         launch_one<T, 64, 1, Q8>(a, s);
     else if (D <= 1024 && !few)
         launch_one<T, 64, 2, Q8>(a, s);
@@ -74,11 +90,9 @@ void launch_norm(const NormArgs &a, hipStream_t s)
     else if (D <= 8192)
         launch_one<T, 256, 4, Q8>(a, s);
     else if (D <= 16384)
-        launch_one<T, 1024, 2, Q8>(a, s);
-    else if (D <= kNormRow)
-        launch_one<T, 1024, 8, Q8>(a, s);
+        launch_one<T, 512, 4, Q8>(a, s);
     else
-        hipLaunchKernelGGL((norm_long_kernel<T, Q8>), dim3((unsigned)a.M), dim3(1024), 0, s, a);
+        launch_one<T, 1024, 8, Q8>(a, s);
 }
 
 struct BackPlan {
@@ -89,7 +103,7 @@ struct BackPlan {
     int64_t part_ld = 0, ws_bytes = 0;
 };
 
-constexpr int back_threads(int64_t D) { return D <= 512 ? 64 : D <= 8192 ? 256 : 1024; }
+constexpr int back_threads(int64_t D) { return D <= 512 ? 64 : D <= 4096 ? 256 : D <= 8192 ? 512 : 1024; }
 
 conv_i8_status_t analyze(const dense_layer_norm_backward_t *args, BackPlan *p)
 {
@@ -125,47 +139,52 @@ conv_i8_status_t analyze(const dense_layer_norm_backward_t *args, BackPlan *p)
         return CONV_I8_ERR_PARAM;
     p->sums = d.dweight.dtype != DENSE_NONE;
     p->part_ld = round_up(p->D, 8);
-    if (p->D > kBackRow) {
+    if (!back_in_registers(p->D)) {
         const int64_t blocks = p->M < 64 ? p->M : 64;
         p->wgs = (int)(p->M > 0 ? ceil_div(p->M, ceil_div(p->M, blocks)) : 0);
     } else {
-        // two workgroups a CU, and at least four rows for each group of threads
-        const int rows = norm_threads(back_threads(p->D)) / back_threads(p->D);
+        // eight waves or more on a CU, and at least four rows for each group of threads
+        const int threads = norm_threads(back_threads(p->D));
+        const int rows = threads / back_threads(p->D), most = threads <= 256 ? 2 * kCUs : kCUs;
         const int64_t want = ceil_div(p->M, 4 * rows);
-        p->wgs = (int)(want < 2 * kCUs ? want : 2 * kCUs);
+        p->wgs = (int)(want < most ? want : most);
     }
     p->ws_bytes = p->sums ? round_up((int64_t)p->wgs * 2 * p->part_ld * 4, kWsAlign) : 0;
     return CONV_I8_OK;
 }
 
-template <typename T, int P, int V>
+template <typename T, int P, int V, int AHEAD>
 void launch_back_one(const NormBackArgs &a, int wgs, hipStream_t s)
 {
-    if (a.part)
-        hipLaunchKernelGGL((norm_backward_kernel<T, P, V, true>), dim3((unsigned)wgs), dim3(norm_threads(P)), 0, s, a);
+    const dim3 grid((unsigned)wgs), block(norm_threads(P));
+    auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, s, a); };
+    if (a.D % 8 == 0)
+        a.part ? launch(norm_backward_kernel<T, P, V, AHEAD, false, true>)
+               : launch(norm_backward_kernel<T, P, V, AHEAD, false, false>);
     else
-        hipLaunchKernelGGL((norm_backward_kernel<T, P, V, false>), dim3((unsigned)wgs), dim3(norm_threads(P)), 0, s, a);
+        a.part ? launch(norm_backward_kernel<T, P, V, AHEAD, true, true>)
+               : launch(norm_backward_kernel<T, P, V, AHEAD, true, false>);
 }
 
 template <typename T>
 void launch_back(const NormBackArgs &a, int wgs, hipStream_t s)
 {
     const int D = a.D;
-    if (D <= 512)
-        launch_back_one<T, 64, 1>(a, wgs, s);
-    else if (D <= 2048)
-        launch_back_one<T, 256, 1>(a, wgs, s);
-    else if (D <= 4096)
-        launch_back_one<T, 256, 2>(a, wgs, s);
-    else if (D <= 8192)
-        launch_back_one<T, 256, 4>(a, wgs, s);
-    else if (D <= kBackRow)
-        launch_back_one<T, 1024, 2>(a, wgs, s);
-    else {
+    if (!back_in_registers(D)) {
         hipLaunchKernelGGL(norm_backward_long_kernel<T>, dim3((unsigned)a.M), dim3(1024), 0, s, a);
         if (a.part)
             hipLaunchKernelGGL(norm_backward_sums_kernel<T>, dim3((unsigned)ceil_div(D, 2048), (unsigned)wgs), dim3(256),
                                0, s, a, (int)ceil_div(a.M, wgs));
+    } else if (D <= 512) {
+        launch_back_one<T, 64, 1, 1>(a, wgs, s);
+    } else if (D <= 2048) {
+        launch_back_one<T, 256, 1, 1>(a, wgs, s);
+    } else if (D <= 4096) {
+        launch_back_one<T, 256, 2, 1>(a, wgs, s);
+    } else if (D <= 8192) {
+        launch_back_one<T, 512, 2, 1>(a, wgs, s);
+    } else {
+        launch_back_one<T, 1024, 2, 0>(a, wgs, s);
     }
 }
 

@@ -6,6 +6,14 @@
 // columns each, group v at columns (v P + thread) 8, so that every load of a
 // wave is one contiguous run.  With P = 64 a wave owns its row and the sums
 // need no barrier; wider rows, or few of them, take a workgroup per row.
+//
+// What they need is bytes in flight.  A thread group walks over rows and loads
+// the next one, in the form it has in memory, before it works on the present
+// one, and a load has no condition per lane (TAIL: D is no multiple of eight).
+// 16384 x 4096
+// BF16: forward 50 us (5.3 TB/s; a copy of the same bytes reaches 5.9), with a
+// workgroup per row that loads, reduces and stores in turn 82; backward 76 us
+// (5.2 TB/s), without the next row's loads 133.
 #pragma once
 
 #include "dense_common.hpp"
@@ -51,107 +59,213 @@ __device__ __forceinline__ float quant_scale(float top, float &inv)
     return top < INFINITY ? top / 127.0f : __builtin_nanf("");
 }
 
+// columns of a row of D that wave `wave` of its P threads holds
+template <int P, int V>
+__device__ __forceinline__ int wave_columns(int D, int wave)
+{
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        n += min(max(D - (i * P + wave * 64) * 8, 0), 512);
+    return n;
+}
+
 // threads of a workgroup: at least 256, so that P = 64 packs four rows
 constexpr int norm_threads(int P) { return P < 256 ? 256 : P; }
 
-template <typename T, int P, int V, bool Q8>
-__global__ __launch_bounds__(norm_threads(P)) void norm_kernel(const NormArgs a)
+// Group i of a thread's part of a row, as it lies in memory.  Whether a group
+// can be partial does not depend on the thread.
+template <typename T, int P, int V>
+__device__ __forceinline__ void load_row(const T *p, int D, int t, Raw8<T> (&r)[V])
 {
-    constexpr int RPW = norm_threads(P) / P;  // rows per workgroup
-    __shared__ float red[3 * (P > 64 ? P / 64 : 1)];
-    const int t = threadIdx.x % P;
-    const int64_t m = (int64_t)blockIdx.x * RPW + threadIdx.x / P;
-    if (m >= a.M)
-        return;  // whole waves; with P > 64 there is one row per workgroup
-    const T *x = (const T *)a.x + m * a.ldx;
-
-    float v[V][8];
 #pragma unroll
     for (int i = 0; i < V; ++i)
-        load_n(x + (i * P + t) * 8, a.D - (i * P + t) * 8, v[i]);
+        r[i] = load_raw(p, (i * P + t) * 8, D);
+}
 
+template <bool TAIL, int P, typename T>
+__device__ __forceinline__ void widen_group(const Raw8<T> &r, int D, int i, int t, float (&v)[8])
+{
+    if ((i + 1) * P * 8 <= D)
+        widen(r, v);
+    else
+        widen_part<TAIL>(r, (i * P + t) * 8, D, v);
+}
+
+// The same of a row of weights, or `absent` everywhere where there are none
+template <typename T>
+__device__ __forceinline__ Raw8<T> load_param(const T *p, float absent, int c, int D)
+{
+    typedef T vec __attribute__((ext_vector_type(8)));
+    return p ? load_raw(p, c, D) : __builtin_bit_cast(Raw8<T>, (vec)(T)absent);
+}
+
+template <typename T, int P, int V>
+__device__ __forceinline__ void load_params(const T *p, float absent, int D, int t, Raw8<T> (&r)[V])
+{
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        r[i] = load_param(p, absent, (i * P + t) * 8, D);
+}
+
+// Mean and sum of squared distances from it, of a row held by P threads.  A
+// wave takes both of its own columns (cols of them), two passes over registers;
+// the waves' pairs are joined through LDS with one barrier:
+//   M2 = sum over waves of M2_w + n_w (mean_w - mean)^2
+template <int P, int V>
+__device__ __forceinline__ void row_moments(float (&v)[V][8], int D, int t, float cols, float d, float2 *red, float &mean,
+                                            float &m2)
+{
     float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
         for (int k = 0; k < 8; ++k)
             s += v[i][k];
-    const float mean = row_reduce<P>(s, red, 0) / a.d;
+    mean = wave_sum<64>(s) / cols;
     s = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int cnt = a.D - (i * P + t) * 8;
+        const int cnt = D - (i * P + t) * 8;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            v[i][k] = k < cnt ? v[i][k] - mean : 0.0f;
-            s = __builtin_fmaf(v[i][k], v[i][k], s);
+            const float c = v[i][k] - mean;
+            s = (i + 1) * P * 8 <= D || k < cnt ? __builtin_fmaf(c, c, s) : s;
         }
     }
-    const float rstd = 1.0f / sqrtf(row_reduce<P>(s, red, 1) / a.d + a.eps);
-    if (t == 0) {
-        if (a.mean)
-            a.mean[m] = mean;
-        if (a.rstd)
-            a.rstd[m] = rstd;
-    }
-    float top = 0.0f;
-    bool nan = false;
+    m2 = wave_sum<64>(s);
+    if constexpr (P > 64) {
+        constexpr int NW = P / 64;
+        if ((threadIdx.x & 63) == 0)
+            red[threadIdx.x >> 6] = make_float2(mean, m2);
+        __syncthreads();
+        float2 w[NW];
+        float n[NW];
+        s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int c = (i * P + t) * 8, cnt = a.D - c;
-        if (cnt <= 0)
-            continue;
-        float w[8], b[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            w[k] = 1.0f;
-            b[k] = 0.0f;
+        for (int i = 0; i < NW; ++i) {
+            w[i] = red[i];
+            n[i] = (float)wave_columns<P, V>(D, i);
+            if (n[i] > 0.0f)
+                s = __builtin_fmaf(n[i], w[i].x, s);
         }
-        if (a.weight)
-            load_n((const T *)a.weight + c, cnt, w);
-        if (a.bias)
-            load_n((const T *)a.bias + c, cnt, b);
+        mean = s / d;
+        m2 = 0.0f;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            v[i][k] = __builtin_fmaf(v[i][k] * rstd, w[k], b[k]);
-            if constexpr (Q8) {
-                const float u = k < cnt ? v[i][k] : 0.0f;
-                top = fmaxf(top, fabsf(u));
-                nan |= u != u;
+        for (int i = 0; i < NW; ++i)
+            if (n[i] > 0.0f) {
+                const float c = w[i].x - mean;
+                m2 += __builtin_fmaf(n[i] * c, c, w[i].y);
             }
-        }
-        if constexpr (!Q8)
-            store_n((T *)a.y + m * a.ldy + c, cnt, v[i]);
     }
-    if constexpr (Q8) {
-        float inv;
-        const float scale = quant_scale(row_reduce<P, true>(nan ? INFINITY : top, red, 2), inv);
-        if (t == 0)
-            a.scale[m] = scale;
+}
+
+// Rows walk over the grid: a thread group takes every gridDim-th one, with the
+// next row's loads in flight while it works on the present one and the weights
+// held over all of them (HOLD).  Workgroups of 1024 threads have 128 registers
+// each and do neither: 32 columns a thread would spill.
+template <typename T, int P, int V, bool HOLD, bool TAIL, bool Q8>
+__global__ __launch_bounds__(norm_threads(P)) void norm_kernel(const NormArgs a)
+{
+    constexpr int RPW = norm_threads(P) / P;  // rows per workgroup
+    constexpr int NW = P > 64 ? P / 64 : 1;
+    __shared__ float2 red[2][NW];
+    __shared__ float redq[2][NW];
+    const int t = threadIdx.x % P;
+    int64_t m = (int64_t)blockIdx.x * RPW + threadIdx.x / P;
+    if (m >= a.M)
+        return;  // whole waves; with P > 64 there is one row per workgroup
+    const int64_t step = (int64_t)gridDim.x * RPW;
+    const float cols = (float)wave_columns<P, V>(a.D, P > 64 ? threadIdx.x >> 6 : 0);
+
+    Raw8<T> row[V], w[V], b[V];
+    load_row<T, P, V>((const T *)a.x + m * a.ldx, a.D, t, row);
+    if constexpr (HOLD) {
+        load_params<T, P, V>((const T *)a.weight, 1.0f, a.D, t, w);
+        load_params<T, P, V>((const T *)a.bias, 0.0f, a.D, t, b);
+    }
+
+    int set = 0;
+    for (;;) {
+        float v[V][8];
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            widen_group<TAIL, P>(row[i], a.D, i, t, v[i]);
+        const int64_t next = m + step;
+        if (HOLD && next < a.M)
+            load_row<T, P, V>((const T *)a.x + next * a.ldx, a.D, t, row);
+        float mean, m2;
+        row_moments<P, V>(v, a.D, t, cols, a.d, red[set], mean, m2);
+        const float rstd = 1.0f / sqrtf(m2 / a.d + a.eps);
+        if (t == 0) {
+            if (a.mean)
+                a.mean[m] = mean;
+            if (a.rstd)
+                a.rstd[m] = rstd;
+        }
+        float top = 0.0f;
+        bool nan = false;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int c = (i * P + t) * 8, cnt = a.D - c;
-            if (cnt <= 0)
-                continue;
-            struct __attribute__((packed)) Q { int8_t e[8]; } q;
+            const bool whole = (i + 1) * P * 8 <= a.D;
+            float wv[8], bv[8];
+            if constexpr (!HOLD) {
+                w[i] = load_param((const T *)a.weight, 1.0f, c, a.D);
+                b[i] = load_param((const T *)a.bias, 0.0f, c, a.D);
+            }
+            widen_group<TAIL, P>(w[i], a.D, i, t, wv);
+            widen_group<TAIL, P>(b[i], a.D, i, t, bv);
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                q.e[k] = (int8_t)(int)__builtin_rintf(fminf(fmaxf(v[i][k] * inv, -127.0f), 127.0f));
-            int8_t *y = (int8_t *)a.y + m * a.ldy + c;
-            if (cnt >= 8) {
-                *(Q *)y = q;
-            } else {
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (k < cnt)
-                        y[k] = q.e[k];
+            for (int k = 0; k < 8; ++k) {
+                v[i][k] = __builtin_fmaf((v[i][k] - mean) * rstd, wv[k], bv[k]);
+                if constexpr (Q8) {
+                    const float u = whole || k < cnt ? v[i][k] : 0.0f;
+                    top = fmaxf(top, fabsf(u));
+                    nan |= u != u;
+                }
+            }
+            if constexpr (!Q8) {
+                T *y = (T *)a.y + m * a.ldy + c;
+                if (whole || (!TAIL && cnt > 0))
+                    store_all(y, v[i]);
+                else if constexpr (TAIL)
+                    store_n(y, cnt, v[i]);
             }
         }
+        if constexpr (Q8) {
+            float inv;
+            const float scale = quant_scale(row_reduce<P, true>(nan ? INFINITY : top, redq[set], 0), inv);
+            if (t == 0)
+                a.scale[m] = scale;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int c = (i * P + t) * 8, cnt = a.D - c;
+                const bool whole = (i + 1) * P * 8 <= a.D;
+                struct __attribute__((packed)) Q { int8_t e[8]; } q;
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    q.e[k] = (int8_t)(int)__builtin_rintf(fminf(fmaxf(v[i][k] * inv, -127.0f), 127.0f));
+                int8_t *y = (int8_t *)a.y + m * a.ldy + c;
+                if (whole || (TAIL ? cnt >= 8 : cnt > 0)) {
+                    *(Q *)y = q;
+                } else if constexpr (TAIL) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (k < cnt)
+                            y[k] = q.e[k];
+                }
+            }
+        }
+        if (!HOLD || next >= a.M)
+            break;
+        m = next;
+        set ^= 1;  // the other set: a slow wave may still read this one
     }
 }
 
 // Rows longer than the registers hold: the row is read again (from cache) for
-// each step.
+// each step.  Also rows of fewer than eight columns, which the loads above need.
 template <typename T, bool Q8>
 __global__ __launch_bounds__(1024) void norm_long_kernel(const NormArgs a)
 {
@@ -246,27 +360,22 @@ struct NormBackArgs {
 };
 
 // dx of one row after another, with the columns' sums of dy xh and dy kept in
-// registers over all rows of a thread and written once per workgroup.
-template <typename T, int P, int V, bool SUMS>
+// registers over all rows of a thread and written once per workgroup.  AHEAD
+// rows are in flight while one is worked on; with none (workgroups of 1024
+// threads, which have 128 registers each) the weights are read again for each
+// row too.
+template <typename T, int P, int V, int AHEAD, bool TAIL, bool SUMS>
 __global__ __launch_bounds__(norm_threads(P)) void norm_backward_kernel(const NormBackArgs a)
 {
     constexpr int RPW = norm_threads(P) / P;
     constexpr int NWR = P > 64 ? P / 64 : 1;
-    __shared__ float red[4 * NWR];
+    __shared__ float2 red[2][NWR];
     const int t = threadIdx.x % P;
     const int sub = threadIdx.x / P;
 
-    float w[V][8];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        if (a.weight) {
-            load_n((const T *)a.weight + (i * P + t) * 8, a.D - (i * P + t) * 8, w[i]);
-        } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                w[i][k] = 1.0f;
-        }
-    }
+    Raw8<T> w[V];
+    if constexpr (AHEAD > 0)
+        load_params<T, P, V>((const T *)a.weight, 1.0f, a.D, t, w);
     float sw[V][8], sb[V][8];
 #pragma unroll
     for (int i = 0; i < V; ++i)
@@ -274,44 +383,65 @@ __global__ __launch_bounds__(norm_threads(P)) void norm_backward_kernel(const No
         for (int k = 0; k < 8; ++k)
             sw[i][k] = sb[i][k] = 0.0f;
 
-    int set = 0;
-    for (int64_t m = (int64_t)blockIdx.x * RPW + sub; m < a.M; m += (int64_t)gridDim.x * RPW) {
-        const float mean = a.mean[m], rstd = a.rstd[m];
-        float xh[V][8], dy[V][8];
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int c = (i * P + t) * 8;
-            load_n((const T *)a.x + m * a.ldx + c, a.D - c, xh[i]);
-            load_n((const T *)a.dy + m * a.lddy + c, a.D - c, dy[i]);
+    struct Rows {
+        Raw8<T> x[V], dy[V];
+        float mean, rstd;
+    } ring[AHEAD > 0 ? AHEAD : 1];
+    const int64_t step = (int64_t)gridDim.x * RPW;
+    auto load = [&](int64_t m, Rows &r) __attribute__((always_inline)) {
+        if (m < a.M) {
+            load_row<T, P, V>((const T *)a.x + m * a.ldx, a.D, t, r.x);
+            load_row<T, P, V>((const T *)a.dy + m * a.lddy, a.D, t, r.dy);
+            r.mean = a.mean[m];
+            r.rstd = a.rstd[m];
         }
+    };
+    int64_t m = (int64_t)blockIdx.x * RPW + sub;
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+        load(m + i * step, ring[i]);
+
+    int set = 0;
+    auto work = [&](Rows &r) __attribute__((always_inline)) {
+        if constexpr (AHEAD == 0) {
+            load(m, r);
+            load_params<T, P, V>((const T *)a.weight, 1.0f, a.D, t, w);
+        }
+        const Rows cur = r;
+        const float mean = cur.mean, rstd = cur.rstd;
+        if constexpr (AHEAD > 0)
+            load(m + AHEAD * step, r);
+        float xh[V][8], c[V][8];
         float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
-        for (int i = 0; i < V; ++i)
+        for (int i = 0; i < V; ++i) {
+            float wv[8], dy[8];
+            widen_group<TAIL, P>(w[i], a.D, i, t, wv);
+            widen_group<TAIL, P>(cur.x[i], a.D, i, t, xh[i]);
+            widen_group<TAIL, P>(cur.dy[i], a.D, i, t, dy);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 xh[i][k] = (xh[i][k] - mean) * rstd;
-                const float c = dy[i][k] * w[i][k];
-                s1 += c;
-                s2 = __builtin_fmaf(c, xh[i][k], s2);
+                c[i][k] = dy[k] * wv[k];
+                s1 += c[i][k];
+                s2 = __builtin_fmaf(c[i][k], xh[i][k], s2);
                 if constexpr (SUMS) {
-                    sw[i][k] = __builtin_fmaf(dy[i][k], xh[i][k], sw[i][k]);
-                    sb[i][k] += dy[i][k];
+                    sw[i][k] = __builtin_fmaf(dy[k], xh[i][k], sw[i][k]);
+                    sb[i][k] += dy[k];
                 }
             }
+        }
         s1 = wave_sum<64>(s1);
         s2 = wave_sum<64>(s2);
         if constexpr (P > 64) {
-            float *r = red + set * 2 * NWR;
-            if ((threadIdx.x & 63) == 0) {
-                r[threadIdx.x >> 6] = s1;
-                r[NWR + (threadIdx.x >> 6)] = s2;
-            }
+            if ((threadIdx.x & 63) == 0)
+                red[set][threadIdx.x >> 6] = make_float2(s1, s2);
             __syncthreads();
             s1 = s2 = 0.0f;
 #pragma unroll
             for (int i = 0; i < NWR; ++i) {
-                s1 += r[i];
-                s2 += r[NWR + i];
+                s1 += red[set][i].x;
+                s2 += red[set][i].y;
             }
             set ^= 1;  // the other set: a slow wave may still read this one
         }
@@ -319,13 +449,25 @@ __global__ __launch_bounds__(norm_threads(P)) void norm_backward_kernel(const No
         s2 /= a.d;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int c = (i * P + t) * 8;
+            const int at = (i * P + t) * 8;
             float o[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-                o[k] = rstd * (dy[i][k] * w[i][k] - s1 - xh[i][k] * s2);
-            store_n((T *)a.dx + m * a.lddx + c, a.D - c, o);
+                o[k] = rstd * (c[i][k] - s1 - xh[i][k] * s2);
+            T *dx = (T *)a.dx + m * a.lddx + at;
+            if ((i + 1) * P * 8 <= a.D || (!TAIL && at < a.D))
+                store_all(dx, o);
+            else if constexpr (TAIL)
+                store_n(dx, a.D - at, o);
         }
+        m += step;
+    };
+    while (m < a.M) {
+        // m is the same for all of a workgroup where its threads share a row
+        for_each<(AHEAD > 0 ? AHEAD : 1)>([&](auto ic) __attribute__((always_inline)) {
+            if (m < a.M)
+                work(ring[decltype(ic)::value]);
+        });
     }
     if constexpr (SUMS) {
         if constexpr (RPW > 1) {

@@ -76,25 +76,71 @@ __global__ __launch_bounds__(256) void act_grad_kernel(const ActGradArgs a)
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         sum[i] = 0.0f;
-    if (cnt > 0) {
-#pragma unroll 4
-        for (int m = m0 + wave; m < m1; m += 4) {
-            float v[8];
-            load_n((const T *)a.dy + m * a.ldy + n, cnt, v);
+    // FORM 2: eight columns for every lane, 1: eight or none, 0: any number;
+    // -1: fewer than eight columns in all
+    auto some = [&](auto form, auto uc, int m) __attribute__((always_inline)) {
+        constexpr int FORM = decltype(form)::value, U = decltype(uc)::value;
+        float v[U][8];
+        if constexpr (FORM < 0) {
+            load_n((const T *)a.dy + m * a.ldy + n, cnt, v[0]);
             if constexpr (ACT != DENSE_ACT_NONE) {
                 float z[8];
                 load_n((const T *)a.z + m * a.ldz + n, cnt, z);
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    v[i] *= act_slope<ACT>(z[i]);
+                    v[0][i] *= act_slope<ACT>(z[i]);
             }
-            if (a.g)
-                store_all((T *)a.g + m * a.ldg + n, v);
+        } else {
+            Raw8<T> dy[U], z[U];
+            auto wide = [&](const Raw8<T> &r, float (&w)[8]) {
+                if constexpr (FORM == 2)
+                    widen(r, w);
+                else
+                    widen_part<FORM == 0>(r, n, a.N, w);
+            };
+#pragma unroll
+            for (int u = 0; u < U; ++u) {  // the loads of all rows go out together
+                dy[u] = load_raw((const T *)a.dy + (m + 4 * u) * a.ldy, n, a.N);
+                if constexpr (ACT != DENSE_ACT_NONE)
+                    z[u] = load_raw((const T *)a.z + (m + 4 * u) * a.ldz, n, a.N);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                wide(dy[u], v[u]);
+                if constexpr (ACT != DENSE_ACT_NONE) {
+                    float zv[8];
+                    wide(z[u], zv);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        v[u][i] *= act_slope<ACT>(zv[i]);
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (a.g && (FORM == 2 || cnt > 0))
+                store_all((T *)a.g + (m + 4 * u) * a.ldg + n, v[u]);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                sum[i] += v[i];
+                sum[i] += v[u][i];
         }
-    }
+    };
+    auto rows = [&](auto form) __attribute__((always_inline)) {
+        int m = m0 + wave;
+        if constexpr (decltype(form)::value >= 0)
+            for (; m + 12 < m1; m += 16)
+                some(form, Size<4>{}, m);
+        for (; m < m1; m += 4)
+            some(form, Size<1>{}, m);
+    };
+    if ((int)blockIdx.x * 512 + 512 <= a.N)
+        rows(Size<2>{});
+    else if (a.N % 8 == 0)
+        rows(Size<1>{});
+    else if (a.N > 8)
+        rows(Size<0>{});
+    else
+        rows(Size<-1>{});
     if (!a.colsum)
         return;
 #pragma unroll
