@@ -39,6 +39,7 @@
 // cannot give that order) turn through LDS.
 #pragma once
 
+#include "colsum.hpp"
 #include "dense_common.hpp"
 
 namespace dense {
@@ -221,19 +222,31 @@ __device__ __forceinline__ void finish_whole(const Epilogue &e, typename Acc4<T>
 
 // NSA, NSB: slots of the operands' rings, NSB or NSB + 1 and NSB; LH: loads per
 // thread of a stage that go out in the half that frees their slots (the others
-// in the half after it); OCC: workgroups a CU is to hold at a time (one wave of
-// each per SIMD)
-template <typename T, int TM, int TN, int WGM, int WGN, int NSA, int NSB, int LH, int OCC, bool ASTR, bool BSTR>
-__global__ __launch_bounds__(64 * WGM * WGN, OCC) void gemm_kernel(const GemmArgs g)
+// in the half after it)
+template <typename T, int TM, int TN, int WGM, int WGN, int NSA, int NSB, int LH, bool ASTR, bool BSTR>
+struct TileCfg {
+    static constexpr int NW = WGM * WGN;
+    static constexpr int RING = (NSA * TM + NSB * TN) * kStageBytes;
+    static constexpr int WM = TM / WGM, WN = TN / WGN;
+    // epilogue slab of one wave: up to 64 rows of WN values, padded by 4
+    static constexpr int SP = WN + 4;
+    static constexpr int SLAB = (WM < 64 ? WM : 64) * SP * 4;
+    static constexpr int LDS_BYTES = RING > NW * SLAB ? RING : NW * SLAB;
+};
+
+// One tile of one split.  smem: TileCfg::LDS_BYTES of LDS, aligned to 1024
+template <typename T, int TM, int TN, int WGM, int WGN, int NSA, int NSB, int LH, bool ASTR, bool BSTR>
+__device__ __forceinline__ void gemm_tile(const GemmArgs &g, uint8_t *smem, int block, int split)
 {
-    constexpr int NW = WGM * WGN;
+    typedef TileCfg<T, TM, TN, WGM, WGN, NSA, NSB, LH, ASTR, BSTR> Cfg;
+    constexpr int NW = Cfg::NW;
     constexpr int ES = sizeof(T);
     constexpr int SB = kStageBytes;
     constexpr int BKE = SB / ES;                // inner elements per stage
     constexpr int RPB = 1024 / SB;              // rows-form rows per 1 KiB block
     constexpr int AL = TM / (NW * RPB), BL = TN / (NW * RPB), LPS = AL + BL;
     constexpr int A_BYTES = TM * SB, B_BYTES = TN * SB;
-    constexpr int WM = TM / WGM, WN = TN / WGN;
+    constexpr int WM = Cfg::WM, WN = Cfg::WN;
     constexpr int FM = WM / 16, FN = WN / 16;
     constexpr int NMF = FM * FN;                // matrix instructions per half
     constexpr int NRD = FM + FN;                // fragment reads per half
@@ -241,14 +254,9 @@ __global__ __launch_bounds__(64 * WGM * WGN, OCC) void gemm_kernel(const GemmArg
     static_assert(NSB >= 2 && (NSA == NSB || (NSA == 3 && NSB == 2)), "ring slots");
     static_assert((NSA - 1) * AL + (NSB - 1) * BL < 64, "pipeline depth");
     static_assert(LH <= LPS, "loads of a stage");
-    constexpr int RING = NSA * A_BYTES + NSB * B_BYTES, A_RING = NSA * A_BYTES;
+    constexpr int A_RING = NSA * A_BYTES;
     static_assert(!(ASTR || BSTR) || ES == 2, "transposing reads take 16-bit values");
-
-    // epilogue slab of one wave: up to 64 rows of WN values, padded by 4
-    constexpr int SP = WN + 4;
-    constexpr int SLAB = (WM < 64 ? WM : 64) * SP * 4;
-    constexpr int LDS_BYTES = RING > NW * SLAB ? RING : NW * SLAB;
-    __shared__ __attribute__((aligned(1024))) uint8_t smem[LDS_BYTES];
+    constexpr int SP = Cfg::SP, SLAB = Cfg::SLAB;
 
     const int tid = threadIdx.x;
     const int lane = tid & 63;
@@ -257,7 +265,7 @@ __global__ __launch_bounds__(64 * WGM * WGN, OCC) void gemm_kernel(const GemmArg
     // Tile order: each XCD walks a contiguous run; within it, groups of
     // `group` row tiles go column by column, so the tiles in flight on an XCD
     // share both operands' rows in its L2.
-    const int t = xcd_tile(blockIdx.x, g.tiles);
+    const int t = xcd_tile(block, g.tiles);
     const int per_group = g.group * g.tiles_n;
     const int grp = t / per_group;
     const int rows_here = min(g.group, g.tiles_m - grp * g.group);
@@ -265,7 +273,7 @@ __global__ __launch_bounds__(64 * WGM * WGN, OCC) void gemm_kernel(const GemmArg
     const int m0 = (grp * g.group + in % rows_here) * TM;
     const int n0 = (in / rows_here) * TN;
 
-    const int stage0 = blockIdx.y * g.kchunk;
+    const int stage0 = split * g.kchunk;
     const int stage_end = min(g.nstages, stage0 + g.kchunk);
 
     // ---- load geometry: load i of this wave fills the 1 KiB LDS block
@@ -643,7 +651,7 @@ __global__ __launch_bounds__(64 * WGM * WGN, OCC) void gemm_kernel(const GemmArg
 #pragma unroll
                 for (int u = 0; u < U; ++u)
                     if (m + u * RS < g.M) {
-                        float *p = (float *)g.part + blockIdx.y * g.part_stride + (int64_t)(m + u * RS) * g.part_ld + n;
+                        float *p = (float *)g.part + split * g.part_stride + (int64_t)(m + u * RS) * g.part_ld + n;
                         *(v4f *)p = *(v4f *)&v[u][0];
                         *(v4f *)(p + 4) = *(v4f *)&v[u][4];
                     }
@@ -655,6 +663,38 @@ __global__ __launch_bounds__(64 * WGM * WGN, OCC) void gemm_kernel(const GemmArg
         __builtin_amdgcn_wave_barrier();
         __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
     });
+}
+
+// OCC: workgroups a CU is to hold at a time (one wave of each per SIMD)
+template <typename T, int TM, int TN, int WGM, int WGN, int NSA, int NSB, int LH, int OCC, bool ASTR, bool BSTR>
+__global__ __launch_bounds__(64 * WGM * WGN, OCC) void gemm_kernel(const GemmArgs g)
+{
+    __shared__ __attribute__((aligned(1024)))
+    uint8_t smem[TileCfg<T, TM, TN, WGM, WGN, NSA, NSB, LH, ASTR, BSTR>::LDS_BYTES];
+    gemm_tile<T, TM, TN, WGM, WGN, NSA, NSB, LH, ASTR, BSTR>(g, smem, blockIdx.x, blockIdx.y);
+}
+
+// Both products of the gradients, neither of them split, and the last step of
+// the bias gradient, in one launch: where they are a few microseconds each the
+// gaps between launches and the CUs that one alone leaves idle cost as much.
+struct PairArgs {
+    GemmArgs dx, dw;
+    ColSumArgs sum;   // columns 0: no bias gradient
+};
+
+template <typename T, int TM, int TN, int WGM, int WGN, int NSA, int NSB, int LH, int OCC>
+__global__ __launch_bounds__(64 * WGM * WGN, OCC) void gemm_pair_kernel(const PairArgs p)
+{
+    constexpr int kCols = 64 * WGM * WGN / kSumGroups;
+    __shared__ __attribute__((aligned(1024)))
+    uint8_t smem[TileCfg<T, TM, TN, WGM, WGN, NSA, NSB, LH, false, true>::LDS_BYTES];
+    const int b = blockIdx.x;
+    if (b < p.dx.tiles)
+        gemm_tile<T, TM, TN, WGM, WGN, NSA, NSB, LH, false, true>(p.dx, smem, b, 0);
+    else if (b < p.dx.tiles + p.dw.tiles)
+        gemm_tile<T, TM, TN, WGM, WGN, NSA, NSB, LH, true, true>(p.dw, smem, b - p.dx.tiles, 0);
+    else
+        column_sums<kCols>(p.sum, b - p.dx.tiles - p.dw.tiles, (float(*)[kCols + 1])smem);
 }
 
 // Sum of a split product's partial copies, in the order of the splits, and the

@@ -117,6 +117,7 @@ constexpr TileCost kCost[kTiles] = {
     {0.536, 8.2},
     {0.259, 4.4},
     {0.089, 3.8},
+    {0.194, 4.8},
 };
 
 double gemm_cost(int tile, int64_t M, int64_t N, int64_t kbytes, int splits)
@@ -153,6 +154,10 @@ void plan_gemm(int64_t M, int64_t N, int64_t K, int es, GemmPlan *p)
             const int use = only_split > 0 ? (only_split < 64 ? only_split : 64) : s;
             if (use > 1 && (nstages < (only_split ? 4 : 8) * use || (!only_split && tiles * use > 2 * kCUs * kTile[t].occ)))
                 break;
+            // a deep ring pays in the first round of workgroups only (2048x4096x512: two rounds
+            // 16.3 us, 128x128 14.0)
+            if (!force && kTile[t].deep && tiles * use > kCUs)
+                break;
             const double us = gemm_cost(t, M, N, K * es, use);
             if (us < least) {
                 least = us;
@@ -180,8 +185,8 @@ bool grid_fits(const GemmPlan &p)
 
 // C[M, N] = A B^T over K with the epilogue.  kbytes: inner bytes of a rows-form
 // operand as stored (padded to 16).
-bool run_gemm(int64_t dt, const Operand &a, const void *ap, const Operand &b, const void *bp, int64_t M, int64_t N,
-              int64_t K, const GemmPlan &p, void *part, const Epilogue &epi, hipStream_t stream)
+GemmArgs gemm_args(const Operand &a, const void *ap, const Operand &b, const void *bp, int64_t M, int64_t N, int64_t K,
+                   const GemmPlan &p, void *part, const Epilogue &epi)
 {
     GemmArgs g;
     memset(&g, 0, sizeof g);
@@ -205,12 +210,17 @@ bool run_gemm(int64_t dt, const Operand &a, const void *ap, const Operand &b, co
     g.epi = epi;
     // row strides (0 for an absent matrix) in elements of at most four bytes
     g.epi.tile_offsets = epi.ldo < (1 << 20) && epi.ldr < (1 << 20) && epi.ldp < (1 << 20);
+    return g;
+}
+
+bool run_gemm(int64_t dt, const Operand &a, const Operand &b, const GemmPlan &p, const GemmArgs &g, hipStream_t stream)
+{
     const bool ok = dt == DENSE_BF16 ? launch_gemm_bf16(p.tile, a.cols, b.cols, g, p.splits, stream)
                   : dt == DENSE_FP16 ? launch_gemm_f16(p.tile, a.cols, b.cols, g, p.splits, stream)
                                      : launch_gemm_i8(p.tile, a.cols, b.cols, g, p.splits, stream);
     if (!ok || p.splits <= 1)
         return ok;
-    const int64_t items = M * (p.part_ld / 8);
+    const int64_t items = (int64_t)g.M * (p.part_ld / 8);
     const dim3 grid((unsigned)ceil_div(items, 256)), block(256);
     if (dt == DENSE_INT8)
         hipLaunchKernelGGL(split_finish_kernel<true>, grid, block, 0, stream, g, p.splits);
@@ -398,9 +408,9 @@ conv_i8_status_t run_linear(const LinearPlan &p, void *ws, hipStream_t stream)
     uint8_t *pa = (uint8_t *)ws, *pb = pa + p.a.pack_bytes, *part = pb + p.b.pack_bytes;
     if (!launch_pack(p.a, pa, p.b, pb, stream))
         return CONV_I8_ERR_HIP;
-    return run_gemm(p.d.x.dtype, p.a, p.a.packed ? pa : p.a.src, p.b, p.b.packed ? pb : p.b.src, p.M, p.N, p.K, p.gemm,
-                    part, epi, stream)
-               ? CONV_I8_OK : CONV_I8_ERR_HIP;
+    const GemmArgs g = gemm_args(p.a, p.a.packed ? pa : p.a.src, p.b, p.b.packed ? pb : p.b.src, p.M, p.N, p.K, p.gemm,
+                                 part, epi);
+    return run_gemm(p.d.x.dtype, p.a, p.b, p.gemm, g, stream) ? CONV_I8_OK : CONV_I8_ERR_HIP;
 }
 
 // ---- linear_backward -------------------------------------------------------
@@ -419,6 +429,14 @@ struct BackwardPlan {
     Operand gt, xb;            // dw = g^T x: both in columns form over m
     GemmPlan dx, dw;
     int64_t part_bytes = 0, ws_bytes = 0;
+
+    // Both products go out in one launch.  The same tile and no split, so each
+    // is computed as it would be alone.
+    bool pair() const
+    {
+        return want_dx && want_dw && dx.tile == kPairTile && dw.tile == kPairTile && dx.splits == 1 && dw.splits == 1 &&
+               (int64_t)dx.tiles_m * dx.tiles_n + (int64_t)dw.tiles_m * dw.tiles_n < (1 << 24);
+    }
 };
 
 conv_i8_status_t analyze(const dense_linear_backward_t *args, BackwardPlan *p)
@@ -586,18 +604,15 @@ conv_i8_status_t run_backward(const BackwardPlan &p, void *ws, hipStream_t strea
         if (hipGetLastError() != hipSuccess)
             return CONV_I8_ERR_HIP;
     }
+    ColSumArgs c;
+    memset(&c, 0, sizeof c);
     if (p.want_db) {
-        ColSumArgs c;
-        memset(&c, 0, sizeof c);
         c.part = (const float *)sums;
         c.ld = p.sum_ld;
         c.rows = p.row_blocks;  // none: zeros
         c.cols = c.split = c.valid = (int)p.N;
         c.out0 = const_cast<void *>(d.dbias.ptr);
         c.dt = (int)dt;
-        hipLaunchKernelGGL(colsum_kernel<>, dim3((unsigned)ceil_div(p.N, 32)), dim3(256), 0, stream, c);
-        if (hipGetLastError() != hipSuccess)
-            return CONV_I8_ERR_HIP;
     }
     if (!launch_pack(p.wb, pw, p.xb, px, stream))
         return CONV_I8_ERR_HIP;
@@ -605,18 +620,31 @@ conv_i8_status_t run_backward(const BackwardPlan &p, void *ws, hipStream_t strea
     Epilogue e;
     memset(&e, 0, sizeof e);
     e.out_dt = (int)dt;
+    GemmArgs dx, dw;
     if (p.want_dx) {
         e.out = const_cast<void *>(d.dx.ptr);
         e.ldo = d.dx.row_stride;
-        if (!run_gemm(dt, p.ga, gp, p.wb, p.wb.packed ? pw : p.wb.src, p.M, p.K, p.N, p.dx, part, e, stream))
-            return CONV_I8_ERR_HIP;
+        dx = gemm_args(p.ga, gp, p.wb, p.wb.packed ? pw : p.wb.src, p.M, p.K, p.N, p.dx, part, e);
     }
     if (p.want_dw) {
         e.out = const_cast<void *>(d.dw.ptr);
         e.ldo = d.dw.row_stride;
-        if (!run_gemm(dt, p.gt, gp, p.xb, p.xb.packed ? px : p.xb.src, p.N, p.K, p.M, p.dw, part, e, stream))
+        dw = gemm_args(p.gt, gp, p.xb, p.xb.packed ? px : p.xb.src, p.N, p.K, p.M, p.dw, part, e);
+    }
+    if (p.pair()) {
+        const PairArgs both = {dx, dw, c};
+        const bool ok = dt == DENSE_BF16 ? launch_gemm_pair_bf16(both, stream) : launch_gemm_pair_f16(both, stream);
+        return ok ? CONV_I8_OK : CONV_I8_ERR_HIP;
+    }
+    if (p.want_db) {
+        hipLaunchKernelGGL(colsum_kernel<>, dim3((unsigned)ceil_div(p.N, 32)), dim3(32 * kSumGroups), 0, stream, c);
+        if (hipGetLastError() != hipSuccess)
             return CONV_I8_ERR_HIP;
     }
+    if (p.want_dx && !run_gemm(dt, p.ga, p.wb, p.dx, dx, stream))
+        return CONV_I8_ERR_HIP;
+    if (p.want_dw && !run_gemm(dt, p.gt, p.xb, p.dw, dw, stream))
+        return CONV_I8_ERR_HIP;
     return CONV_I8_OK;
 }
 
@@ -706,7 +734,8 @@ conv_i8_status_t dense_linear_backward_plan(const dense_linear_backward_t *args,
         describe(p.dx, p.ga, p.wb, dx, sizeof dx);
     if (p.want_dw)
         describe(p.dw, p.gt, p.xb, dw, sizeof dw);
-    snprintf(text, sizeof text, "g=%s dx: %s; dw: %s", p.write_g ? "written" : "dy", dx, dw);
+    snprintf(text, sizeof text, "g=%s launches=%s dx: %s; dw: %s", p.write_g ? "written" : "dy",
+             p.pair() ? "paired" : "apart", dx, dw);
     if (strlen(text) + 1 > len)
         return CONV_I8_ERR_PARAM;
     memcpy(buf, text, strlen(text) + 1);

@@ -1,9 +1,9 @@
 // Layer norm's C entries: argument checks, the choice of kernel, the launches.
 #include <string.h>
 
+#include "colsum.hpp"
 #include "host_common.hpp"
 #include "norm_kernel.hpp"
-#include "rows_kernel.hpp"
 
 namespace dense {
 namespace {
@@ -288,7 +288,7 @@ conv_i8_status_t dense_layer_norm_backward(const dense_layer_norm_backward_t *ar
         c.out0 = const_cast<void *>(p.d.dweight.ptr);
         c.out1 = const_cast<void *>(p.d.dbias.ptr);
         c.dt = (int)dt;
-        hipLaunchKernelGGL(colsum_kernel<>, dim3((unsigned)ceil_div(c.cols, 32)), dim3(256), 0, s, c);
+        hipLaunchKernelGGL(colsum_kernel<>, dim3((unsigned)ceil_div(c.cols, 32)), dim3(32 * kSumGroups), 0, s, c);
         if (hipGetLastError() != hipSuccess)
             return CONV_I8_ERR_HIP;
     }

@@ -10,8 +10,7 @@
 // What they need is bytes in flight.  A thread group walks over rows and loads
 // the next one, in the form it has in memory, before it works on the present
 // one, and a load has no condition per lane (TAIL: D is no multiple of eight).
-// 16384 x 4096
-// BF16: forward 50 us (5.3 TB/s; a copy of the same bytes reaches 5.9), with a
+// 16384 x 4096 BF16: forward 50 us (5.3 TB/s; a copy of the same bytes reaches 5.9), with a
 // workgroup per row that loads, reduces and stores in turn 82; backward 76 us
 // (5.2 TB/s), without the next row's loads 133.
 #pragma once

@@ -1,8 +1,9 @@
 // Memory-bound passes around the products: copies of operands into the form
-// the product kernel reads in place, the gradient of the activation with the
-// column sums of the bias gradient, and the reduction of those sums.
+// the product kernel reads in place, and the gradient of the activation with the
+// column sums of the bias gradient.
 #pragma once
 
+#include "colsum.hpp"
 #include "dense_common.hpp"
 
 namespace dense {
@@ -151,52 +152,6 @@ __global__ __launch_bounds__(256) void act_grad_kernel(const ActGradArgs a)
         if (blockIdx.x * 512 + c < a.N)
             a.colsum[blockIdx.y * a.sum_ld + blockIdx.x * 512 + c] =
                 (red[0][c] + red[1][c]) + (red[2][c] + red[3][c]);
-}
-
-// out[c] = sum over r of part[r][c], rows in a fixed order: eight groups of
-// threads take every eighth row of 32 columns and are added through LDS.
-// Columns [0, split) go to out0 and [split, cols) to out1, the first `valid`
-// of each.
-struct ColSumArgs {
-    const float *part;
-    int64_t ld;
-    int rows, cols;
-    int split, valid;
-    void *out0, *out1;
-    int dt;
-};
-
-template <int COLS = 32>
-__global__ __launch_bounds__(256) void colsum_kernel(const ColSumArgs a)
-{
-    constexpr int G = 256 / COLS;
-    __shared__ float red[G][COLS + 1];
-    const int c = threadIdx.x % COLS, grp = threadIdx.x / COLS;
-    const int col = blockIdx.x * COLS + c;
-    const bool second = col >= a.split;
-    const int oc = second ? col - a.split : col;
-    const bool live = col < a.cols && oc < a.valid;
-    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (live) {
-        const float *p = a.part + col;
-        int r = grp;
-        for (; r + 3 * G < a.rows; r += 4 * G) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                s[k] += p[(r + G * k) * a.ld];
-        }
-        for (; r < a.rows; r += G)
-            s[0] += p[r * a.ld];
-    }
-    red[grp][c] = (s[0] + s[1]) + (s[2] + s[3]);
-    __syncthreads();
-    if (grp == 0 && live) {
-        float v = 0.0f;
-#pragma unroll
-        for (int k = 0; k < G; ++k)
-            v += red[k][c];
-        store_dt(second ? a.out1 : a.out0, a.dt, oc, v);
-    }
 }
 
 }  // namespace dense

@@ -578,3 +578,80 @@ def test_offsets_past_32_bits(ci8):
     dxn, _, _ = ci8.layer_norm_backward(h, y, None, mean, rstd)
     (v, e), _, _ = ref.layer_norm_backward(h[rows], y[rows], None, mean[rows], rstd[rows])
     ref.check(dxn[rows], v, e, "norm dx rows")
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16, I8])
+@pytest.mark.parametrize("tile", ["128x128d", "128x128d/2", "128x128d/3"])
+@pytest.mark.parametrize("m,n,k", [(128, 128, 64), (300, 200, 160), (65, 513, 1056), (257, 264, 4096), (130, 100, 24)])
+def test_linear_deep_ring(ci8, monkeypatch, dtype, tile, m, n, k):
+    """The five-slot ring with fewer, as many and more stages than slots."""
+    monkeypatch.setenv("CONV_I8_DENSE_TILE", tile)
+    run_linear(ci8, m, n, k, dtype, act=ACTS[(m + k // 32) % 5], residual=m % 2 == 0, keep=True)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("m,n,k", [(520, 264, 300), (289, 1040, 96)])
+def test_backward_deep_ring(ci8, monkeypatch, dtype, m, n, k):
+    monkeypatch.setenv("CONV_I8_DENSE_TILE", "128x128d")
+    run_backward(ci8, m, n, k, dtype, "silu")
+
+
+@pytest.mark.parametrize("act", ["none", "gelu"])
+@pytest.mark.parametrize("m,n,k", [(777, 520, 264), (64, 64, 64), (130, 9, 1000), (7, 1000, 130), (2, 3, 5)])
+def test_backward_pair(ci8, m, n, k, act):
+    """Both products and the bias gradient in one launch, and the same bits when each is asked for alone."""
+    from int8_convolution_forward_amd.dense import linear_backward_plan
+    run_backward(ci8, m, n, k, BF16, act)
+    g = gen(21)
+    dy, x, w, z = values(g, m, n), values(g, m, k), values(g, n, k), values(g, m, n)
+    plan = linear_backward_plan(dy, x, w, preact=z, activation=act)
+    assert "launches=paired" in plan, plan
+    assert "launches=apart" in linear_backward_plan(dy, x, w, preact=z, activation=act, need_dx=False)
+    full = ci8.linear_backward(dy, x, w, preact=z, activation=act)
+    for i in range(3):
+        part = ci8.linear_backward(dy, x, w, preact=z, activation=act, need_dx=i == 0, need_dw=i == 1, need_dbias=i == 2)
+        assert torch.equal(part[i], full[i])
+
+
+# more rows than thread groups, so that each walks over several
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("m,d", [(2500, 4096), (2300, 4001), (1500, 9001), (1200, 16384), (4500, 777), (9000, 130), (9001, 8),
+                                 (5000, 11), (3000, 6), (1030, 20000)])
+def test_norm_many_rows(ci8, dtype, m, d):
+    run_norm(ci8, m, d, dtype, weight=d % 3 != 0)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
+@pytest.mark.parametrize("m,d", [(1100, 4096), (1100, 4001), (1050, 8192), (1041, 8191), (1030, 12345), (9000, 130), (3000, 7),
+                                 (600, 9), (5000, 8)])
+def test_norm_backward_many_rows(ci8, dtype, m, d):
+    run_norm_backward(ci8, m, d, dtype, weight=d % 3 != 0)
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("m,n", [(1, 513), (37, 520), (70, 1001), (130, 7), (66, 8), (19, 1024)])
+def test_backward_bias_only(ci8, m, n, act):
+    """The pass over dy and z at whole, partial and narrow strips of columns."""
+    run_backward(ci8, m, n, 8, BF16, act, dy_layout=dict(pitch=n % 3), z_layout=dict(pitch=5))
+    g = gen(22)
+    dy, z = values(g, m, n, dtype=FP16), values(g, m, n, dtype=FP16, scale=2.0)
+    x, w = values(g, m, 8, dtype=FP16), values(g, n, 8, dtype=FP16)
+    got = ci8.linear_backward(dy, x, w, preact=z, activation=act, need_dx=False, need_dw=False)[2]
+    ref.check(got, *ref.linear_backward(dy, x, w, z if act != "none" else None, act)[2], "dbias")
+
+
+def test_gelu_tanh_far_values(ci8):
+    """Pre-activations up to the type's largest: no overflow inside the gate, its slope or their products."""
+    big = torch.tensor([0.0, 5, -5, 12, -12, 100, -100, 1e4, -1e4, 1e15, -1e15, 1e19, -1e19, 3e38, -3e38], device="cuda").to(BF16)
+    n = big.numel()
+    one = torch.ones(40, 1, dtype=BF16, device="cuda")
+    for m in (2, 40):
+        y = ci8.linear(one[:m], big[:, None].contiguous(), activation="gelu_tanh")
+        want = ref.act(big.double(), "gelu_tanh")
+        assert bool(torch.isfinite(y).all())
+        ref.check(y, want.expand(m, n), (ref.ACT_ERR * big.double().abs() + ref.rounding(want.abs(), BF16)).expand(m, n), "far")
+    z = big.expand(4, n).contiguous()
+    db = ci8.linear_backward(torch.ones_like(z), one[:4], big[:, None].contiguous(), preact=z, activation="gelu_tanh",
+                             need_dx=False, need_dw=False)[2]
+    far = big.double().abs() >= 100
+    assert torch.equal(db[far].double(), 4.0 * (big[far] > 0).double())
