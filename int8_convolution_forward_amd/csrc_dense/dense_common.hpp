@@ -221,7 +221,6 @@ constexpr float kGeluC = 0.797884560802865f;   // sqrt(2/pi)
 constexpr float kGeluA = 0.044715f;
 constexpr float kGeluE1 = -2.302208198144325f;  // -2 sqrt(2/pi) log2 e
 constexpr float kGeluE3 = -0.102943239579983f;  // kGeluA times it
-constexpr float kSqrtHalf = 0.707106781186548f;
 constexpr float kInvSqrt2Pi = 0.398942280401433f;
 
 // 0.5 (1 + tanh u) = sigmoid(2u), so the tanh form of gelu is z sigmoid(2u).
@@ -232,11 +231,29 @@ __device__ __forceinline__ float gelu_tanh_gate(float z, float z2)
     return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * __builtin_fmaf(z2, kGeluE3, kGeluE1)));
 }
 
-// Normal distribution function through erfc, which keeps its relative
-// precision in the lower tail.
-__device__ __forceinline__ float normal_cdf(float z)
+// exp(-z^2/2) and the normal distribution function.  With t = 1 / (1 + c |z|) the
+// lower tail is t Q(t) exp(-z^2/2): Q, of degree 9, is a fit to
+// exp(z^2/2) cdf(-|z|) / t with the least relative error, 2^-24.9, over all z.
+// Rounded to 32 bits everything is within 3 2^-24, and the tail keeps its
+// relative precision (11 2^-24 down to z = -3; the rounding of z^2 in the
+// exponent).  About 20 operations, where the library's erfc takes several times
+// as many and branches.
+__device__ __forceinline__ float normal_cdf(float z, float &bell)
 {
-    return 0.5f * erfcf(-kSqrtHalf * z);
+    bell = __builtin_amdgcn_exp2f(-0.72134752044448f * (z * z));
+    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(fabsf(z), 3.181980550e-01f, 1.0f));
+    float q = -2.069549154e-02f;
+    q = __builtin_fmaf(q, t, 9.534367189e-02f);
+    q = __builtin_fmaf(q, t, -1.502907509e-01f);
+    q = __builtin_fmaf(q, t, 7.120001795e-02f);
+    q = __builtin_fmaf(q, t, -1.117871554e-02f);
+    q = __builtin_fmaf(q, t, 5.997513579e-02f);
+    q = __builtin_fmaf(q, t, 8.762607770e-02f);
+    q = __builtin_fmaf(q, t, 1.141358198e-01f);
+    q = __builtin_fmaf(q, t, 1.269415814e-01f);
+    q = __builtin_fmaf(q, t, 1.269426604e-01f);
+    const float tail = t * q * bell;
+    return z < 0.0f ? tail : 1.0f - tail;
 }
 
 template <int ACT>
@@ -244,9 +261,10 @@ __device__ __forceinline__ float activate(float z)
 {
     if constexpr (ACT == DENSE_ACT_RELU)
         return z < 0.0f ? 0.0f : z;  // keeps a NaN
-    else if constexpr (ACT == DENSE_ACT_GELU)
-        return z * normal_cdf(z);
-    else if constexpr (ACT == DENSE_ACT_GELU_TANH)
+    else if constexpr (ACT == DENSE_ACT_GELU) {
+        float bell;
+        return z * normal_cdf(z, bell);
+    } else if constexpr (ACT == DENSE_ACT_GELU_TANH)
         return z * gelu_tanh_gate(z, z * z);
     else if constexpr (ACT == DENSE_ACT_SILU)
         return z * sigmoid(z);
@@ -260,7 +278,9 @@ __device__ __forceinline__ float act_slope(float z)
     if constexpr (ACT == DENSE_ACT_RELU) {
         return z > 0.0f ? 1.0f : z == z ? 0.0f : z;
     } else if constexpr (ACT == DENSE_ACT_GELU) {
-        return normal_cdf(z) + z * kInvSqrt2Pi * __builtin_amdgcn_exp2f(-0.72134752044448f * z * z);
+        float bell;
+        const float cdf = normal_cdf(z, bell);
+        return __builtin_fmaf(z * kInvSqrt2Pi, bell, cdf);
     } else if constexpr (ACT == DENSE_ACT_GELU_TANH) {
         // p + z p (1 - p) 2u'(z); z^2 is bounded where p (1 - p) is already 0,
         // so that it cannot overflow against it

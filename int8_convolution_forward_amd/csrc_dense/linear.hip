@@ -354,9 +354,9 @@ bool launch_skinny(const SkinnyArgs &s, const LinearPlan &p, hipStream_t stream)
     const dim3 one((unsigned)ceil_div(s.N, 16)), two((unsigned)ceil_div(s.N, 32));
     if (!p.aligned) {
         if (p.M <= 16)
-            hipLaunchKernelGGL((skinny_direct_kernel<T, 1, 8>), one, dim3(512), 0, stream, s);
+            hipLaunchKernelGGL((skinny_unaligned_kernel<T, 1, 8, 4>), one, dim3(512), 0, stream, s);
         else
-            hipLaunchKernelGGL((skinny_direct_kernel<T, 2, 8>), one, dim3(512), 0, stream, s);
+            hipLaunchKernelGGL((skinny_unaligned_kernel<T, 2, 8, 2>), one, dim3(512), 0, stream, s);
     } else if (p.M <= 4) {
         if (p.waves == 4)
             hipLaunchKernelGGL((skinny_kernel<T, 1, 1, 4, 4, false>), one, dim3(256), 0, stream, s);

@@ -99,6 +99,7 @@ struct BackPlan {
     dense_layer_norm_backward_t d;
     int64_t M, D;
     bool sums;
+    bool once = false;   // norm_backward_once_kernel
     int wgs = 0;         // workgroups that walk the rows, or row blocks of a long row's sums
     int64_t part_ld = 0, ws_bytes = 0;
 };
@@ -149,21 +150,30 @@ conv_i8_status_t analyze(const dense_layer_norm_backward_t *args, BackPlan *p)
         const int64_t want = ceil_div(p->M, 4 * rows);
         p->wgs = (int)(want < most ? want : most);
     }
-    p->ws_bytes = p->sums ? round_up((int64_t)p->wgs * 2 * p->part_ld * 4, kWsAlign) : 0;
+    p->once = p->sums && p->M > 0 && p->M <= kOnceRows && back_in_registers(p->D);
+    p->ws_bytes = p->sums && !p->once ? round_up((int64_t)p->wgs * 2 * p->part_ld * 4, kWsAlign) : 0;
     return CONV_I8_OK;
 }
 
 template <typename T, int P, int V, int AHEAD>
 void launch_back_one(const NormBackArgs &a, int wgs, hipStream_t s)
 {
-    const dim3 grid((unsigned)wgs), block(norm_threads(P));
-    auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, s, a); };
-    if (a.D % 8 == 0)
+    const dim3 block(norm_threads(P));
+    auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3((unsigned)wgs), block, 0, s, a); };
+    if (a.dweight) {
+        const int cols = (int)ceil_div(a.D, kOnceCols);
+        const dim3 grid((unsigned)(cols + ceil_div(a.M, norm_threads(P) / P)));
+        if (a.D % 8 == 0)
+            hipLaunchKernelGGL((norm_backward_once_kernel<T, P, V, false>), grid, block, 0, s, a, cols);
+        else
+            hipLaunchKernelGGL((norm_backward_once_kernel<T, P, V, true>), grid, block, 0, s, a, cols);
+    } else if (a.D % 8 == 0) {
         a.part ? launch(norm_backward_kernel<T, P, V, AHEAD, false, true>)
                : launch(norm_backward_kernel<T, P, V, AHEAD, false, false>);
-    else
+    } else {
         a.part ? launch(norm_backward_kernel<T, P, V, AHEAD, true, true>)
                : launch(norm_backward_kernel<T, P, V, AHEAD, true, false>);
+    }
 }
 
 template <typename T>
@@ -262,8 +272,12 @@ conv_i8_status_t dense_layer_norm_backward(const dense_layer_norm_backward_t *ar
     a.M = (int)p.M;
     a.D = (int)p.D;
     a.d = (float)a.D;
-    a.part = p.sums ? (float *)workspace : nullptr;
+    a.part = p.sums && !p.once ? (float *)workspace : nullptr;
     a.part_ld = p.part_ld;
+    if (p.once) {
+        a.dweight = const_cast<void *>(p.d.dweight.ptr);
+        a.dbias = const_cast<void *>(p.d.dbias.ptr);
+    }
     hipStream_t s = (hipStream_t)stream;
     const int64_t dt = p.d.x.dtype;
     if (p.M > 0) {
@@ -276,7 +290,7 @@ conv_i8_status_t dense_layer_norm_backward(const dense_layer_norm_backward_t *ar
         if (hipGetLastError() != hipSuccess)
             return CONV_I8_ERR_HIP;
     }
-    if (p.sums) {
+    if (p.sums && !p.once) {
         ColSumArgs c;
         memset(&c, 0, sizeof c);
         c.part = a.part;

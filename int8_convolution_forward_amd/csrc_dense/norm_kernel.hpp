@@ -107,6 +107,15 @@ __device__ __forceinline__ void load_params(const T *p, float absent, int D, int
         r[i] = load_param(p, absent, (i * P + t) * 8, D);
 }
 
+// Keeps what is computed from r inside the loop it stands in: widened weights
+// held over all rows would take twice the registers (16-bit types).
+template <typename T>
+__device__ __forceinline__ void pin(Raw8<T> &r)
+{
+    if constexpr (sizeof(T) == 2)
+        asm volatile("" : "+v"(r.w[0]));
+}
+
 // Mean and sum of squared distances from it, of a row held by P threads.  A
 // wave takes both of its own columns (cols of them), two passes over registers;
 // the waves' pairs are joined through LDS with one barrier:
@@ -213,6 +222,8 @@ __global__ __launch_bounds__(norm_threads(P)) void norm_kernel(const NormArgs a)
                 w[i] = load_param((const T *)a.weight, 1.0f, c, a.D);
                 b[i] = load_param((const T *)a.bias, 0.0f, c, a.D);
             }
+            pin(w[i]);
+            pin(b[i]);
             widen_group<TAIL, P>(w[i], a.D, i, t, wv);
             widen_group<TAIL, P>(b[i], a.D, i, t, bv);
 #pragma unroll
@@ -356,6 +367,7 @@ struct NormBackArgs {
     float d;                        // D; sums are divided by it, so that a constant row's mean is exact
     float *part;              // [workgroup][2][part_ld]: column sums of dy xh and of dy; null: not computed
     int64_t part_ld;
+    void *dweight, *dbias;    // norm_backward_once_kernel only
 };
 
 // dx of one row after another, with the columns' sums of dy xh and dy kept in
@@ -364,7 +376,7 @@ struct NormBackArgs {
 // threads, which have 128 registers each) the weights are read again for each
 // row too.
 template <typename T, int P, int V, int AHEAD, bool TAIL, bool SUMS>
-__global__ __launch_bounds__(norm_threads(P)) void norm_backward_kernel(const NormBackArgs a)
+__device__ __forceinline__ void backward_rows(const NormBackArgs &a, int block, int blocks)
 {
     constexpr int RPW = norm_threads(P) / P;
     constexpr int NWR = P > 64 ? P / 64 : 1;
@@ -386,7 +398,7 @@ __global__ __launch_bounds__(norm_threads(P)) void norm_backward_kernel(const No
         Raw8<T> x[V], dy[V];
         float mean, rstd;
     } ring[AHEAD > 0 ? AHEAD : 1];
-    const int64_t step = (int64_t)gridDim.x * RPW;
+    const int64_t step = (int64_t)blocks * RPW;
     auto load = [&](int64_t m, Rows &r) __attribute__((always_inline)) {
         if (m < a.M) {
             load_row<T, P, V>((const T *)a.x + m * a.ldx, a.D, t, r.x);
@@ -395,7 +407,7 @@ __global__ __launch_bounds__(norm_threads(P)) void norm_backward_kernel(const No
             r.rstd = a.rstd[m];
         }
     };
-    int64_t m = (int64_t)blockIdx.x * RPW + sub;
+    int64_t m = (int64_t)block * RPW + sub;
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i)
         load(m + i * step, ring[i]);
@@ -415,6 +427,7 @@ __global__ __launch_bounds__(norm_threads(P)) void norm_backward_kernel(const No
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             float wv[8], dy[8];
+            pin(w[i]);
             widen_group<TAIL, P>(w[i], a.D, i, t, wv);
             widen_group<TAIL, P>(cur.x[i], a.D, i, t, xh[i]);
             widen_group<TAIL, P>(cur.dy[i], a.D, i, t, dy);
@@ -490,18 +503,93 @@ __global__ __launch_bounds__(norm_threads(P)) void norm_backward_kernel(const No
                     for (int r = 0; r < RPW; ++r)
                         v += cs[r][src];
                     if (col < a.D)
-                        a.part[((int64_t)blockIdx.x * 2 + (i >= V)) * a.part_ld + col] = v;
+                        a.part[((int64_t)block * 2 + (i >= V)) * a.part_ld + col] = v;
                 }
             }
         } else {
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const int c = (i * P + t) * 8;
-                float *p = a.part + (int64_t)blockIdx.x * 2 * a.part_ld + c;
+                float *p = a.part + (int64_t)block * 2 * a.part_ld + c;
                 store_n(p, a.D - c, sw[i]);
                 store_n(p + a.part_ld, a.D - c, sb[i]);
             }
         }
+    }
+}
+
+template <typename T, int P, int V, int AHEAD, bool TAIL, bool SUMS>
+__global__ __launch_bounds__(norm_threads(P)) void norm_backward_kernel(const NormBackArgs a)
+{
+    backward_rows<T, P, V, AHEAD, TAIL, SUMS>(a, blockIdx.x, gridDim.x);
+}
+
+// Everything in one launch, for up to kOnceRows rows: the first workgroups sum 32
+// columns each over all rows, four threads to a row, the others take one row per
+// thread group.  x and dy are read twice, the second time from cache; what it
+// saves is the partial sums on their way out and back, and a launch, whose 4 us
+// are half of such a call.
+constexpr int64_t kOnceRows = 1024;
+constexpr int kOnceCols = 32;
+
+template <typename T, int P, int V, bool TAIL>
+__global__ __launch_bounds__(norm_threads(P)) void norm_backward_once_kernel(const NormBackArgs a, int col_blocks)
+{
+    if ((int)blockIdx.x >= col_blocks) {
+        backward_rows<T, P, V, 0, TAIL, false>(a, blockIdx.x - col_blocks, gridDim.x - col_blocks);
+        return;
+    }
+    constexpr int LANES = kOnceCols / 8, G = norm_threads(P) / LANES, U = 4;
+    __shared__ float sums[2][norm_threads(P) / 64][kOnceCols];
+    const int c = blockIdx.x * kOnceCols + (threadIdx.x % LANES) * 8, grp = threadIdx.x / LANES;
+    float sw[8] = {}, sb[8] = {};
+    for (int m = grp; m < a.M; m += U * G) {
+        Raw8<T> x[U], dy[U];
+        float mean[U], rstd[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {  // rows past the end repeat the last one
+            const int64_t r = min(m + u * G, a.M - 1);
+            x[u] = load_raw((const T *)a.x + r * a.ldx, c, a.D);
+            dy[u] = load_raw((const T *)a.dy + r * a.lddy, c, a.D);
+            mean[u] = a.mean[r];
+            rstd[u] = a.rstd[r];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (m + u * G >= a.M)
+                break;
+            float xv[8], g[8];
+            widen_part<TAIL>(x[u], c, a.D, xv);
+            widen_part<TAIL>(dy[u], c, a.D, g);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                sw[k] = __builtin_fmaf(g[k], (xv[k] - mean[u]) * rstd[u], sw[k]);
+                sb[k] += g[k];
+            }
+        }
+    }
+    // the wave's sixteen rows by shuffles, the waves through LDS
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+#pragma unroll
+        for (int o = 32; o >= LANES; o >>= 1) {
+            sw[k] += __shfl_xor(sw[k], o, 64);
+            sb[k] += __shfl_xor(sb[k], o, 64);
+        }
+    if ((threadIdx.x & 63) < LANES)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            sums[0][threadIdx.x >> 6][(threadIdx.x % LANES) * 8 + k] = sw[k];
+            sums[1][threadIdx.x >> 6][(threadIdx.x % LANES) * 8 + k] = sb[k];
+        }
+    __syncthreads();
+    const int col = blockIdx.x * kOnceCols + threadIdx.x % kOnceCols, which = threadIdx.x / kOnceCols;
+    if (which < 2 && col < a.D) {
+        float v = 0.0f;
+#pragma unroll
+        for (int i = 0; i < norm_threads(P) / 64; ++i)
+            v += sums[which][i][threadIdx.x % kOnceCols];
+        ((T *)(which ? a.dbias : a.dweight))[col] = (T)v;
     }
 }
 

@@ -36,7 +36,9 @@ __global__ __launch_bounds__(256) void pack_kernel(const PackArgs a)
     const int64_t i = (int64_t)(second ? blockIdx.x - a.first : blockIdx.x) * 256 + threadIdx.x;
     if (i >= j.items)
         return;
-    const int64_t r = i / j.chunks, c = (i - r * j.chunks) * E;
+    // a 64-bit division costs more than the copy
+    const int64_t r = j.items <= 0xffffffffll ? (int64_t)((uint32_t)i / (uint32_t)j.chunks) : i / j.chunks;
+    const int64_t c = (i - r * j.chunks) * E;
     const U *s = (const U *)j.src + r * j.rs + c * j.cs;
     Piece p;
     if (j.cs == 1 && c + E <= j.cols) {

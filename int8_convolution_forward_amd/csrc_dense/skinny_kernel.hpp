@@ -9,9 +9,9 @@
 // Where rows are 16-byte aligned, skinny_kernel streams the blocks of w -- and,
 // for more than four rows, of x -- through a part of LDS that is the wave's own
 // (no barriers), by loads in which eight lanes take 128 contiguous bytes of a
-// row.  Loading a fragment straight into registers, as skinny_direct_kernel
-// does for unaligned rows, makes 16 lanes touch 16 rows at a time, and the
-// cache then delivers 16 bytes a cycle instead of 64: one bf16 token through
+// row.  Loading a fragment straight into registers makes 16 lanes touch 16 rows
+// at a time, and the cache then delivers 16 bytes a cycle instead of 64: one bf16
+// token through
 // [8192, 2048] takes 7.2 us that way and 6.7 through LDS (33.5 MB, 5.0 TB/s,
 // what a large copy reaches), 16 int8 tokens through [2048, 8192] 9.1 and 5.4.
 // Splitting the inner dimension over workgroups as well, with a second launch
@@ -243,75 +243,94 @@ __global__ __launch_bounds__(64 * W) void skinny_kernel(const SkinnyArgs g)
     skinny_finish<T, G, R, W>(g, red, n0);
 }
 
-// Rows that are not 16-byte aligned: fragments straight into registers
-template <typename T, int G, int W>
-__global__ __launch_bounds__(64 * W) void skinny_direct_kernel(const SkinnyArgs g)
+// Rows that are not 16-byte aligned: the same loads, eight lanes to 128 bytes of
+// a row, but by way of registers (a load into LDS needs aligned chunks), U
+// blocks of w and x at a time.  One fp16 token through [6736, 4313]: 14 us, with
+// fragments loaded straight from memory 25.
+template <typename T, int G, int W, int U>
+__global__ __launch_bounds__(64 * W) void skinny_unaligned_kernel(const SkinnyArgs g)
 {
     typedef typename Acc4<T>::type acc_t;
-    __shared__ acc_t red[W][G][64];
+    constexpr int BLOCK = 2048 * (1 + G);              // LDS bytes of one block: w's 16 rows, then x's
+    constexpr int RED = W * G * 1024;
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[W * U * BLOCK > RED ? W * U * BLOCK : RED];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n0 = blockIdx.x * 16;
-    const int r = lane & 15;
-    const int q = (lane >> 4) * 16;
+    const int r = lane & 15, q = lane >> 4;
 
-    const uint8_t *wp = g.w + (int64_t)min(n0 + r, g.N - 1) * g.ldw + q;
-    const uint8_t *xp[G];
+    // load h of 16 rows: row 8 h + lane / 8, chunk lane % 8; rows past the end repeat the last one
+    const int chunk = (lane & 7) * 16;
+    const uint8_t *src[2 * (1 + G)];
+    int dst[2];
 #pragma unroll
-    for (int i = 0; i < G; ++i)
-        xp[i] = g.x + (int64_t)min(16 * i + r, g.M - 1) * g.ldx + q;
+    for (int h = 0; h < 2; ++h) {
+        const int row = h * 8 + (lane >> 3);
+        dst[h] = row * 128 + row_swizzle<128>(row, lane & 7) * 16;
+        src[h] = g.w + (int64_t)min(n0 + row, g.N - 1) * g.ldw + chunk;
+#pragma unroll
+        for (int i = 0; i < G; ++i)
+            src[2 + 2 * i + h] = g.x + (int64_t)min(16 * i + row, g.M - 1) * g.ldx + chunk;
+    }
+    uint8_t *mine = smem + wave * U * BLOCK;
 
     acc_t acc[G];
 #pragma unroll
     for (int i = 0; i < G; ++i)
         acc[i] = acc_t{0, 0, 0, 0};
-
-    // U blocks of 128 bytes a row in flight
-    constexpr int U = 4;
+    // LAST: the block in which the inner dimension may end before the block does
+    auto blocks_at = [&](auto nc, auto last, int64_t b) __attribute__((always_inline)) {
+        constexpr int N = decltype(nc)::value;
+        v4i v[N][2 * (1 + G)];
+#pragma unroll
+        for (int u = 0; u < N; ++u)
+#pragma unroll
+            for (int i = 0; i < 2 * (1 + G); ++i) {
+                const int64_t k = (b + u * W) * 128;
+                if constexpr (decltype(last)::value)
+                    v[u][i] = load_piece_tail<T>(src[i] + k, g.kbytes - k - chunk);
+                else
+                    v[u][i] = load_piece<T>(src[i] + k);
+            }
+#pragma unroll
+        for (int u = 0; u < N; ++u)
+#pragma unroll
+            for (int i = 0; i < 2 * (1 + G); ++i)
+                *(v4i *)(mine + u * BLOCK + (i >> 1) * 2048 + dst[i & 1]) = v[u][i];
+        // the wave's own LDS, whose operations run in order: only the compiler
+        // must not move the reads up (or the next block's writes)
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+#pragma unroll
+        for (int u = 0; u < N; ++u)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint8_t *s = mine + u * BLOCK + r * 128 + row_swizzle<128>(r, h * 4 + q) * 16;
+                const v4i wv = *(const v4i *)s;
+#pragma unroll
+                for (int i = 0; i < G; ++i)
+                    acc[i] = mfma16<T>(wv, *(const v4i *)(s + (1 + i) * 2048), acc[i]);
+            }
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    };
     const int64_t blocks = g.kbytes >> 7;
     int64_t b = wave;
-    for (; b + (U - 1) * W < blocks; b += U * W) {
-        v4i wv[2 * U], xv[2 * U][G];
-#pragma unroll
-        for (int u = 0; u < 2 * U; ++u) {
-            const int64_t k = (b + (u >> 1) * W) * 128 + (u & 1) * 64;
-            wv[u] = load_piece<T>(wp + k);
-#pragma unroll
-            for (int i = 0; i < G; ++i)
-                xv[u][i] = load_piece<T>(xp[i] + k);
-        }
-#pragma unroll
-        for (int u = 0; u < 2 * U; ++u)
-#pragma unroll
-            for (int i = 0; i < G; ++i)
-                acc[i] = mfma16<T>(wv[u], xv[u][i], acc[i]);
-    }
-    for (; b < blocks; b += W) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const v4i wv = load_piece<T>(wp + b * 128 + u * 64);
-#pragma unroll
-            for (int i = 0; i < G; ++i)
-                acc[i] = mfma16<T>(wv, load_piece<T>(xp[i] + b * 128 + u * 64), acc[i]);
-        }
-    }
-    if (b == blocks) {  // the wave whose turn the last, partial block is
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int64_t k = b * 128 + u * 64;
-            const int64_t valid = g.kbytes - k - q;
-            const v4i wv = load_piece_tail<T>(wp + k, valid);
-#pragma unroll
-            for (int i = 0; i < G; ++i)
-                acc[i] = mfma16<T>(wv, load_piece_tail<T>(xp[i] + k, valid), acc[i]);
-        }
-    }
+    for (; b + (U - 1) * W < blocks; b += U * W)
+        blocks_at(Size<U>{}, Size<0>{}, b);
+    for (; b < blocks; b += W)
+        blocks_at(Size<1>{}, Size<0>{}, b);
+    if (b == blocks)  // the wave whose turn the last, partial block is
+        blocks_at(Size<1>{}, Size<1>{}, b);
 
+    __syncthreads();
+    acc_t(*red)[G][64] = (acc_t(*)[G][64])smem;
 #pragma unroll
     for (int i = 0; i < G; ++i)
         red[wave][i][lane] = acc[i];
     __syncthreads();
-
     skinny_finish<T, G, 1, W>(g, red, n0);
 }
 

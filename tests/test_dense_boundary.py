@@ -187,7 +187,9 @@ def test_workspace_is_checked():
     assert status == "CONV_I8_OK" and need >= (64 + 48) * 33 * 2
     for ws, n in ((FAKE, need - 1), (FAKE + 64, need), (None, need)):
         assert dense.lib.dense_linear(args, ws, n, None) != 0
-    args = norm_backward()
+    assert size("dense_layer_norm_backward", norm_backward()) == ("CONV_I8_OK", 0)  # a few rows need none
+    m = mat(5000, 32, BF16)
+    args = norm_backward(dy=m, x=m, dx=m, mean=vec(5000, FP32), rstd=vec(5000, FP32))
     status, need = size("dense_layer_norm_backward", args)
     assert status == "CONV_I8_OK" and need >= 2 * 32 * 4
     assert ci8.STATUS[dense.lib.dense_layer_norm_backward(args, FAKE, need - 1, None)] == "CONV_I8_ERR_WORKSPACE"
