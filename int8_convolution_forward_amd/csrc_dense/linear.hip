@@ -76,18 +76,25 @@ PackJob pack_job(const Operand &o, void *dst)
     return j;
 }
 
+// Both jobs of a launch; returns its workgroups.
+int64_t pack_jobs(const Operand &a, void *da, const Operand &b, void *db, PackArgs *p)
+{
+    p->job[0] = pack_job(a, da);
+    p->job[1] = pack_job(b, db);
+    const int64_t g0 = ceil_div(p->job[0].items, 256), g1 = ceil_div(p->job[1].items, 256);
+    p->first = (int)g0;
+    return g0 + g1;
+}
+
 bool launch_pack(const Operand &a, void *da, const Operand &b, void *db, hipStream_t stream)
 {
     PackArgs p;
-    p.job[0] = pack_job(a, da);
-    p.job[1] = pack_job(b, db);
-    const int64_t g0 = ceil_div(p.job[0].items, 256), g1 = ceil_div(p.job[1].items, 256);
-    if (g0 + g1 == 0)
+    const int64_t wgs = pack_jobs(a, da, b, db, &p);
+    if (wgs == 0)
         return true;
-    if (g0 + g1 > 0x7fffffff)
+    if (wgs > 0x7fffffff)
         return false;
-    p.first = (int)g0;
-    const dim3 grid((unsigned)(g0 + g1)), block(256);
+    const dim3 grid((unsigned)wgs), block(256);
     if (a.es == 1)
         hipLaunchKernelGGL(pack_kernel<uint8_t>, grid, block, 0, stream, p);
     else
@@ -105,19 +112,21 @@ struct GemmPlan {
 
 // Microseconds a product takes with a tile and a split: the stages of the CU
 // that has the most workgroups, what a round of workgroups costs besides
-// (filling the pipeline, the epilogue), the output's bytes, and for a split the
-// second launch and the pass over the partial sums.  The constants are a fit to
-// 200 measured times over 20 shapes from 40x100x8192 to 8192x8192x2048; the
-// tile it picks is 3 % slower than the best one at the mean.
+// (filling the pipeline, the epilogue; workgroups that share a CU hide it from
+// each other), the output's bytes, and for a split the second launch and the
+// pass over the partial sums.  The constants are a fit to measured times of 27
+// shapes from 64x1024x1024 to 8192x8192x2048, with which the tile it picks is
+// within 10 % of the best one.
 struct TileCost {
     double stage;  // us per 64 bytes of the inner dimension of one workgroup
     double round;  // us per round of workgroups
+    double out;    // us per 10^6 outputs
 };
 constexpr TileCost kCost[kTiles] = {
-    {0.536, 8.2},
-    {0.259, 4.4},
-    {0.089, 3.8},
-    {0.194, 4.8},
+    {0.536, 8.2, 0.45},
+    {0.259, 4.4, 0.45},
+    {0.089, 3.8, 0.90},
+    {0.194, 4.8, 0.45},
 };
 
 double gemm_cost(int tile, int64_t M, int64_t N, int64_t kbytes, int splits)
@@ -126,15 +135,42 @@ double gemm_cost(int tile, int64_t M, int64_t N, int64_t kbytes, int splits)
     const TileCost &c = kCost[tile];
     const int64_t wgs = ceil_div(M, t.tm) * ceil_div(N, t.tn) * splits;
     const int64_t per_cu = ceil_div(wgs, kCUs);
-    const double busy = (double)(per_cu * ceil_div(kbytes, 64 * splits)) * c.stage + c.round;
+    const double stages = (double)(per_cu * ceil_div(kbytes, 64 * splits)) * c.stage;
     const double rounds = (double)ceil_div(per_cu, t.occ) * c.round;
+    const double busy = t.occ == 1 ? stages + rounds : stages + c.round > rounds ? stages + c.round : rounds;
     const double mn = 1.0e-6 * (double)M * (double)N;
-    return (busy > rounds ? busy : rounds) + (splits > 1 ? 4.4 + 1.2 * mn * splits : 0.94 * mn);
+    return busy + (splits > 1 ? 4.4 + 1.2 * mn * splits : c.out * mn);
+}
+
+// The same of both gradients' products in one launch with tile kPairTile:
+// either all CUs work through both, or the longer reduction lasts longest.
+double pair_cost(int64_t M, int64_t N, int64_t K)
+{
+    const Tile &t = kTile[kPairTile];
+    const TileCost &c = kCost[kPairTile];
+    const double sx = (double)ceil_div(2 * N, 64), sw = (double)ceil_div(2 * M, 64);
+    const double all = (sx * (double)ceil_div(M, t.tm) + sw * (double)ceil_div(N, t.tm)) * (double)ceil_div(K, t.tn) / kCUs;
+    const double longest = sx > sw ? sx : sw;
+    return (all > longest ? all : longest) * c.stage + c.round + c.out * 1.0e-6 * (double)(M + N) * (double)K;
 }
 
 const char *forced_tile() { return getenv("CONV_I8_DENSE_TILE"); }
 
-void plan_gemm(int64_t M, int64_t N, int64_t K, int es, GemmPlan *p)
+void set_plan(int64_t M, int64_t N, int64_t K, int es, int tile, int splits, GemmPlan *p)
+{
+    const int64_t nstages = ceil_div(K * es, kStageBytes);
+    p->tile = tile;
+    p->tiles_m = (int)ceil_div(M, kTile[tile].tm);
+    p->tiles_n = (int)ceil_div(N, kTile[tile].tn);
+    p->nstages = (int)nstages;
+    p->kchunk = nstages > 0 ? (int)ceil_div(nstages, splits) : 0;
+    p->splits = nstages > 0 ? (int)ceil_div(nstages, p->kchunk) : 1;
+    p->part_ld = (int)round_up(N, 8);
+    p->part_bytes = p->splits > 1 ? round_up((int64_t)p->splits * M * p->part_ld * 4, kWsAlign) : 0;
+}
+
+// Returns the microseconds expected.
+double plan_gemm(int64_t M, int64_t N, int64_t K, int es, GemmPlan *p)
 {
     const int64_t nstages = ceil_div(K * es, kStageBytes);
     int best = 0, best_s = 1;
@@ -168,14 +204,8 @@ void plan_gemm(int64_t M, int64_t N, int64_t K, int es, GemmPlan *p)
                 break;
         }
     }
-    p->tile = best;
-    p->tiles_m = (int)ceil_div(M, kTile[best].tm);
-    p->tiles_n = (int)ceil_div(N, kTile[best].tn);
-    p->nstages = (int)nstages;
-    p->kchunk = nstages > 0 ? (int)ceil_div(nstages, best_s) : 0;
-    p->splits = nstages > 0 ? (int)ceil_div(nstages, p->kchunk) : 1;
-    p->part_ld = (int)round_up(N, 8);
-    p->part_bytes = p->splits > 1 ? round_up((int64_t)p->splits * M * p->part_ld * 4, kWsAlign) : 0;
+    set_plan(M, N, K, es, best, best_s, p);
+    return least;
 }
 
 bool grid_fits(const GemmPlan &p)
@@ -430,8 +460,7 @@ struct BackwardPlan {
     GemmPlan dx, dw;
     int64_t part_bytes = 0, ws_bytes = 0;
 
-    // Both products go out in one launch.  The same tile and no split, so each
-    // is computed as it would be alone.
+    // Both products go out in one launch.
     bool pair() const
     {
         return want_dx && want_dw && dx.tile == kPairTile && dw.tile == kPairTile && dx.splits == 1 && dw.splits == 1 &&
@@ -528,6 +557,7 @@ conv_i8_status_t analyze(const dense_linear_backward_t *args, BackwardPlan *p)
     p->gt.cols = true;
     p->gt.dim = p->N;
     p->gt.inner = p->M;
+    double apart = 0.0;
     if (p->want_dx) {
         p->wb.src = d.w.ptr;
         p->wb.rs = d.w.col_stride;
@@ -537,7 +567,7 @@ conv_i8_status_t analyze(const dense_linear_backward_t *args, BackwardPlan *p)
         plan_operand(&p->wb, false, true);
         DENSE_TRY(check_reach(p->ga));
         DENSE_TRY(check_reach(p->wb));
-        plan_gemm(p->M, p->K, p->N, 2, &p->dx);
+        apart += plan_gemm(p->M, p->K, p->N, 2, &p->dx);
         if (!grid_fits(p->dx))
             return CONV_I8_ERR_UNSUPPORTED;
         p->part_bytes = p->dx.part_bytes;
@@ -551,7 +581,13 @@ conv_i8_status_t analyze(const dense_linear_backward_t *args, BackwardPlan *p)
         plan_operand(&p->xb, false, true);
         DENSE_TRY(check_reach(p->gt));
         DENSE_TRY(check_reach(p->xb));
-        plan_gemm(p->N, p->K, p->M, 2, &p->dw);
+        apart += plan_gemm(p->N, p->K, p->M, 2, &p->dw);
+        // apart: a launch more, and the bias gradient's (320x400x7312: 26 us apart, 21 paired)
+        if (p->want_dx && !forced_tile() && pair_cost(p->M, p->N, p->K) < apart + 4.0) {
+            set_plan(p->M, p->K, p->N, 2, kPairTile, 1, &p->dx);
+            set_plan(p->N, p->K, p->M, 2, kPairTile, 1, &p->dw);
+            p->part_bytes = 0;
+        }
         if (!grid_fits(p->dw))
             return CONV_I8_ERR_UNSUPPORTED;
         if (p->dw.part_bytes > p->part_bytes)
@@ -562,17 +598,15 @@ conv_i8_status_t analyze(const dense_linear_backward_t *args, BackwardPlan *p)
 }
 
 template <typename T>
-void launch_act_grad(int64_t act, dim3 grid, const ActGradArgs &a, hipStream_t stream)
+void launch_prepare(int64_t act, dim3 grid, const ActGradArgs &a, const PackArgs &pack, hipStream_t stream)
 {
-    const dim3 block(256);
+    auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, a, pack); };
     switch (act) {
-    case DENSE_ACT_RELU: hipLaunchKernelGGL((act_grad_kernel<T, DENSE_ACT_RELU>), grid, block, 0, stream, a); break;
-    case DENSE_ACT_GELU: hipLaunchKernelGGL((act_grad_kernel<T, DENSE_ACT_GELU>), grid, block, 0, stream, a); break;
-    case DENSE_ACT_GELU_TANH:
-        hipLaunchKernelGGL((act_grad_kernel<T, DENSE_ACT_GELU_TANH>), grid, block, 0, stream, a);
-        break;
-    case DENSE_ACT_SILU: hipLaunchKernelGGL((act_grad_kernel<T, DENSE_ACT_SILU>), grid, block, 0, stream, a); break;
-    default: hipLaunchKernelGGL((act_grad_kernel<T, DENSE_ACT_NONE>), grid, block, 0, stream, a); break;
+    case DENSE_ACT_RELU: launch(act_grad_kernel<T, DENSE_ACT_RELU>); break;
+    case DENSE_ACT_GELU: launch(act_grad_kernel<T, DENSE_ACT_GELU>); break;
+    case DENSE_ACT_GELU_TANH: launch(act_grad_kernel<T, DENSE_ACT_GELU_TANH>); break;
+    case DENSE_ACT_SILU: launch(act_grad_kernel<T, DENSE_ACT_SILU>); break;
+    default: launch(act_grad_kernel<T, DENSE_ACT_NONE>); break;
     }
 }
 
@@ -596,11 +630,17 @@ conv_i8_status_t run_backward(const BackwardPlan &p, void *ws, hipStream_t strea
         a.ldg = p.ldg;
         a.colsum = p.want_db ? (float *)sums : nullptr;
         a.sum_ld = p.sum_ld;
-        const dim3 grid((unsigned)ceil_div(p.N, 512), (unsigned)p.row_blocks);
+        a.strips = (int)ceil_div(p.N, 512);
+        a.blocks = a.strips * p.row_blocks;
+        PackArgs pack;
+        const int64_t wgs = a.blocks + pack_jobs(p.wb, pw, p.xb, px, &pack);
+        if (wgs > 0x7fffffff)
+            return CONV_I8_ERR_HIP;
+        const dim3 grid((unsigned)wgs);
         if (dt == DENSE_BF16)
-            launch_act_grad<bf16>(d.activation, grid, a, stream);
+            launch_prepare<bf16>(d.activation, grid, a, pack, stream);
         else
-            launch_act_grad<f16>(d.activation, grid, a, stream);
+            launch_prepare<f16>(d.activation, grid, a, pack, stream);
         if (hipGetLastError() != hipSuccess)
             return CONV_I8_ERR_HIP;
     }
@@ -614,7 +654,7 @@ conv_i8_status_t run_backward(const BackwardPlan &p, void *ws, hipStream_t strea
         c.out0 = const_cast<void *>(d.dbias.ptr);
         c.dt = (int)dt;
     }
-    if (!launch_pack(p.wb, pw, p.xb, px, stream))
+    if (!p.pass && !launch_pack(p.wb, pw, p.xb, px, stream))
         return CONV_I8_ERR_HIP;
     const void *gp = p.write_g ? (const void *)g : d.dy.ptr;
     Epilogue e;

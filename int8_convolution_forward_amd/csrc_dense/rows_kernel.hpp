@@ -27,13 +27,13 @@ struct PackArgs {
 // One thread copies one chunk; both operands of a product go in one launch.
 // U is an unsigned integer of the element's size.
 template <typename U>
-__global__ __launch_bounds__(256) void pack_kernel(const PackArgs a)
+__device__ __forceinline__ void pack_chunk(const PackArgs &a, int block)
 {
     constexpr int E = 16 / sizeof(U);
     struct __attribute__((packed, aligned(sizeof(U)))) Piece { U e[E]; };
-    const bool second = (int)blockIdx.x >= a.first;
+    const bool second = block >= a.first;
     const PackJob &j = a.job[second];
-    const int64_t i = (int64_t)(second ? blockIdx.x - a.first : blockIdx.x) * 256 + threadIdx.x;
+    const int64_t i = (int64_t)(second ? block - a.first : block) * 256 + threadIdx.x;
     if (i >= j.items)
         return;
     // a 64-bit division costs more than the copy
@@ -51,6 +51,12 @@ __global__ __launch_bounds__(256) void pack_kernel(const PackArgs a)
     *(v4i *)((U *)j.dst + i * E) = __builtin_bit_cast(v4i, p);
 }
 
+template <typename U>
+__global__ __launch_bounds__(256) void pack_kernel(const PackArgs a)
+{
+    pack_chunk<U>(a, blockIdx.x);
+}
+
 // g = dy act'(z), written with a row pitch of whole 16-byte chunks (zeros past
 // N), and column sums of the unrounded g over a block of rows.
 struct ActGradArgs {
@@ -58,6 +64,7 @@ struct ActGradArgs {
     int64_t ldy, ldz;
     int M, N;
     int rows;                 // rows per workgroup
+    int strips, blocks;       // workgroups along a row, and of this pass
     void *g;                  // null: only the column sums
     int64_t ldg;
     float *colsum;            // [row block][sum_ld], or null
@@ -66,15 +73,20 @@ struct ActGradArgs {
 
 // A wave takes 512 columns (eight per lane) of every fourth row of its block,
 // so that each load is one contiguous 1 KiB; the four waves' column sums are
-// added through LDS in order.
+// added through LDS in order.  The workgroups after those copy operands.
 template <typename T, int ACT>
-__global__ __launch_bounds__(256) void act_grad_kernel(const ActGradArgs a)
+__global__ __launch_bounds__(256) void act_grad_kernel(const ActGradArgs a, const PackArgs pack)
 {
+    if ((int)blockIdx.x >= a.blocks) {
+        pack_chunk<uint16_t>(pack, blockIdx.x - a.blocks);
+        return;
+    }
+    const int rb = blockIdx.x / a.strips, strip = blockIdx.x - rb * a.strips;
     __shared__ float red[4][512];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int n = blockIdx.x * 512 + lane * 8;
+    const int n = strip * 512 + lane * 8;
     const int cnt = a.N - n;
-    const int m0 = blockIdx.y * a.rows, m1 = min(a.M, m0 + a.rows);
+    const int m0 = rb * a.rows, m1 = min(a.M, m0 + a.rows);
     float sum[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -136,7 +148,7 @@ __global__ __launch_bounds__(256) void act_grad_kernel(const ActGradArgs a)
         for (; m < m1; m += 4)
             some(form, Size<1>{}, m);
     };
-    if ((int)blockIdx.x * 512 + 512 <= a.N)
+    if (strip * 512 + 512 <= a.N)
         rows(Size<2>{});
     else if (a.N % 8 == 0)
         rows(Size<1>{});
@@ -151,8 +163,8 @@ __global__ __launch_bounds__(256) void act_grad_kernel(const ActGradArgs a)
         red[wave][lane * 8 + i] = sum[i];
     __syncthreads();
     for (int c = threadIdx.x; c < 512; c += 256)
-        if (blockIdx.x * 512 + c < a.N)
-            a.colsum[blockIdx.y * a.sum_ld + blockIdx.x * 512 + c] =
+        if (strip * 512 + c < a.N)
+            a.colsum[rb * a.sum_ld + strip * 512 + c] =
                 (red[0][c] + red[1][c]) + (red[2][c] + red[3][c]);
 }
 
