@@ -70,7 +70,7 @@ def bind_command(out: str) -> list:
     return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1",
             "-DUSE_ROCM=1", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
             *[f for i in include for f in ("-I", i)], DENSE_BIND_SOURCE, "-o", out, "-L", os.path.join(base, "lib"),
-            "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_hip"]
+            "-ltorch_python", "-ltorch_hip", "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_hip"]
 
 
 def build(verbose: bool = False, dense_only: bool = False) -> str:

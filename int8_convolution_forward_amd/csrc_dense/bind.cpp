@@ -10,6 +10,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/hip/EmptyTensor.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -120,9 +121,10 @@ void check(long code)
         throw Stop{code};
 }
 
+// torch's allocator without its dispatcher
 at::Tensor empty(at::IntArrayRef shape, at::ScalarType t, c10::Device d)
 {
-    return at::empty(shape, at::TensorOptions().dtype(t).device(d));
+    return at::Tensor(at::detail::empty_cuda(shape, t, d, std::nullopt));
 }
 
 // x's leading shape with another last dim
