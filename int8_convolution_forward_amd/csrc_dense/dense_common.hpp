@@ -383,22 +383,41 @@ __device__ __forceinline__ unsigned lds_address(const void *p)
     return (unsigned)(unsigned long long)(lds_void *)p;
 }
 
-template <int WIDTH>
-__device__ __forceinline__ float wave_sum(float v)
+// Another lane's value, by a lane permutation that costs no trip through LDS
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v)
 {
-#pragma unroll
-    for (int o = WIDTH / 2; o >= 1; o >>= 1)
-        v += __shfl_xor(v, o, 64);
-    return v;
+    const int i = __builtin_bit_cast(int, v);
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(i, i, CTRL, 0xf, 0xf, false));
 }
 
-template <int WIDTH>
+__device__ __forceinline__ float lane_value(float v, int lane)
+{
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+}
+
+// f over the 64 lanes of a wave, the result in all of them: neighbours, pairs,
+// halves of eight and of sixteen lanes exchanged, then the four rows of sixteen.
+// (By shuffles, which go through LDS, a layer norm of 4096 columns spends more
+// time on its reductions than on its arithmetic.)
+template <typename F>
+__device__ __forceinline__ float wave_reduce(float v, F f)
+{
+    v = f(v, dpp<0xB1>(v));   // lanes 1 0 3 2 of each four
+    v = f(v, dpp<0x4E>(v));   // lanes 2 3 0 1
+    v = f(v, dpp<0x141>(v));  // eight lanes mirrored
+    v = f(v, dpp<0x140>(v));  // sixteen lanes mirrored
+    return f(f(lane_value(v, 0), lane_value(v, 16)), f(lane_value(v, 32), lane_value(v, 48)));
+}
+
+__device__ __forceinline__ float wave_sum(float v)
+{
+    return wave_reduce(v, [](float a, float b) { return a + b; });
+}
+
 __device__ __forceinline__ float wave_max(float v)
 {
-#pragma unroll
-    for (int o = WIDTH / 2; o >= 1; o >>= 1)
-        v = fmaxf(v, __shfl_xor(v, o, 64));
-    return v;
+    return wave_reduce(v, [](float a, float b) { return fmaxf(a, b); });
 }
 
 // Workgroups are dealt round-robin to the 8 XCDs; each XCD gets one contiguous

@@ -88,9 +88,11 @@ void launch_norm(const NormArgs &a, hipStream_t s)
     else if (D <= 4096)
         launch_one<T, 256, 2, Q8>(a, s);
     else if (D <= 8192)
-        launch_one<T, 256, 4, Q8>(a, s);
+        Q8 ? launch_one<T, 512, 2, Q8>(a, s) : launch_one<T, 256, 4, Q8>(a, s);
     else if (D <= 16384)
         launch_one<T, 512, 4, Q8>(a, s);
+    else if (D <= 32768)
+        launch_one<T, 1024, 4, Q8>(a, s);
     else
         launch_one<T, 1024, 8, Q8>(a, s);
 }
@@ -104,7 +106,7 @@ struct BackPlan {
     int64_t part_ld = 0, ws_bytes = 0;
 };
 
-constexpr int back_threads(int64_t D) { return D <= 512 ? 64 : D <= 4096 ? 256 : D <= 8192 ? 512 : 1024; }
+constexpr int back_threads(int64_t D) { return D <= 1024 ? 64 : D <= 4096 ? 256 : D <= 8192 ? 512 : 1024; }
 
 conv_i8_status_t analyze(const dense_layer_norm_backward_t *args, BackPlan *p)
 {
@@ -150,7 +152,7 @@ conv_i8_status_t analyze(const dense_layer_norm_backward_t *args, BackPlan *p)
         const int64_t want = ceil_div(p->M, 4 * rows);
         p->wgs = (int)(want < most ? want : most);
     }
-    p->once = p->sums && p->M > 0 && p->M <= kOnceRows && back_in_registers(p->D);
+    p->once = p->sums && p->M > 0 && p->M <= once_rows((int)size_of(dt)) && back_in_registers(p->D);
     p->ws_bytes = p->sums && !p->once ? round_up((int64_t)p->wgs * 2 * p->part_ld * 4, kWsAlign) : 0;
     return CONV_I8_OK;
 }
@@ -187,6 +189,8 @@ void launch_back(const NormBackArgs &a, int wgs, hipStream_t s)
                                0, s, a, (int)ceil_div(a.M, wgs));
     } else if (D <= 512) {
         launch_back_one<T, 64, 1, 1>(a, wgs, s);
+    } else if (D <= 1024) {
+        launch_back_one<T, 64, 2, 1>(a, wgs, s);
     } else if (D <= 2048) {
         launch_back_one<T, 256, 1, 1>(a, wgs, s);
     } else if (D <= 4096) {

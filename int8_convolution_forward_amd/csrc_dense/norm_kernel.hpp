@@ -10,7 +10,7 @@
 // What they need is bytes in flight.  A thread group walks over rows and loads
 // the next one, in the form it has in memory, before it works on the present
 // one, and a load has no condition per lane (TAIL: D is no multiple of eight).
-// 16384 x 4096 BF16: forward 50 us (5.3 TB/s; a copy of the same bytes reaches 5.9), with a
+// 16384 x 4096 BF16: forward 45 us (6.0 TB/s; a copy of the same bytes reaches 5.9), with a
 // workgroup per row that loads, reduces and stores in turn 82; backward 76 us
 // (5.2 TB/s), without the next row's loads 133.
 #pragma once
@@ -34,7 +34,7 @@ struct NormArgs {
 template <int P, bool MAX = false>
 __device__ __forceinline__ float row_reduce(float v, float *red, int set)
 {
-    v = MAX ? wave_max<64>(v) : wave_sum<64>(v);
+    v = MAX ? wave_max(v) : wave_sum(v);
     if constexpr (P > 64) {
         constexpr int NW = P / 64;
         float *r = red + set * NW;
@@ -50,12 +50,20 @@ __device__ __forceinline__ float row_reduce(float v, float *red, int set)
 }
 
 // Scale of an INT8 row whose largest magnitude is `top`, and its inverse (0 for
-// a row of zeros).  A row with a value that is not finite gets the scale NaN;
-// callers pass infinity for a NaN, because a maximum skips NaN.
+// a row of zeros, finite for one whose values are below the normal range).  A
+// row with a value that is not finite gets the scale NaN; callers pass infinity
+// for a NaN, because a maximum skips NaN.
 __device__ __forceinline__ float quant_scale(float top, float &inv)
 {
-    inv = top > 0.0f ? 127.0f / top : 0.0f;
+    inv = top > 0.0f ? fminf(127.0f / top, 3.4028234e38f) : 0.0f;
     return top < INFINITY ? top / 127.0f : __builtin_nanf("");
+}
+
+// v * inv, at most 127 in magnitude, rounded half to even, in the low byte: the
+// sum with 1.5 2^23 has the integer in its last bits.
+__device__ __forceinline__ int8_t quantise(float v, float inv)
+{
+    return (int8_t)__builtin_bit_cast(int, __builtin_fmaf(v, inv, 12582912.0f));
 }
 
 // columns of a row of D that wave `wave` of its P threads holds
@@ -130,7 +138,7 @@ __device__ __forceinline__ void row_moments(float (&v)[V][8], int D, int t, floa
 #pragma unroll
         for (int k = 0; k < 8; ++k)
             s += v[i][k];
-    mean = wave_sum<64>(s) / cols;
+    mean = wave_sum(s) / cols;
     s = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -141,7 +149,7 @@ __device__ __forceinline__ void row_moments(float (&v)[V][8], int D, int t, floa
             s = (i + 1) * P * 8 <= D || k < cnt ? __builtin_fmaf(c, c, s) : s;
         }
     }
-    m2 = wave_sum<64>(s);
+    m2 = wave_sum(s);
     if constexpr (P > 64) {
         constexpr int NW = P / 64;
         if ((threadIdx.x & 63) == 0)
@@ -211,8 +219,7 @@ __global__ __launch_bounds__(norm_threads(P)) void norm_kernel(const NormArgs a)
             if (a.rstd)
                 a.rstd[m] = rstd;
         }
-        float top = 0.0f;
-        bool nan = false;
+        float top = 0.0f, bad = 0.0f;  // bad: NaN if a value is not finite
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int c = (i * P + t) * 8, cnt = a.D - c;
@@ -229,10 +236,9 @@ __global__ __launch_bounds__(norm_threads(P)) void norm_kernel(const NormArgs a)
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 v[i][k] = __builtin_fmaf((v[i][k] - mean) * rstd, wv[k], bv[k]);
-                if constexpr (Q8) {
-                    const float u = whole || k < cnt ? v[i][k] : 0.0f;
-                    top = fmaxf(top, fabsf(u));
-                    nan |= u != u;
+                if constexpr (Q8) {  // past the row's end weight and bias, and so the value, are 0
+                    top = fmaxf(top, fabsf(v[i][k]));
+                    bad = __builtin_fmaf(v[i][k], 0.0f, bad);
                 }
             }
             if constexpr (!Q8) {
@@ -245,7 +251,7 @@ __global__ __launch_bounds__(norm_threads(P)) void norm_kernel(const NormArgs a)
         }
         if constexpr (Q8) {
             float inv;
-            const float scale = quant_scale(row_reduce<P, true>(nan ? INFINITY : top, redq[set], 0), inv);
+            const float scale = quant_scale(row_reduce<P, true>(bad == 0.0f ? top : INFINITY, redq[set], 0), inv);
             if (t == 0)
                 a.scale[m] = scale;
 #pragma unroll
@@ -255,7 +261,7 @@ __global__ __launch_bounds__(norm_threads(P)) void norm_kernel(const NormArgs a)
                 struct __attribute__((packed)) Q { int8_t e[8]; } q;
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                    q.e[k] = (int8_t)(int)__builtin_rintf(fminf(fmaxf(v[i][k] * inv, -127.0f), 127.0f));
+                    q.e[k] = quantise(v[i][k], inv);
                 int8_t *y = (int8_t *)a.y + m * a.ldy + c;
                 if (whole || (TAIL ? cnt >= 8 : cnt > 0)) {
                     *(Q *)y = q;
@@ -353,7 +359,7 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(const NormArgs a)
 #pragma unroll
             for (int k = 0; k < 8; ++k)
                 if (k < cnt)
-                    y[k] = (int8_t)(int)__builtin_rintf(fminf(fmaxf(v[k] * inv, -127.0f), 127.0f));
+                    y[k] = quantise(v[k], inv);
         }
     }
 }
@@ -443,8 +449,8 @@ __device__ __forceinline__ void backward_rows(const NormBackArgs &a, int block, 
                 }
             }
         }
-        s1 = wave_sum<64>(s1);
-        s2 = wave_sum<64>(s2);
+        s1 = wave_sum(s1);
+        s2 = wave_sum(s2);
         if constexpr (P > 64) {
             if ((threadIdx.x & 63) == 0)
                 red[set][threadIdx.x >> 6] = make_float2(s1, s2);
@@ -524,12 +530,14 @@ __global__ __launch_bounds__(norm_threads(P)) void norm_backward_kernel(const No
     backward_rows<T, P, V, AHEAD, TAIL, SUMS>(a, blockIdx.x, gridDim.x);
 }
 
-// Everything in one launch, for up to kOnceRows rows: the first workgroups sum 32
-// columns each over all rows, four threads to a row, the others take one row per
-// thread group.  x and dy are read twice, the second time from cache; what it
-// saves is the partial sums on their way out and back, and a launch, whose 4 us
-// are half of such a call.
-constexpr int64_t kOnceRows = 1024;
+// Everything in one launch, for few rows: the first workgroups sum 32 columns
+// each over all rows, four threads to a row, the others take one row per thread
+// group.  x and dy are read twice, the second time from cache; what it saves is
+// the partial sums on their way out and back, and a launch.  With many rows the
+// walk down the columns lasts longest, in 16-bit types sooner, where a row's 32
+// columns are half a cache line: 256 x 4096 BF16 5.2 us (two launches 10.4),
+// 512 x 4096 9.7 (11.9), 1024 x 4096 18.8 (15.0); 1003 x 1537 FP32 11.4 (12.3).
+constexpr int64_t once_rows(int value_size) { return value_size == 4 ? 1024 : 640; }
 constexpr int kOnceCols = 32;
 
 template <typename T, int P, int V, bool TAIL>
@@ -539,7 +547,7 @@ __global__ __launch_bounds__(norm_threads(P)) void norm_backward_once_kernel(con
         backward_rows<T, P, V, 0, TAIL, false>(a, blockIdx.x - col_blocks, gridDim.x - col_blocks);
         return;
     }
-    constexpr int LANES = kOnceCols / 8, G = norm_threads(P) / LANES, U = 4;
+    constexpr int LANES = kOnceCols / 8, G = norm_threads(P) / LANES, U = 16 / sizeof(T);
     __shared__ float sums[2][norm_threads(P) / 64][kOnceCols];
     const int c = blockIdx.x * kOnceCols + (threadIdx.x % LANES) * 8, grp = threadIdx.x / LANES;
     float sw[8] = {}, sb[8] = {};
