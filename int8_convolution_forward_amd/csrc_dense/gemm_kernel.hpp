@@ -53,7 +53,7 @@ struct GemmArgs {
     int M, N;
     int kbytes;            // inner dimension in bytes of a rows-form operand, a multiple of 16
     int K;                 // inner dimension in elements
-    int nstages;           // stages of 64 bytes
+    int nstages;           // stages of kStageBytes
     int kchunk;            // stages per split
     int tiles_m, tiles_n, tiles;
     int group;             // row tiles per group of the tile order

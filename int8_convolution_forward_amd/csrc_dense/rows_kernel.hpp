@@ -58,7 +58,11 @@ __global__ __launch_bounds__(256) void pack_kernel(const PackArgs a)
 }
 
 // g = dy act'(z), written with a row pitch of whole 16-byte chunks (zeros past
-// N), and column sums of the unrounded g over a block of rows.
+// N), and column sums of the unrounded g over a block of rows.  g is rounded to
+// the operands' type, since the matrix unit takes both of a product's operands in
+// it; the rounding is of the size of dy's and z's own.
+// 8192 x 8192 BF16 with the slope of gelu's tanh form: 75 us (403 MB, 5.4 TB/s);
+// with loads of one row at a time, each under a condition, 100.
 struct ActGradArgs {
     const void *dy, *z;       // z null: g = dy
     int64_t ldy, ldz;

@@ -30,8 +30,8 @@ from . import ConvI8Error, _on_one_gpu, build as _build, status_string
 __all__ = ["linear", "linear_plan", "linear_backward", "linear_backward_plan", "layer_norm", "layer_norm_i8",
            "layer_norm_backward", "ACTIVATIONS", "DENSE_LIB_PATH"]
 
-# CONV_I8_DENSE_LIB names another build of the library (the host-sanitizer
-# test loads a host-only build with AddressSanitizer through it)
+# CONV_I8_DENSE_LIB names another build of the library (the sanitizer test
+# loads a host-only build with AddressSanitizer through it)
 DENSE_LIB_PATH = os.environ.get("CONV_I8_DENSE_LIB") or _build.DENSE_LIB
 
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
