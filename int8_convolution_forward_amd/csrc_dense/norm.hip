@@ -53,9 +53,10 @@ conv_i8_status_t analyze(const dense_layer_norm_t *args, dense_layer_norm_t *d)
 }
 
 // Two rows for each thread group once there are more than 1024 workgroups: the
-// second one's loads then overlap the first one's work, and the card still
-// balances itself (16384 x 4096 BF16: 48.6 us, one row each 55.9, sixteen 52.3).
-// Wide groups (512 threads) hold fewer workgroups on a CU and take more rows.
+// second one's loads overlap the first one's work, and the card still balances
+// itself (16384 x 4096 BF16: two rows 50.0 us, one 49.9, four 53.8, sixteen 53.2).
+// Wide groups (512 threads) hold fewer workgroups on a CU and take more rows
+// (4096 x 16384: four rows 55.4 us, two 59.3, one 74.4).
 template <typename T, int P, int V, bool Q8>
 void launch_one(const NormArgs &a, hipStream_t s)
 {
@@ -106,7 +107,7 @@ struct BackPlan {
     int64_t part_ld = 0, ws_bytes = 0;
 };
 
-constexpr int back_threads(int64_t D) { return D <= 1024 ? 64 : D <= 4096 ? 256 : D <= 8192 ? 512 : 1024; }
+constexpr int back_threads(int64_t D) { return D <= 1024 ? 64 : D <= 2048 ? 256 : D <= 8192 ? 512 : 1024; }
 
 conv_i8_status_t analyze(const dense_layer_norm_backward_t *args, BackPlan *p)
 {
@@ -146,7 +147,9 @@ conv_i8_status_t analyze(const dense_layer_norm_backward_t *args, BackPlan *p)
         const int64_t blocks = p->M < 64 ? p->M : 64;
         p->wgs = (int)(p->M > 0 ? ceil_div(p->M, ceil_div(p->M, blocks)) : 0);
     } else {
-        // eight waves or more on a CU, and at least four rows for each group of threads
+        // eight waves or more on a CU, and at least four rows for each group of threads: more
+        // workgroups leave more partial sums (16384 x 4096 BF16: 256 workgroups of 512 threads
+        // 74.0 us, 512 of 256 76.2, 512 of 512 75.9)
         const int threads = norm_threads(back_threads(p->D));
         const int rows = threads / back_threads(p->D), most = threads <= 256 ? 2 * kCUs : kCUs;
         const int64_t want = ceil_div(p->M, 4 * rows);
@@ -194,7 +197,7 @@ void launch_back(const NormBackArgs &a, int wgs, hipStream_t s)
     } else if (D <= 2048) {
         launch_back_one<T, 256, 1, 1>(a, wgs, s);
     } else if (D <= 4096) {
-        launch_back_one<T, 256, 2, 1>(a, wgs, s);
+        launch_back_one<T, 512, 1, 1>(a, wgs, s);
     } else if (D <= 8192) {
         launch_back_one<T, 512, 2, 1>(a, wgs, s);
     } else {
