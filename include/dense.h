@@ -90,7 +90,14 @@ conv_i8_status_t dense_linear_workspace_size(const dense_linear_t *args, size_t 
  * workspace is not 256-byte aligned. */
 conv_i8_status_t dense_linear(const dense_linear_t *args, void *workspace, size_t bytes, void *stream);
 
-/* One line that says how the call would run.  Host-only. */
+/* One line that says how the call would run.  Host-only.
+ *
+ * For tests and measurements, the environment variable CONV_I8_DENSE_TILE names
+ * the tile of every product of the dense layer and its gradients ("256x256",
+ * "128x128", "64x64", "128x128d") and, after a slash, its split of the inner
+ * dimension (1 to 64; the largest that leaves each part four stages, if that is
+ * less).  The kernel for a few rows is then not used.  Any other value is
+ * CONV_I8_ERR_PARAM. */
 conv_i8_status_t dense_linear_plan(const dense_linear_t *args, char *buf, size_t len);
 
 /*

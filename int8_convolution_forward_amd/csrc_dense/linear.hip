@@ -157,7 +157,34 @@ double pair_cost(int64_t M, int64_t N, int64_t K)
     return (all > longest ? all : longest) * c.stage + c.round + c.out * 1.0e-6 * (double)(M + N) * (double)K;
 }
 
-const char *forced_tile() { return getenv("CONV_I8_DENSE_TILE"); }
+// CONV_I8_DENSE_TILE, for tests and sweeps: "128x128" names a tile for every
+// product, "128x128/4" a tile and a split.
+struct Forced {
+    bool on = false;
+    int tile = 0, split = 0;  // split 0: the plan's choice
+};
+
+conv_i8_status_t forced_tile(Forced *f)
+{
+    const char *s = getenv("CONV_I8_DENSE_TILE");
+    if (!s || !*s)
+        return CONV_I8_OK;
+    const char *slash = strchr(s, '/');
+    const size_t len = slash ? (size_t)(slash - s) : strlen(s);
+    while (f->tile < kTiles && (strlen(kTile[f->tile].name) != len || memcmp(kTile[f->tile].name, s, len) != 0))
+        ++f->tile;
+    if (f->tile == kTiles)
+        return CONV_I8_ERR_PARAM;
+    if (slash) {
+        char *end;
+        const long n = strtol(slash + 1, &end, 10);
+        if (end == slash + 1 || *end || n < 1 || n > 64)
+            return CONV_I8_ERR_PARAM;
+        f->split = (int)n;
+    }
+    f->on = true;
+    return CONV_I8_OK;
+}
 
 void set_plan(int64_t M, int64_t N, int64_t K, int es, int tile, int splits, GemmPlan *p)
 {
@@ -173,38 +200,35 @@ void set_plan(int64_t M, int64_t N, int64_t K, int es, int tile, int splits, Gem
 }
 
 // Returns the microseconds expected.
-double plan_gemm(int64_t M, int64_t N, int64_t K, int es, GemmPlan *p)
+double plan_gemm(int64_t M, int64_t N, int64_t K, int es, const Forced &forced, GemmPlan *p)
 {
     const int64_t nstages = ceil_div(K * es, kStageBytes);
+    if (forced.on && forced.split > 0) {
+        // of a product with fewer than four stages for each part, as many parts as have four
+        const int64_t most = nstages / 4 > 1 ? nstages / 4 : 1;
+        set_plan(M, N, K, es, forced.tile, (int)(forced.split < most ? forced.split : most), p);
+        return gemm_cost(forced.tile, M, N, K * es, p->splits);
+    }
     int best = 0, best_s = 1;
     double least = 1e30;
-    const char *force = forced_tile();  // "128x128" or "128x128/4": a tile and a split for tests and sweeps
     for (int t = 0; t < kTiles; ++t) {
-        int only_split = 0;
-        if (force) {
-            const size_t len = strlen(kTile[t].name);
-            if (strncmp(force, kTile[t].name, len) != 0 || (force[len] != 0 && force[len] != '/'))
-                continue;
-            only_split = force[len] == '/' ? atoi(force + len + 1) : 0;
-        }
+        if (forced.on && t != forced.tile)
+            continue;
         const int64_t tiles = ceil_div(M, kTile[t].tm) * ceil_div(N, kTile[t].tn);
         for (const int s : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
             // a split keeps eight stages, and two rounds of workgroups are enough
-            const int use = only_split > 0 ? (only_split < 64 ? only_split : 64) : s;
-            if (use > 1 && (nstages < (only_split ? 4 : 8) * use || (!only_split && tiles * use > 2 * kCUs * kTile[t].occ)))
+            if (s > 1 && (nstages < 8 * s || tiles * s > 2 * kCUs * kTile[t].occ))
                 break;
             // a deep ring pays in the first round of workgroups only (2048x4096x512: two rounds
             // 16.3 us, 128x128 14.0)
-            if (!force && kTile[t].deep && tiles * use > kCUs)
+            if (!forced.on && kTile[t].deep && tiles * s > kCUs)
                 break;
-            const double us = gemm_cost(t, M, N, K * es, use);
+            const double us = gemm_cost(t, M, N, K * es, s);
             if (us < least) {
                 least = us;
                 best = t;
-                best_s = use;
+                best_s = s;
             }
-            if (only_split > 0)
-                break;
         }
     }
     set_plan(M, N, K, es, best, best_s, p);
@@ -326,9 +350,11 @@ conv_i8_status_t analyze(const dense_linear_t *args, LinearPlan *p)
 
     if (p->M == 0 || p->N == 0)
         return CONV_I8_OK;
+    Forced forced;
+    DENSE_TRY(forced_tile(&forced));
     const int es = (int)size_of(dt);
     const bool x_rows = d.x.col_stride == 1 || p->K <= 1, w_rows = d.w.col_stride == 1 || p->K <= 1;
-    p->skinny = p->M <= kSkinnyRows && x_rows && w_rows && !forced_tile();
+    p->skinny = p->M <= kSkinnyRows && x_rows && w_rows && !forced.on;
     if (p->skinny) {
         p->aligned = (((uintptr_t)d.x.ptr | (uintptr_t)d.w.ptr) & 15) == 0 && p->K * es % 16 == 0 &&
                      (p->M <= 1 || d.x.row_stride * es % 16 == 0) && (p->N <= 1 || d.w.row_stride * es % 16 == 0);
@@ -355,7 +381,7 @@ conv_i8_status_t analyze(const dense_linear_t *args, LinearPlan *p)
     plan_operand(&p->b, true, es == 2);
     DENSE_TRY(check_reach(p->a));
     DENSE_TRY(check_reach(p->b));
-    plan_gemm(p->M, p->N, p->K, es, &p->gemm);
+    plan_gemm(p->M, p->N, p->K, es, forced, &p->gemm);
     if (!grid_fits(p->gemm))
         return CONV_I8_ERR_UNSUPPORTED;
     p->ws_bytes = p->a.pack_bytes + p->b.pack_bytes + p->gemm.part_bytes;
@@ -562,6 +588,8 @@ conv_i8_status_t analyze(const dense_linear_backward_t *args, BackwardPlan *p)
     p->gt.cols = true;
     p->gt.dim = p->N;
     p->gt.inner = p->M;
+    Forced forced;
+    DENSE_TRY(forced_tile(&forced));
     double apart = 0.0;
     if (p->want_dx) {
         p->wb.src = d.w.ptr;
@@ -572,7 +600,7 @@ conv_i8_status_t analyze(const dense_linear_backward_t *args, BackwardPlan *p)
         plan_operand(&p->wb, false, true);
         DENSE_TRY(check_reach(p->ga));
         DENSE_TRY(check_reach(p->wb));
-        apart += plan_gemm(p->M, p->K, p->N, 2, &p->dx);
+        apart += plan_gemm(p->M, p->K, p->N, 2, forced, &p->dx);
         if (!grid_fits(p->dx))
             return CONV_I8_ERR_UNSUPPORTED;
         p->part_bytes = p->dx.part_bytes;
@@ -586,9 +614,9 @@ conv_i8_status_t analyze(const dense_linear_backward_t *args, BackwardPlan *p)
         plan_operand(&p->xb, false, true);
         DENSE_TRY(check_reach(p->gt));
         DENSE_TRY(check_reach(p->xb));
-        apart += plan_gemm(p->N, p->K, p->M, 2, &p->dw);
+        apart += plan_gemm(p->N, p->K, p->M, 2, forced, &p->dw);
         // apart: a launch more, and the bias gradient's (320x400x7312: 26 us apart, 21 paired)
-        if (p->want_dx && !forced_tile() && pair_cost(p->M, p->N, p->K) < apart + 4.0) {
+        if (p->want_dx && !forced.on && pair_cost(p->M, p->N, p->K) < apart + 4.0) {
             set_plan(p->M, p->K, p->N, 2, kPairTile, 1, &p->dx);
             set_plan(p->N, p->K, p->M, 2, kPairTile, 1, &p->dw);
             p->part_bytes = 0;
