@@ -11,8 +11,8 @@ namespace dense {
 struct ColSumArgs {
     const float *part;
     int64_t ld;
-    int rows, cols;
-    int split, valid;
+    int rows;
+    int64_t cols, split, valid;
     void *out0, *out1;
     int dt;
 };
@@ -29,9 +29,9 @@ __device__ __forceinline__ void column_sums(const ColSumArgs &a, int block, floa
 {
     constexpr int G = kSumGroups, U = 8;
     const int c = threadIdx.x % COLS, grp = threadIdx.x / COLS;
-    const int col = block * COLS + c;
+    const int64_t col = (int64_t)block * COLS + c;
     const bool second = col >= a.split;
-    const int oc = second ? col - a.split : col;
+    const int64_t oc = second ? col - a.split : col;
     const bool live = col < a.cols && oc < a.valid;
     float s[U] = {};
     if (live) {
@@ -64,11 +64,24 @@ __device__ __forceinline__ void column_sums(const ColSumArgs &a, int block, floa
     }
 }
 
+// Workgroups of colsum_kernel: they walk over the columns where one each would
+// be more threads than a launch may have (2^32).
+inline dim3 colsum_grid(int64_t cols)
+{
+    const int64_t wgs = (cols + 31) / 32;
+    return dim3((unsigned)(wgs < (1 << 21) ? wgs : 1 << 21));
+}
+
 template <int COLS = 32>
 __global__ __launch_bounds__(COLS * kSumGroups) void colsum_kernel(const ColSumArgs a)
 {
     __shared__ float red[kSumGroups][COLS + 1];
-    column_sums<COLS>(a, blockIdx.x, red);
+    const int blocks = (int)((a.cols + COLS - 1) / COLS);
+    for (int b = blockIdx.x; b < blocks; b += gridDim.x) {
+        column_sums<COLS>(a, b, red);
+        if (b + (int)gridDim.x < blocks)
+            __syncthreads();  // the sums are read before the next columns overwrite them
+    }
 }
 
 }  // namespace dense

@@ -38,7 +38,7 @@ bool launch_gemm_pair_f16(const PairArgs &p, hipStream_t stream);
 template <typename T>
 bool launch_gemm_pair(const PairArgs &p, hipStream_t stream)
 {
-    const int sums = (p.sum.cols + 256 / kSumGroups - 1) / (256 / kSumGroups);
+    const int sums = (int)(p.sum.cols + 256 / kSumGroups - 1) / (256 / kSumGroups);
     const dim3 grid((unsigned)(p.dx.tiles + p.dw.tiles + sums)), block(256);
     hipLaunchKernelGGL((gemm_pair_kernel<T, 64, 64, 2, 2, 3, 3, 4, 3>), grid, block, 0, stream, p);
     return hipGetLastError() == hipSuccess;

@@ -15,8 +15,10 @@ inline int64_t size_of(int64_t dt)
     return dt == DENSE_INT8 ? 1 : dt == DENSE_FP32 ? 4 : is_half(dt) ? 2 : 0;
 }
 
-// Largest dim: indexes and grid sizes then stay within 32 bits.
+// Largest dim: indexes along it then stay within 32 bits.
 constexpr int64_t kMaxDim = (int64_t)1 << 30;
+// A launch has fewer than 2^32 threads.
+inline bool launch_fits(int64_t wgs, int threads) { return wgs < ((int64_t)1 << 32) / threads; }
 // Largest stride: a byte offset of kMaxDim rows then stays within 63 bits.
 constexpr int64_t kMaxStride = (int64_t)1 << 30;
 

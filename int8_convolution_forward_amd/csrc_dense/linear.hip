@@ -57,9 +57,14 @@ void plan_operand(Operand *o, bool allow_rows, bool allow_cols)
     }
 }
 
+// Workgroups that copy an operand.
+int64_t pack_wgs(const Operand &o) { return o.packed ? ceil_div((o.cols ? o.inner : o.dim) * (o.ld / 16), 256) : 0; }
+
 conv_i8_status_t check_reach(const Operand &o)
 {
-    return o.ld > (o.cols ? kMaxColBytes : kMaxRowBytes) ? CONV_I8_ERR_UNSUPPORTED : CONV_I8_OK;
+    if (o.ld > (o.cols ? kMaxColBytes : kMaxRowBytes) || !launch_fits(pack_wgs(o), 256))
+        return CONV_I8_ERR_UNSUPPORTED;
+    return CONV_I8_OK;
 }
 
 PackJob pack_job(const Operand &o, void *dst)
@@ -84,9 +89,8 @@ int64_t pack_jobs(const Operand &a, void *da, const Operand &b, void *db, PackAr
 {
     p->job[0] = pack_job(a, da);
     p->job[1] = pack_job(b, db);
-    const int64_t g0 = ceil_div(p->job[0].items, 256), g1 = ceil_div(p->job[1].items, 256);
-    p->first = (int)g0;
-    return g0 + g1;
+    p->first = (int)pack_wgs(a);
+    return pack_wgs(a) + pack_wgs(b);
 }
 
 bool launch_pack(const Operand &a, void *da, const Operand &b, void *db, hipStream_t stream)
@@ -95,8 +99,6 @@ bool launch_pack(const Operand &a, void *da, const Operand &b, void *db, hipStre
     const int64_t wgs = pack_jobs(a, da, b, db, &p);
     if (wgs == 0)
         return true;
-    if (wgs > 0x7fffffff)
-        return false;
     const dim3 grid((unsigned)wgs), block(256);
     if (a.es == 1)
         hipLaunchKernelGGL(pack_kernel<uint8_t>, grid, block, 0, stream, p);
@@ -235,9 +237,10 @@ double plan_gemm(int64_t M, int64_t N, int64_t K, int es, const Forced &forced, 
     return least;
 }
 
-bool grid_fits(const GemmPlan &p)
+bool grid_fits(const GemmPlan &p, int64_t M)
 {
-    return (int64_t)p.tiles_m * p.tiles_n < ((int64_t)1 << 30) && p.splits <= 65535;
+    return launch_fits((int64_t)p.tiles_m * p.tiles_n, 256) &&
+           (p.splits <= 1 || launch_fits(ceil_div(M * (p.part_ld / 8), 256), 256));
 }
 
 // C[M, N] = A B^T over K with the epilogue.  kbytes: inner bytes of a rows-form
@@ -288,8 +291,9 @@ bool run_gemm(int64_t dt, const Operand &a, const Operand &b, const GemmPlan &p,
 
 // ---- linear ----------------------------------------------------------------
 
-// Largest M the kernel for a few rows takes.
-constexpr int64_t kSkinnyRows = 32;
+// Largest M the kernel for a few rows takes, and largest N: its workgroups have
+// up to 1024 threads for 16 columns each, and a launch fewer than 2^32.
+constexpr int64_t kSkinnyRows = 32, kSkinnyCols = (int64_t)1 << 25;
 
 struct LinearPlan {
     dense_linear_t d;
@@ -354,7 +358,7 @@ conv_i8_status_t analyze(const dense_linear_t *args, LinearPlan *p)
     DENSE_TRY(forced_tile(&forced));
     const int es = (int)size_of(dt);
     const bool x_rows = d.x.col_stride == 1 || p->K <= 1, w_rows = d.w.col_stride == 1 || p->K <= 1;
-    p->skinny = p->M <= kSkinnyRows && x_rows && w_rows && !forced.on;
+    p->skinny = p->M <= kSkinnyRows && p->N <= kSkinnyCols && x_rows && w_rows && !forced.on;
     if (p->skinny) {
         p->aligned = (((uintptr_t)d.x.ptr | (uintptr_t)d.w.ptr) & 15) == 0 && p->K * es % 16 == 0 &&
                      (p->M <= 1 || d.x.row_stride * es % 16 == 0) && (p->N <= 1 || d.w.row_stride * es % 16 == 0);
@@ -382,7 +386,9 @@ conv_i8_status_t analyze(const dense_linear_t *args, LinearPlan *p)
     DENSE_TRY(check_reach(p->a));
     DENSE_TRY(check_reach(p->b));
     plan_gemm(p->M, p->N, p->K, es, forced, &p->gemm);
-    if (!grid_fits(p->gemm))
+    if (!grid_fits(p->gemm, p->M))
+        return CONV_I8_ERR_UNSUPPORTED;
+    if (!launch_fits(pack_wgs(p->a) + pack_wgs(p->b), 256))
         return CONV_I8_ERR_UNSUPPORTED;
     p->ws_bytes = p->a.pack_bytes + p->b.pack_bytes + p->gemm.part_bytes;
     return CONV_I8_OK;
@@ -493,7 +499,7 @@ struct BackwardPlan {
     bool pair() const
     {
         return want_dx && want_dw && dx.tile == kPairTile && dw.tile == kPairTile && dx.splits == 1 && dw.splits == 1 &&
-               (int64_t)dx.tiles_m * dx.tiles_n + (int64_t)dw.tiles_m * dw.tiles_n < (1 << 24);
+               launch_fits((int64_t)dx.tiles_m * dx.tiles_n + (int64_t)dw.tiles_m * dw.tiles_n + ceil_div(N, 8), 256);
     }
 };
 
@@ -601,7 +607,7 @@ conv_i8_status_t analyze(const dense_linear_backward_t *args, BackwardPlan *p)
         DENSE_TRY(check_reach(p->ga));
         DENSE_TRY(check_reach(p->wb));
         apart += plan_gemm(p->M, p->K, p->N, 2, forced, &p->dx);
-        if (!grid_fits(p->dx))
+        if (!grid_fits(p->dx, p->M))
             return CONV_I8_ERR_UNSUPPORTED;
         p->part_bytes = p->dx.part_bytes;
     }
@@ -621,11 +627,13 @@ conv_i8_status_t analyze(const dense_linear_backward_t *args, BackwardPlan *p)
             set_plan(p->N, p->K, p->M, 2, kPairTile, 1, &p->dw);
             p->part_bytes = 0;
         }
-        if (!grid_fits(p->dw))
+        if (!grid_fits(p->dw, p->N))
             return CONV_I8_ERR_UNSUPPORTED;
         if (p->dw.part_bytes > p->part_bytes)
             p->part_bytes = p->dw.part_bytes;  // the two products run one after the other
     }
+    if (!launch_fits(ceil_div(p->N, 512) * p->row_blocks + pack_wgs(p->wb) + pack_wgs(p->xb), 256))
+        return CONV_I8_ERR_UNSUPPORTED;
     p->ws_bytes = p->g_bytes + p->sum_bytes + p->wb.pack_bytes + p->xb.pack_bytes + p->part_bytes;
     return CONV_I8_OK;
 }
@@ -667,8 +675,6 @@ conv_i8_status_t run_backward(const BackwardPlan &p, void *ws, hipStream_t strea
         a.blocks = a.strips * p.row_blocks;
         PackArgs pack;
         const int64_t wgs = a.blocks + pack_jobs(p.wb, pw, p.xb, px, &pack);
-        if (wgs > 0x7fffffff)
-            return CONV_I8_ERR_HIP;
         const dim3 grid((unsigned)wgs);
         if (dt == DENSE_BF16)
             launch_prepare<bf16>(d.activation, grid, a, pack, stream);
@@ -683,7 +689,7 @@ conv_i8_status_t run_backward(const BackwardPlan &p, void *ws, hipStream_t strea
         c.part = (const float *)sums;
         c.ld = p.sum_ld;
         c.rows = p.row_blocks;  // none: zeros
-        c.cols = c.split = c.valid = (int)p.N;
+        c.cols = c.split = c.valid = p.N;
         c.out0 = const_cast<void *>(d.dbias.ptr);
         c.dt = (int)dt;
     }
@@ -710,7 +716,7 @@ conv_i8_status_t run_backward(const BackwardPlan &p, void *ws, hipStream_t strea
         return ok ? CONV_I8_OK : CONV_I8_ERR_HIP;
     }
     if (p.want_db) {
-        hipLaunchKernelGGL(colsum_kernel<>, dim3((unsigned)ceil_div(p.N, 32)), dim3(32 * kSumGroups), 0, stream, c);
+        hipLaunchKernelGGL(colsum_kernel<>, colsum_grid(p.N), dim3(32 * kSumGroups), 0, stream, c);
         if (hipGetLastError() != hipSuccess)
             return CONV_I8_ERR_HIP;
     }

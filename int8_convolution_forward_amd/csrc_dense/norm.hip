@@ -12,7 +12,7 @@ constexpr int64_t kWsAlign = 256;
 // Longest row that stays in registers, forward and backward.
 constexpr int64_t kNormRow = 65536;
 constexpr int64_t kBackRow = 16384;
-// Rows outside these, or of fewer than eight columns, are read again for each step.
+// Longer rows are read again for each step; rows of fewer than eight columns have kernels of their own.
 inline bool back_in_registers(int64_t D) { return D >= 8 && D <= kBackRow; }
 
 conv_i8_status_t check_stat(dense_vec_t *v, int64_t n)
@@ -52,6 +52,13 @@ conv_i8_status_t analyze(const dense_layer_norm_t *args, dense_layer_norm_t *d)
     return CONV_I8_OK;
 }
 
+// A launch has fewer than 2^32 threads: past so many workgroups they walk over rows.
+inline unsigned capped(int64_t wgs, int threads)
+{
+    const int64_t most = threads <= 256 ? 1 << 21 : 1 << 16;
+    return (unsigned)(wgs < most ? wgs : most);
+}
+
 // Two rows for each thread group once there are more than 1024 workgroups: the
 // second one's loads overlap the first one's work, and the card still balances
 // itself (16384 x 4096 BF16: two rows 50.0 us, one 49.9, four 53.8, sixteen 53.2).
@@ -65,7 +72,7 @@ void launch_one(const NormArgs &a, hipStream_t s)
     int64_t wgs = ceil_div(a.M, rows);
     if (hold && wgs > 1024)
         wgs = P > 256 || wgs <= 2048 ? 1024 : ceil_div(wgs, 2);
-    const dim3 grid((unsigned)wgs), block(norm_threads(P));
+    const dim3 grid(capped(wgs, norm_threads(P))), block(norm_threads(P));
     if (a.D % 8 == 0)
         hipLaunchKernelGGL((norm_kernel<T, P, V, hold, false, Q8>), grid, block, 0, s, a);
     else
@@ -78,8 +85,10 @@ void launch_norm(const NormArgs &a, hipStream_t s)
     const int D = a.D;
     // a wave per row while that gives each CU a few waves, else a workgroup per row
     const bool few = a.M < 4 * kCUs;
-    if (D < 8 || D > kNormRow)
-        hipLaunchKernelGGL((norm_long_kernel<T, Q8>), dim3((unsigned)a.M), dim3(1024), 0, s, a);
+    if (D <= kNarrow)
+        hipLaunchKernelGGL((norm_narrow_kernel<T, Q8>), dim3(capped(ceil_div(a.M, 256), 256)), dim3(256), 0, s, a);
+    else if (D > kNormRow)
+        hipLaunchKernelGGL((norm_long_kernel<T, Q8>), dim3(capped(a.M, 1024)), dim3(1024), 0, s, a);
     else if (D <= 512)
         launch_one<T, 64, 1, Q8>(a, s);
     else if (D <= 1024 && !few)
@@ -143,7 +152,11 @@ conv_i8_status_t analyze(const dense_layer_norm_backward_t *args, BackPlan *p)
         return CONV_I8_ERR_PARAM;
     p->sums = d.dweight.dtype != DENSE_NONE;
     p->part_ld = round_up(p->D, 8);
-    if (!back_in_registers(p->D)) {
+    if (p->D <= kNarrow) {
+        // four rows a thread before there are more than two workgroups on a CU
+        const int64_t want = ceil_div(p->M, 4 * 256);
+        p->wgs = (int)(want < 2 * kCUs ? want : 2 * kCUs);
+    } else if (!back_in_registers(p->D)) {
         const int64_t blocks = p->M < 64 ? p->M : 64;
         p->wgs = (int)(p->M > 0 ? ceil_div(p->M, ceil_div(p->M, blocks)) : 0);
     } else {
@@ -185,8 +198,10 @@ template <typename T>
 void launch_back(const NormBackArgs &a, int wgs, hipStream_t s)
 {
     const int D = a.D;
-    if (!back_in_registers(D)) {
-        hipLaunchKernelGGL(norm_backward_long_kernel<T>, dim3((unsigned)a.M), dim3(1024), 0, s, a);
+    if (D <= kNarrow) {
+        hipLaunchKernelGGL(norm_backward_narrow_kernel<T>, dim3((unsigned)wgs), dim3(256), 0, s, a);
+    } else if (!back_in_registers(D)) {
+        hipLaunchKernelGGL(norm_backward_long_kernel<T>, dim3(capped(a.M, 1024)), dim3(1024), 0, s, a);
         if (a.part)
             hipLaunchKernelGGL(norm_backward_sums_kernel<T>, dim3((unsigned)ceil_div(D, 2048), (unsigned)wgs), dim3(256),
                                0, s, a, (int)ceil_div(a.M, wgs));
@@ -303,13 +318,13 @@ conv_i8_status_t dense_layer_norm_backward(const dense_layer_norm_backward_t *ar
         c.part = a.part;
         c.ld = 2 * p.part_ld;
         c.rows = p.M > 0 ? p.wgs : 0;  // none: zeros
-        c.cols = (int)(2 * p.part_ld);
-        c.split = (int)p.part_ld;
-        c.valid = (int)p.D;
+        c.cols = 2 * p.part_ld;
+        c.split = p.part_ld;
+        c.valid = p.D;
         c.out0 = const_cast<void *>(p.d.dweight.ptr);
         c.out1 = const_cast<void *>(p.d.dbias.ptr);
         c.dt = (int)dt;
-        hipLaunchKernelGGL(colsum_kernel<>, dim3((unsigned)ceil_div(c.cols, 32)), dim3(32 * kSumGroups), 0, s, c);
+        hipLaunchKernelGGL(colsum_kernel<>, colsum_grid(c.cols), dim3(32 * kSumGroups), 0, s, c);
         if (hipGetLastError() != hipSuccess)
             return CONV_I8_ERR_HIP;
     }

@@ -179,7 +179,8 @@ __device__ __forceinline__ void row_moments(float (&v)[V][8], int D, int t, floa
 // Rows walk over the grid: a thread group takes every gridDim-th one, with the
 // next row's loads in flight while it works on the present one and the weights
 // held over all of them (HOLD).  Workgroups of 1024 threads have 128 registers
-// each and do neither: 32 columns a thread would spill.
+// each and do neither: 32 columns a thread would spill.  They take one row, or
+// several where a launch could not have as many threads.
 template <typename T, int P, int V, bool HOLD, bool TAIL, bool Q8>
 __global__ __launch_bounds__(norm_threads(P)) void norm_kernel(const NormArgs a)
 {
@@ -195,14 +196,16 @@ __global__ __launch_bounds__(norm_threads(P)) void norm_kernel(const NormArgs a)
     const float cols = (float)wave_columns<P, V>(a.D, P > 64 ? threadIdx.x >> 6 : 0);
 
     Raw8<T> row[V], w[V], b[V];
-    load_row<T, P, V>((const T *)a.x + m * a.ldx, a.D, t, row);
     if constexpr (HOLD) {
+        load_row<T, P, V>((const T *)a.x + m * a.ldx, a.D, t, row);
         load_params<T, P, V>((const T *)a.weight, 1.0f, a.D, t, w);
         load_params<T, P, V>((const T *)a.bias, 0.0f, a.D, t, b);
     }
 
     int set = 0;
     for (;;) {
+        if constexpr (!HOLD)
+            load_row<T, P, V>((const T *)a.x + m * a.ldx, a.D, t, row);
         float v[V][8];
 #pragma unroll
         for (int i = 0; i < V; ++i)
@@ -273,7 +276,7 @@ __global__ __launch_bounds__(norm_threads(P)) void norm_kernel(const NormArgs a)
                 }
             }
         }
-        if (!HOLD || next >= a.M)
+        if (next >= a.M)
             break;
         m = next;
         set ^= 1;  // the other set: a slow wave may still read this one
@@ -281,85 +284,144 @@ __global__ __launch_bounds__(norm_threads(P)) void norm_kernel(const NormArgs a)
 }
 
 // Rows longer than the registers hold: the row is read again (from cache) for
-// each step.  Also rows of fewer than eight columns, which the loads above need.
+// each step.  Of the three sets of `red`, a row's next use of one comes after
+// another set's barrier, so rows need none between them.
 template <typename T, bool Q8>
 __global__ __launch_bounds__(1024) void norm_long_kernel(const NormArgs a)
 {
     __shared__ float red[3 * 16];
     const int t = threadIdx.x;
-    const int64_t m = blockIdx.x;
-    const T *x = (const T *)a.x + m * a.ldx;
-    float s = 0.0f;
-    for (int64_t c = t * 8; c < a.D; c += 8192) {
-        float v[8];
-        load_n(x + c, (int)(a.D - c), v);
+    for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x) {
+        const T *x = (const T *)a.x + m * a.ldx;
+        float s = 0.0f;
+        for (int64_t c = t * 8; c < a.D; c += 8192) {
+            float v[8];
+            load_n(x + c, (int)(a.D - c), v);
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            s += v[k];
-    }
-    const float mean = row_reduce<1024>(s, red, 0) / a.d;
-    s = 0.0f;
-    for (int64_t c = t * 8; c < a.D; c += 8192) {
-        float v[8];
-        load_n(x + c, (int)(a.D - c), v, mean);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            s = __builtin_fmaf(v[k] - mean, v[k] - mean, s);
-    }
-    const float rstd = 1.0f / sqrtf(row_reduce<1024>(s, red, 1) / a.d + a.eps);
-    if (t == 0) {
-        if (a.mean)
-            a.mean[m] = mean;
-        if (a.rstd)
-            a.rstd[m] = rstd;
-    }
-    auto value = [&](int64_t c, int cnt, float (&v)[8]) {
-        float w[8], b[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            w[k] = 1.0f;
-            b[k] = 0.0f;
+            for (int k = 0; k < 8; ++k)
+                s += v[k];
         }
-        load_n(x + c, cnt, v);
-        if (a.weight)
-            load_n((const T *)a.weight + c, cnt, w);
-        if (a.bias)
-            load_n((const T *)a.bias + c, cnt, b);
+        const float mean = row_reduce<1024>(s, red, 0) / a.d;
+        s = 0.0f;
+        for (int64_t c = t * 8; c < a.D; c += 8192) {
+            float v[8];
+            load_n(x + c, (int)(a.D - c), v, mean);
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            v[k] = __builtin_fmaf((v[k] - mean) * rstd, w[k], b[k]);
-    };
-    float top = 0.0f;
-    bool nan = false;
-    for (int64_t c = t * 8; c < a.D; c += 8192) {
-        const int cnt = (int)(a.D - c);
-        float v[8];
-        value(c, cnt, v);
-        if constexpr (Q8) {
+            for (int k = 0; k < 8; ++k)
+                s = __builtin_fmaf(v[k] - mean, v[k] - mean, s);
+        }
+        const float rstd = 1.0f / sqrtf(row_reduce<1024>(s, red, 1) / a.d + a.eps);
+        if (t == 0) {
+            if (a.mean)
+                a.mean[m] = mean;
+            if (a.rstd)
+                a.rstd[m] = rstd;
+        }
+        auto value = [&](int64_t c, int cnt, float (&v)[8]) {
+            float w[8], b[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                const float u = k < cnt ? v[k] : 0.0f;
-                top = fmaxf(top, fabsf(u));
-                nan |= u != u;
+                w[k] = 1.0f;
+                b[k] = 0.0f;
             }
-        } else {
-            store_n((T *)a.y + m * a.ldy + c, cnt, v);
-        }
-    }
-    if constexpr (Q8) {
-        float inv;
-        const float scale = quant_scale(row_reduce<1024, true>(nan ? INFINITY : top, red, 2), inv);
-        if (t == 0)
-            a.scale[m] = scale;
+            load_n(x + c, cnt, v);
+            if (a.weight)
+                load_n((const T *)a.weight + c, cnt, w);
+            if (a.bias)
+                load_n((const T *)a.bias + c, cnt, b);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                v[k] = __builtin_fmaf((v[k] - mean) * rstd, w[k], b[k]);
+        };
+        float top = 0.0f;
+        bool nan = false;
         for (int64_t c = t * 8; c < a.D; c += 8192) {
             const int cnt = (int)(a.D - c);
             float v[8];
             value(c, cnt, v);
-            int8_t *y = (int8_t *)a.y + m * a.ldy + c;
+            if constexpr (Q8) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (k < cnt)
-                    y[k] = quantise(v[k], inv);
+                for (int k = 0; k < 8; ++k) {
+                    const float u = k < cnt ? v[k] : 0.0f;
+                    top = fmaxf(top, fabsf(u));
+                    nan |= u != u;
+                }
+            } else {
+                store_n((T *)a.y + m * a.ldy + c, cnt, v);
+            }
+        }
+        if constexpr (Q8) {
+            float inv;
+            const float scale = quant_scale(row_reduce<1024, true>(nan ? INFINITY : top, red, 2), inv);
+            if (t == 0)
+                a.scale[m] = scale;
+            for (int64_t c = t * 8; c < a.D; c += 8192) {
+                const int cnt = (int)(a.D - c);
+                float v[8];
+                value(c, cnt, v);
+                int8_t *y = (int8_t *)a.y + m * a.ldy + c;
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (k < cnt)
+                        y[k] = quantise(v[k], inv);
+            }
+        }
+    }
+}
+
+// Rows of fewer than eight columns, which the loads above need: a thread per
+// row.  4 000 000 rows of 7 BF16 values take 22 us, bound by HBM (144 MB); with a
+// workgroup per row 24 ms.
+constexpr int kNarrow = 7;
+
+template <typename T, bool Q8>
+__global__ __launch_bounds__(256) void norm_narrow_kernel(const NormArgs a)
+{
+    const int D = a.D;
+    float w[kNarrow], b[kNarrow];
+#pragma unroll
+    for (int k = 0; k < kNarrow; ++k) {
+        w[k] = 1.0f;
+        b[k] = 0.0f;
+    }
+    if (a.weight)
+        load_n((const T *)a.weight, D, w);
+    if (a.bias)
+        load_n((const T *)a.bias, D, b);
+    for (int64_t m = (int64_t)blockIdx.x * 256 + threadIdx.x; m < a.M; m += (int64_t)gridDim.x * 256) {
+        float v[kNarrow];
+        load_n((const T *)a.x + m * a.ldx, D, v);
+        float s = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kNarrow; ++k)
+            s += v[k];
+        const float mean = s / a.d;
+        s = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kNarrow; ++k)
+            s = k < D ? __builtin_fmaf(v[k] - mean, v[k] - mean, s) : s;
+        const float rstd = 1.0f / sqrtf(s / a.d + a.eps);
+        if (a.mean)
+            a.mean[m] = mean;
+        if (a.rstd)
+            a.rstd[m] = rstd;
+        float top = 0.0f;
+        bool nan = false;
+#pragma unroll
+        for (int k = 0; k < kNarrow; ++k) {
+            v[k] = k < D ? __builtin_fmaf((v[k] - mean) * rstd, w[k], b[k]) : 0.0f;
+            top = fmaxf(top, fabsf(v[k]));
+            nan |= v[k] != v[k];
+        }
+        if constexpr (Q8) {
+            float inv;
+            a.scale[m] = quant_scale(nan ? INFINITY : top, inv);
+#pragma unroll
+            for (int k = 0; k < kNarrow; ++k)
+                if (k < D)
+                    ((int8_t *)a.y + m * a.ldy)[k] = quantise(v[k], inv);
+        } else {
+            store_n((T *)a.y + m * a.ldy, D, v);
         }
     }
 }
@@ -601,49 +663,51 @@ __global__ __launch_bounds__(norm_threads(P)) void norm_backward_once_kernel(con
     }
 }
 
-// Rows longer than the registers hold: dx with the row read twice ...
+// Rows longer than the registers hold: dx with the row read twice (the two sets
+// of `red` alternate, so rows need no barrier between them) ...
 template <typename T>
 __global__ __launch_bounds__(1024) void norm_backward_long_kernel(const NormBackArgs a)
 {
     __shared__ float red[2 * 16];
     const int t = threadIdx.x;
-    const int64_t m = blockIdx.x;
-    const T *x = (const T *)a.x + m * a.ldx, *g = (const T *)a.dy + m * a.lddy;
-    const float mean = a.mean[m], rstd = a.rstd[m];
-    auto load = [&](int64_t c, int cnt, float (&xh)[8], float (&cv)[8]) {
-        float w[8];
-        load_n(x + c, cnt, xh, mean);
-        load_n(g + c, cnt, cv);
+    for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x) {
+        const T *x = (const T *)a.x + m * a.ldx, *g = (const T *)a.dy + m * a.lddy;
+        const float mean = a.mean[m], rstd = a.rstd[m];
+        auto load = [&](int64_t c, int cnt, float (&xh)[8], float (&cv)[8]) {
+            float w[8];
+            load_n(x + c, cnt, xh, mean);
+            load_n(g + c, cnt, cv);
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            w[k] = 1.0f;
-        if (a.weight)
-            load_n((const T *)a.weight + c, cnt, w);
+            for (int k = 0; k < 8; ++k)
+                w[k] = 1.0f;
+            if (a.weight)
+                load_n((const T *)a.weight + c, cnt, w);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            xh[k] = (xh[k] - mean) * rstd;
-            cv[k] *= w[k];
+            for (int k = 0; k < 8; ++k) {
+                xh[k] = (xh[k] - mean) * rstd;
+                cv[k] *= w[k];
+            }
+        };
+        float s1 = 0.0f, s2 = 0.0f;
+        for (int64_t c = t * 8; c < a.D; c += 8192) {
+            float xh[8], cv[8];
+            load(c, (int)(a.D - c), xh, cv);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                s1 += cv[k];
+                s2 = __builtin_fmaf(cv[k], xh[k], s2);
+            }
         }
-    };
-    float s1 = 0.0f, s2 = 0.0f;
-    for (int64_t c = t * 8; c < a.D; c += 8192) {
-        float xh[8], cv[8];
-        load(c, (int)(a.D - c), xh, cv);
+        s1 = row_reduce<1024>(s1, red, 0) / a.d;
+        s2 = row_reduce<1024>(s2, red, 1) / a.d;
+        for (int64_t c = t * 8; c < a.D; c += 8192) {
+            float xh[8], cv[8];
+            load(c, (int)(a.D - c), xh, cv);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            s1 += cv[k];
-            s2 = __builtin_fmaf(cv[k], xh[k], s2);
+            for (int k = 0; k < 8; ++k)
+                cv[k] = rstd * (cv[k] - s1 - xh[k] * s2);
+            store_n((T *)a.dx + m * a.lddx + c, (int)(a.D - c), cv);
         }
-    }
-    s1 = row_reduce<1024>(s1, red, 0) / a.d;
-    s2 = row_reduce<1024>(s2, red, 1) / a.d;
-    for (int64_t c = t * 8; c < a.D; c += 8192) {
-        float xh[8], cv[8];
-        load(c, (int)(a.D - c), xh, cv);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            cv[k] = rstd * (cv[k] - s1 - xh[k] * s2);
-        store_n((T *)a.dx + m * a.lddx + c, (int)(a.D - c), cv);
     }
 }
 
@@ -671,6 +735,60 @@ __global__ __launch_bounds__(256) void norm_backward_sums_kernel(const NormBackA
     float *p = a.part + (int64_t)blockIdx.y * 2 * a.part_ld + c;
     store_n(p, cnt, sw);
     store_n(p + a.part_ld, cnt, sb);
+}
+
+// Rows of fewer than eight columns: a thread per row, the columns' sums over a
+// workgroup's rows in registers, then over its waves.  4 000 000 rows of 7 BF16
+// values: 45 us with the column sums, 40 without (200 MB).
+template <typename T>
+__global__ __launch_bounds__(256) void norm_backward_narrow_kernel(const NormBackArgs a)
+{
+    __shared__ float red[4][2 * kNarrow];
+    const int D = a.D;
+    float w[kNarrow], sw[kNarrow] = {}, sb[kNarrow] = {};
+#pragma unroll
+    for (int k = 0; k < kNarrow; ++k)
+        w[k] = 1.0f;
+    if (a.weight)
+        load_n((const T *)a.weight, D, w);
+    for (int64_t m = (int64_t)blockIdx.x * 256 + threadIdx.x; m < a.M; m += (int64_t)gridDim.x * 256) {
+        const float mean = a.mean[m], rstd = a.rstd[m];
+        float xh[kNarrow], g[kNarrow], c[kNarrow];
+        load_n((const T *)a.x + m * a.ldx, D, xh, mean);
+        load_n((const T *)a.dy + m * a.lddy, D, g);
+        float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kNarrow; ++k) {
+            xh[k] = (xh[k] - mean) * rstd;
+            c[k] = g[k] * w[k];
+            s1 += c[k];
+            s2 = __builtin_fmaf(c[k], xh[k], s2);
+            sw[k] = __builtin_fmaf(g[k], xh[k], sw[k]);
+            sb[k] += g[k];
+        }
+        s1 /= a.d;
+        s2 /= a.d;
+#pragma unroll
+        for (int k = 0; k < kNarrow; ++k)
+            c[k] = rstd * (c[k] - s1 - xh[k] * s2);
+        store_n((T *)a.dx + m * a.lddx, D, c);
+    }
+    if (!a.part)
+        return;
+#pragma unroll
+    for (int k = 0; k < kNarrow; ++k) {
+        sw[k] = wave_sum(sw[k]);
+        sb[k] = wave_sum(sb[k]);
+        if ((threadIdx.x & 63) == 0) {
+            red[threadIdx.x >> 6][k] = sw[k];
+            red[threadIdx.x >> 6][kNarrow + k] = sb[k];
+        }
+    }
+    __syncthreads();
+    const int k = threadIdx.x % kNarrow, which = threadIdx.x / kNarrow;
+    if (which < 2 && k < D)
+        a.part[((int64_t)blockIdx.x * 2 + which) * a.part_ld + k] =
+            (red[0][threadIdx.x] + red[1][threadIdx.x]) + (red[2][threadIdx.x] + red[3][threadIdx.x]);
 }
 
 }  // namespace dense
