@@ -3,15 +3,17 @@
 // exists for the calls whose kernels take a few microseconds: marshalling
 // through Python and ctypes took 6 to 10 us a call, this takes under 2.
 //
-// Every function returns its tensor(s), or an int: a status of conv_i8.h, or
-// kOperands where an operand is not a tensor on one GPU (the caller in Python
-// then names it).  The entries' addresses are handed over once with bind(), so
+// Every function returns its tensor(s), or an int: a status of conv_i8.h,
+// kOperands where an operand is not a tensor on one GPU, or kRecorded where one
+// takes part in automatic differentiation, which these calls do not record (the
+// caller in Python then names it).  The entries' addresses are handed over once with bind(), so
 // that the library stays the one that Python loaded.
 #include <Python.h>
 
 #include <ATen/ATen.h>
 #include <ATen/hip/EmptyTensor.h>
 #include <c10/core/DeviceGuard.h>
+#include <c10/core/GradMode.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/csrc/Dtype.h>
@@ -20,7 +22,7 @@
 
 namespace {
 
-constexpr long kOperands = -1;
+constexpr long kOperands = -1, kRecorded = -2;
 
 struct Entries {
     decltype(&dense_linear) linear;
@@ -46,9 +48,11 @@ int64_t code_of(at::ScalarType t)
 // A status that ends the call
 struct Stop { long code; };
 
-// Tensors of the call: each has to be on the first one's GPU
+// Tensors of the call: each has to be on the first one's GPU, and none may
+// expect its gradient to be recorded
 struct Args {
     c10::Device device{c10::kCPU};
+    const bool grad = c10::GradMode::is_enabled();
 
     const at::Tensor *get(PyObject *o, bool needed)
     {
@@ -59,6 +63,8 @@ struct Args {
         const at::Tensor &t = THPVariable_Unpack(o);
         if (!t.is_cuda() || (device.is_cuda() && t.device() != device))
             throw Stop{kOperands};
+        if ((grad && t.requires_grad()) || t._fw_grad(0).defined())
+            throw Stop{kRecorded};
         device = t.device();
         return &t;
     }
@@ -125,6 +131,14 @@ void check(long code)
 at::Tensor empty(at::IntArrayRef shape, at::ScalarType t, c10::Device d)
 {
     return at::Tensor(at::detail::empty_cuda(shape, t, d, std::nullopt));
+}
+
+// Tells autograd that the caller's tensor was written: a graph that saved it
+// then raises instead of using the new values
+void written(const at::Tensor *t)
+{
+    if (t && !t->is_inference())
+        t->unsafeGetTensorImpl()->bump_version();
 }
 
 // x's leading shape with another last dim
@@ -234,6 +248,8 @@ PyObject *linear(PyObject *, PyObject *const *o, Py_ssize_t n)
         }
         a.y = rows_of(&y);
         run(a, entries.linear_size, entries.linear, in.device);
+        written(out);
+        written(pre);
         return wrap(y);
     });
 }

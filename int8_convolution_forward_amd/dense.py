@@ -13,6 +13,13 @@ native (csrc_dense/bind.cpp), because a call on a single token lasts only a few
 microseconds.  PyTorch provides the memory of outputs and workspaces, allocated
 on the stream the kernels run on.  Argument errors raise ConvI8Error (a status
 of conv_i8.h) before any device work.
+
+Gradients are the calls above; nothing is recorded for automatic
+differentiation.  A tensor that expects it (requires_grad while gradients are
+enabled, or a forward-mode tangent) is refused with a RuntimeError, so that no
+gradient is lost silently: call under torch.no_grad(), or from the forward and
+backward of a torch.autograd.Function.  Tensors given as `out` and `preact`
+count as modified in place.
 """
 from __future__ import annotations
 
@@ -69,6 +76,7 @@ _native.bind(*(ctypes.cast(getattr(lib, n), _P).value for n in (
 
 # The C structures as bytes, for the plans
 _UNKNOWN = 99  # a type code the library refuses
+_RECORDED = -2  # the native side's: an operand takes part in automatic differentiation
 _CODES = {torch.int8: 1, torch.bfloat16: 3, torch.float16: 4, torch.float32: 5}
 _NO_MAT = (0, 0, 0, 0, 0, 0)
 _NO_VEC = (0, 0, 0)
@@ -102,10 +110,15 @@ def _vec(t: Optional[torch.Tensor], name: str) -> tuple:
 
 
 def _refuse(code: int, need: int, **tensors) -> None:
-    """Raises for a call that the native side ended: a status, or operands that
-    are not tensors on one GPU (past the first `need`, None is allowed)."""
+    """Raises for a call that the native side ended: a status, operands that are
+    not tensors on one GPU (past the first `need`, None is allowed), or ones
+    whose gradients would have to be recorded."""
     if code >= 0:
         raise ConvI8Error(code, status_string(code))
+    if code == _RECORDED:
+        name = next((n for n, t in tensors.items() if t is not None and t.requires_grad), "an operand")
+        raise RuntimeError(f"{name}: expects automatic differentiation, which this call does not record; use "
+                           "torch.no_grad() and the backward entries")
     for name in list(tensors)[:need]:
         if tensors[name] is None:
             raise TypeError(f"{name}: expected a torch.Tensor, got None")
