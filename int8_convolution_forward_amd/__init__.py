@@ -17,6 +17,7 @@ implementation.
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 import re
 from typing import Optional, Sequence, Tuple, Union
@@ -35,9 +36,11 @@ __all__ = [
     "conv_wgrad_i8_ws", "conv_wgrad_i8_workspace_size", "conv_wgrad_i8_plain", "conv_wgrad_i8_plan", "MODE_CROSS_CORRELATION",
     "MODE_CONVOLUTION",
     "status_string", "LIB_PATH", "DT_INT8", "DT_INT32", "MAX_REDUCTION", "lib",
-    "linear", "linear_plan", "linear_backward", "linear_backward_plan", "layer_norm", "layer_norm_i8",
-    "layer_norm_backward",
 ]
+_DENSE = ("linear", "linear_plan", "linear_backward", "linear_backward_plan", "layer_norm", "layer_norm_i8",
+          "layer_norm_backward")
+if all(map(os.path.exists, (os.environ.get("CONV_I8_DENSE_LIB") or _build.DENSE_LIB, _build.DENSE_BIND))):
+    __all__ += _DENSE
 
 # CONV_I8_LIB names another build of the library (the host-sanitizer test
 # loads a host-only build with AddressSanitizer through it)
@@ -605,6 +608,15 @@ def conv_wgrad_i8(x: torch.Tensor, dy: torch.Tensor, dw: torch.Tensor, pre_paddi
                             mode, stream)
 
 
-# The dense layer and layer norm (a library of their own, bound in dense.py)
-from .dense import (layer_norm, layer_norm_backward, layer_norm_i8, linear, linear_backward,  # noqa: E402
-                    linear_backward_plan, linear_plan)
+# The dense layer and layer norm are a library of their own, bound in dense.py
+# and loaded at their first use: the convolution runs without it.
+def __getattr__(name: str):
+    if name != "dense" and name not in _DENSE:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    dense = importlib.import_module(__name__ + ".dense")
+    globals().update({n: getattr(dense, n) for n in _DENSE})
+    return dense if name == "dense" else globals()[name]
+
+
+def __dir__():
+    return sorted({*globals(), *_DENSE, "dense"})

@@ -44,17 +44,17 @@ def _run(cmds: list, verbose: bool) -> None:
         if verbose:
             print(" ".join(cmd), flush=True)
         log = tempfile.TemporaryFile("w+")
-        started.append((subprocess.Popen(cmd, stdout=log, stderr=subprocess.STDOUT), log))
+        started.append((cmd, subprocess.Popen(cmd, stdout=log, stderr=subprocess.STDOUT), log))
     # the host pass does not know the packed-fp32 feature name; drop that noise
     noise = "is not a recognized feature for this target"
     failed = []
-    for p, log in started:
+    for cmd, p, log in started:
         rc = p.wait()
         log.seek(0)
         msgs = [l for l in log.read().splitlines() if noise not in l]
         log.close()
         if rc != 0:
-            failed += msgs
+            failed += [f"{cmd[0]} ended with {rc}", *msgs]  # also one that was killed without a word
         elif verbose and msgs:
             print("\n".join(msgs))
     if failed:
@@ -78,16 +78,21 @@ def build(verbose: bool = False, dense_only: bool = False) -> str:
     takes minutes), or only the dense one."""
     os.makedirs(LIB_DIR, exist_ok=True)
     tmp, dense_tmp, bind_tmp = (f + ".tmp" for f in (LIB, DENSE_LIB, DENSE_BIND))
+    if os.path.exists(tmp):
+        os.remove(tmp)
     objects = [os.path.join(LIB_DIR, os.path.basename(s)[:-4] + ".o") for s in DENSE_SOURCES]
     compile_flags = [f for f in HIP_FLAGS if f != "-shared"]
     cmds = [] if dense_only else [[HIPCC, *HIP_FLAGS, "-I", INCLUDE, "-I", CSRC, *SOURCES, "-o", tmp]]
     cmds.append(bind_command(bind_tmp))
     cmds += [[HIPCC, *compile_flags, "-I", INCLUDE, "-I", DENSE_CSRC, "-c", s, "-o", o]
              for s, o in zip(DENSE_SOURCES, objects)]
-    _run(cmds, verbose)
+    try:
+        _run(cmds, verbose)
+    finally:
+        # the convolution's library does without the other one, and without a host compiler
+        if not dense_only and os.path.exists(tmp):
+            os.replace(tmp, LIB)
     _run([[HIPCC, "--offload-arch=gfx950", "-fPIC", "-shared", *objects, "-o", dense_tmp]], verbose)
-    if not dense_only:
-        os.replace(tmp, LIB)
     os.replace(dense_tmp, DENSE_LIB)
     os.replace(bind_tmp, DENSE_BIND)
     return LIB
