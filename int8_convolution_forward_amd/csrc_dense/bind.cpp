@@ -1,4 +1,5 @@
-// Python module of the dense entries: tensors to argument structures, outputs
+// Python module of the dense entries: tensors to argument structures (operands
+// whose layout has no such structure are copied by torch first), outputs
 // and workspaces from torch's allocator on the current stream, the call.  It
 // exists for the calls whose kernels take a few microseconds: marshalling
 // through Python and ctypes took 6 to 10 us a call, this takes under 2.
@@ -49,12 +50,16 @@ int64_t code_of(at::ScalarType t)
 struct Stop { long code; };
 
 // Tensors of the call: each has to be on the first one's GPU, and none may
-// expect its gradient to be recorded
+// expect its gradient to be recorded.  `copies` keeps those of operands that the
+// entries do not take as they are.
 struct Args {
     c10::Device device{c10::kCPU};
     const bool grad = c10::GradMode::is_enabled();
+    c10::SmallVector<at::Tensor, 16> copies;  // two for each of up to eight operands: it never moves them
 
-    const at::Tensor *get(PyObject *o, bool needed)
+    const at::Tensor *keep(at::Tensor t) { return &copies.emplace_back(std::move(t)); }
+
+    const at::Tensor *get(PyObject *o, bool needed, bool output = false)
     {
         if (o == Py_None && !needed)
             return nullptr;
@@ -66,37 +71,59 @@ struct Args {
         if ((grad && t.requires_grad()) || t._fw_grad(0).defined())
             throw Stop{kRecorded};
         device = t.device();
+        if (t.is_neg()) {  // a view that stands for the negatives of what lies in memory
+            if (output)
+                throw Stop{CONV_I8_ERR_UNSUPPORTED};
+            return keep(t.resolve_neg());
+        }
         return &t;
     }
 };
 
-// The tensor as a matrix: leading dims that merge into rows of one stride
-dense_mat_t rows_of(const at::Tensor *t)
+// The tensor as a matrix, if its leading dims merge into rows of one stride
+bool as_rows(const at::Tensor &t, dense_mat_t *m)
 {
-    dense_mat_t m{};
-    if (!t)
-        return m;
-    const auto sizes = t->sizes(), strides = t->strides();
-    const int64_t d = t->dim();
+    const auto sizes = t.sizes(), strides = t.strides();
+    const int64_t d = t.dim();
     if (d < 1)
         throw Stop{CONV_I8_ERR_RANK};
-    m.ptr = t->data_ptr();
-    m.dtype = code_of(t->scalar_type());
-    m.cols = sizes[d - 1];
-    m.col_stride = strides[d - 1];
-    m.rows = 1;
-    m.row_stride = m.cols;
+    m->ptr = t.data_ptr();
+    m->dtype = code_of(t.scalar_type());
+    m->cols = sizes[d - 1];
+    m->col_stride = strides[d - 1];
+    m->rows = 1;
+    m->row_stride = m->cols;
     bool first = true;
     for (int64_t i = d - 2; i >= 0; --i) {
         if (sizes[i] == 1)
             continue;
         if (first)
-            m.row_stride = strides[i];
-        else if (strides[i] != m.row_stride * m.rows && t->numel() != 0)
-            throw Stop{CONV_I8_ERR_STRIDES};
-        m.rows *= sizes[i];
+            m->row_stride = strides[i];
+        else if (strides[i] != m->row_stride * m->rows && t.numel() != 0)
+            return false;
+        m->rows *= sizes[i];
         first = false;
     }
+    return true;
+}
+
+// An output, or an operand that was made here
+dense_mat_t rows_of(const at::Tensor *t)
+{
+    dense_mat_t m{};
+    if (t && !as_rows(*t, &m))
+        throw Stop{CONV_I8_ERR_STRIDES};
+    return m;
+}
+
+// An operand: copied where its leading dims do not merge (a transposed batch) or
+// `packed_cols` asks for a contiguous last dim that it does not have (a gradient
+// expanded from one number).
+dense_mat_t rows_in(Args &in, const at::Tensor *t, bool packed_cols)
+{
+    dense_mat_t m{};
+    if (t && (!as_rows(*t, &m) || (packed_cols && m.col_stride != 1 && m.cols > 1)))
+        as_rows(*in.keep(t->contiguous()), &m);
     return m;
 }
 
@@ -107,7 +134,8 @@ dense_mat_t matrix_of(const at::Tensor *t)
     return rows_of(t);
 }
 
-// A contiguous vector; `any_shape` for values that go with the rows
+// A contiguous vector, one made here or (vec_in) an operand, copied if it has a
+// stride; `any_shape` for values that go with the rows
 dense_vec_t vec_of(const at::Tensor *t, bool any_shape = false)
 {
     dense_vec_t v{};
@@ -119,6 +147,11 @@ dense_vec_t vec_of(const at::Tensor *t, bool any_shape = false)
     v.n = t->numel();
     v.dtype = code_of(t->scalar_type());
     return v;
+}
+
+dense_vec_t vec_in(Args &in, const at::Tensor *t, bool any_shape = false)
+{
+    return vec_of(t && !t->is_contiguous() ? in.keep(t->contiguous()) : t, any_shape);
 }
 
 void check(long code)
@@ -221,16 +254,16 @@ PyObject *linear(PyObject *, PyObject *const *o, Py_ssize_t n)
         Args in;
         const at::Tensor *x = in.get(o[0], true), *w = in.get(o[1], true), *bias = in.get(o[2], false);
         const at::Tensor *res = in.get(o[4], false), *xs = in.get(o[5], false), *ws = in.get(o[6], false);
-        const at::Tensor *pre = in.get(o[8], false), *out = in.get(o[9], false);
+        const at::Tensor *pre = in.get(o[8], false, true), *out = in.get(o[9], false, true);
         const c10::DeviceGuard guard(in.device);
         dense_linear_t a{};
-        a.x = rows_of(x);
+        a.x = rows_in(in, x, false);
         a.w = matrix_of(w);
-        a.residual = rows_of(res);
+        a.residual = rows_in(in, res, true);
         a.preact = rows_of(pre);
-        a.bias = vec_of(bias);
-        a.x_scale = vec_of(xs, true);
-        a.w_scale = vec_of(ws);
+        a.bias = vec_in(in, bias);
+        a.x_scale = vec_in(in, xs, true);
+        a.w_scale = vec_in(in, ws);
         a.activation = PyLong_AsLongLong(o[3]);
         at::Tensor y;
         if (out) {
@@ -266,11 +299,11 @@ PyObject *linear_backward(PyObject *, PyObject *const *o, Py_ssize_t n)
         const c10::DeviceGuard guard(in.device);
         dense_linear_backward_t a{};
         a.activation = PyLong_AsLongLong(o[4]);
-        a.dy = rows_of(dy);
-        a.x = rows_of(x);
+        a.dy = rows_in(in, dy, true);
+        a.x = rows_in(in, x, false);
         a.w = matrix_of(w);
         if (a.activation != DENSE_ACT_NONE)
-            a.preact = rows_of(z);
+            a.preact = rows_in(in, z, true);
         const at::ScalarType t = dy->scalar_type();
         at::Tensor dx, dw, db;
         if (o[5] == Py_True) {
@@ -300,9 +333,9 @@ PyObject *layer_norm(PyObject *, PyObject *const *o, Py_ssize_t n)
         const at::Tensor *x = in.get(o[0], true), *w = in.get(o[1], false), *b = in.get(o[2], false);
         const c10::DeviceGuard guard(in.device);
         dense_layer_norm_t a{};
-        a.x = rows_of(x);
-        a.weight = vec_of(w);
-        a.bias = vec_of(b);
+        a.x = rows_in(in, x, true);
+        a.weight = vec_in(in, w);
+        a.bias = vec_in(in, b);
         a.eps = PyFloat_AsDouble(o[3]);
         if (PyErr_Occurred())
             return nullptr;
@@ -335,11 +368,11 @@ PyObject *layer_norm_backward(PyObject *, PyObject *const *o, Py_ssize_t n)
         const at::Tensor *mean = in.get(o[3], true), *rstd = in.get(o[4], true);
         const c10::DeviceGuard guard(in.device);
         dense_layer_norm_backward_t a{};
-        a.dy = rows_of(dy);
-        a.x = rows_of(x);
-        a.weight = vec_of(w);
-        a.mean = vec_of(mean, true);
-        a.rstd = vec_of(rstd, true);
+        a.dy = rows_in(in, dy, true);
+        a.x = rows_in(in, x, true);
+        a.weight = vec_in(in, w);
+        a.mean = vec_in(in, mean, true);
+        a.rstd = vec_in(in, rstd, true);
         const at::Tensor dx = empty(x->sizes(), x->scalar_type(), in.device);
         at::Tensor dw, db;
         a.dx = rows_of(&dx);

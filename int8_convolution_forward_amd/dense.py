@@ -14,6 +14,13 @@ microseconds.  PyTorch provides the memory of outputs and workspaces, allocated
 on the stream the kernels run on.  Argument errors raise ConvI8Error (a status
 of conv_i8.h) before any device work.
 
+Operands may have any strides.  The kernels read most layouts in place or copy
+them in their own passes; only leading dims that do not merge into rows of one
+stride (a transposed batch), a last dim with a stride where rows have to be
+contiguous (layer norm's x, dy, residual and the kept preact) and vectors with
+a stride are made contiguous by torch before the call.  `out` and `preact` of
+linear have a contiguous last dim and leading dims that merge.
+
 Gradients are the calls above; nothing is recorded for automatic
 differentiation.  A tensor that expects it (requires_grad while gradients are
 enabled, or a forward-mode tangent) is refused with a RuntimeError, so that no
@@ -159,8 +166,9 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None
     (N): fp32, int8 operands only.  The result [..., N] has out_dtype: the
     operands' type by default, bf16 for int8; bf16 and fp16 operands may also
     give fp32.  residual and preact have the result's shape and type; preact is
-    written with the value before the activation, which linear_backward takes.
-    out, if given, is written and returned; it may be the residual itself.
+    written with the value before the activation, which linear_backward takes
+    if it is of the operands' type.  out, if given, is written and returned; it
+    may be the residual itself.
     """
     y = _call(_native.linear, stream, x, w, bias, _activation(activation), residual, x_scale, w_scale, out_dtype, preact,
               out)
@@ -215,7 +223,7 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
                eps: float = 1e-5, stream=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """(y, mean, rstd): layer norm over x's last dim, and the statistics that
     layer_norm_backward takes (fp32, x's leading shape).  x: bf16, fp16 or
-    fp32, its last dim contiguous; weight and bias of its type, or None."""
+    fp32; weight and bias of its type, or None."""
     r = _call(_native.layer_norm, stream, x, weight, bias, eps, False)
     if type(r) is int:
         _refuse(r, 1, x=x, weight=weight, bias=bias)
