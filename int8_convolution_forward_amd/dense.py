@@ -145,6 +145,9 @@ def _call(entry, stream, *args):
     are allocated on the stream that the kernels run on."""
     if stream is None:
         return entry(*args)
+    x = args[0]
+    if isinstance(x, torch.Tensor) and x.is_cuda and x.device != stream.device:
+        raise ValueError(f"stream: on {stream.device}, but the operands are on {x.device}")
     with torch.cuda.stream(stream):
         return entry(*args)
 
