@@ -8,11 +8,12 @@
 
 Argument marshalling only, as in the package's convolution entries: tensors
 become the C structures of include/dense.h, and every step runs in the
-library's HIP kernels on the current stream (or `stream`).  The marshalling is
-native (csrc_dense/bind.cpp), because a call on a single token lasts only a few
-microseconds.  PyTorch provides the memory of outputs and workspaces, allocated
-on the stream the kernels run on.  Argument errors raise ConvI8Error (a status
-of conv_i8.h) before any device work.
+library's HIP kernels on the current stream, or on `stream`, which then has to
+wait for what wrote the operands (they may be freed right after the call).  The
+marshalling is native (csrc_dense/bind.cpp), because a call on a single token
+lasts only a few microseconds.  PyTorch provides the memory of outputs and
+workspaces, allocated on the stream the kernels run on.  Argument errors raise
+ConvI8Error (a status of conv_i8.h) before any device work.
 
 Operands may have any strides.  The kernels read most layouts in place or copy
 them in their own passes; only leading dims that do not merge into rows of one
@@ -142,14 +143,19 @@ def _activation(name: str) -> int:
 
 def _call(entry, stream, *args):
     """entry(*args) with `stream` as the current stream: outputs and workspaces
-    are allocated on the stream that the kernels run on."""
+    are allocated on the stream that the kernels run on, and the memory of the
+    operands is not reused before that stream has passed the call."""
     if stream is None:
         return entry(*args)
     x = args[0]
     if isinstance(x, torch.Tensor) and x.is_cuda and x.device != stream.device:
         raise ValueError(f"stream: on {stream.device}, but the operands are on {x.device}")
     with torch.cuda.stream(stream):
-        return entry(*args)
+        r = entry(*args)
+    for t in args:
+        if isinstance(t, torch.Tensor) and t.is_cuda:
+            t.record_stream(stream)
+    return r
 
 
 def _linear_args(x, w, bias, activation, residual, x_scale, w_scale, preact, out) -> bytes:

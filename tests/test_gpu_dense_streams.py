@@ -35,6 +35,30 @@ def calls(ci8, m, stream):
     ]
 
 
+@pytest.mark.parametrize("m", [5, 700])
+def test_operands_freed_before_the_stream_has_read_them(ci8, m):
+    """Their memory is not handed to other work until the stream is done with the call."""
+    s = torch.cuda.Stream()
+    plain, given = calls(ci8, m, None), calls(ci8, m, s)
+    for i in range(len(plain)):
+        want = plain[i][0](plain[i][1])
+        call, operands = given[i]
+        shapes = [(t.shape, t.dtype) for t in operands]
+        s.wait_stream(torch.cuda.current_stream())
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(20_000_000)
+        got = call(operands)
+        given[i] = None
+        del operands
+        new = [torch.full(shape, 7, dtype=dtype, device="cuda") for shape, dtype in shapes for _ in range(2)]
+        torch.cuda.current_stream().synchronize()
+        s.synchronize()
+        del new
+        for a, b in zip(*(v if isinstance(v, tuple) else (v,) for v in (want, got))):
+            assert torch.equal(a, b), i
+
+
 def test_a_stream_of_another_device_is_refused(ci8):
     other = SimpleNamespace(device=torch.device("cuda", torch.cuda.current_device() + 1))
     for call, operands in calls(ci8, 4, other):
