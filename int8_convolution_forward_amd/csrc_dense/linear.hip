@@ -32,8 +32,8 @@ struct Operand {
 
 // Decides how an operand [dim, inner] is read: in place in rows form (inner
 // contiguous) or, where the kernel has that form, columns form (dim
-// contiguous), if 16-byte chunks are aligned and do not straddle a row's end;
-// otherwise from a packed copy.  Columns form has its inner rows one after the
+// contiguous), if 16-byte chunks are aligned, do not straddle a row's end and are
+// within a tile's reach; otherwise from a packed copy.  Columns form has its inner rows one after the
 // other, none repeated or overlapping: the kernel tells those past the end by
 // the byte range that ends with the last one.
 void plan_operand(Operand *o, bool allow_rows, bool allow_cols)
@@ -48,7 +48,8 @@ void plan_operand(Operand *o, bool allow_rows, bool allow_cols)
     const int64_t pitch = (o->cols ? o->cs : o->rs) * o->es;
     const int64_t n = o->cols ? o->inner : o->dim;
     o->packed = !((rows_ok || cols_ok) && aligned && len * o->es % 16 == 0 &&
-                  (n <= 1 || (pitch % 16 == 0 && (!o->cols || pitch >= len * o->es))));
+                  (n <= 1 || (pitch % 16 == 0 && (!o->cols || pitch >= len * o->es) &&
+                              pitch <= (o->cols ? kMaxColBytes : kMaxRowBytes))));
     if (o->packed) {
         o->ld = round_up(len * o->es, 16);
         o->pack_bytes = round_up(o->ld * n, kWsAlign);
@@ -562,10 +563,11 @@ conv_i8_status_t analyze(const dense_linear_backward_t *args, BackwardPlan *p)
     p->want_dw = p->want_dw && p->N > 0 && p->K > 0;
     p->want_db = p->want_db && p->N > 0;
 
-    // g: dy itself where there is no slope to apply, its rows are aligned and, for dw,
-    // which reads it in columns form, none repeats or overlaps another
+    // g: dy itself where there is no slope to apply, its rows are aligned and within a
+    // tile's reach and, for dw, which reads it in columns form, none repeats or overlaps another
     const bool dy_ok = ((uintptr_t)d.dy.ptr & 15) == 0 && p->N % 8 == 0 &&
-                       (p->M <= 1 || (d.dy.row_stride % 8 == 0 && (!p->want_dw || d.dy.row_stride >= p->N)));
+                       (p->M <= 1 || (d.dy.row_stride % 8 == 0 && (!p->want_dw || d.dy.row_stride >= p->N) &&
+                                      d.dy.row_stride * 2 <= kMaxRowBytes));
     const bool any = p->M > 0 && p->N > 0;
     p->write_g = any && (p->want_dx || p->want_dw) && (act || !dy_ok);
     p->pass = any && (p->write_g || p->want_db);
