@@ -68,7 +68,7 @@ struct GemmArgs {
 // registers than the addend and copies all of them around the loop.  The
 // compiler then knows nothing of its latency: operands come from LDS reads
 // (which it does wait for), one accumulator's instructions are FM*FN apart, and
-// the kernel waits itself before it reads the sums (mfma_drain).
+// the kernel waits itself before it reads the sums (mfma_drain, tie).
 // VGPR: the sums lie in ordinary registers instead.
 template <typename T, bool VGPR>
 __device__ __forceinline__ void mfma16_acc(v4i a, v4i b, typename Acc4<T>::type &c)
@@ -92,6 +92,17 @@ __device__ __forceinline__ void mfma16_acc(v4i a, v4i b, typename Acc4<T>::type 
 __device__ __forceinline__ void mfma_drain()
 {
     asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+}
+
+// Makes what reads a sum depend on a statement after the drain: without it, only
+// the scheduler's habits keep a copy of the sum from being placed before the drain.
+template <bool VGPR, typename A>
+__device__ __forceinline__ void tie(A &c)
+{
+    if constexpr (VGPR)
+        asm volatile("" : "+v"(c));
+    else
+        asm volatile("" : "+a"(c));
 }
 
 // Columns form: permutation of inner row kr's 32-byte groups.  32 lanes of a
@@ -440,9 +451,10 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs &g, uint8_t *smem, int 
     // A wave of the 256x256 tile has 256 sums, all the accumulation registers there
     // are; one row of blocks is kept in ordinary ones, since with none to spare the
     // allocator moves sums about inside the loop.
+    constexpr int kLastAcc = FM * FN == 64 ? FM - 1 : FM;  // blocks of rows before it are in accumulation registers
     auto mfma_one = [&](int buf, auto ic) __attribute__((always_inline)) {
         constexpr int x = decltype(ic)::value / FN, y = decltype(ic)::value % FN;
-        constexpr bool vgpr = FM * FN == 64 && x == FM - 1;
+        constexpr bool vgpr = x >= kLastAcc;
         if constexpr (BSTR)
             mfma16_acc<T, vgpr>(frag[buf][y], frag[buf][FN + x], acc[x][y]);
         else
@@ -562,6 +574,10 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs &g, uint8_t *smem, int 
         }
         wait_vm_lgkm0<0>();  // the trailing loads of zeros still write to the rings
         mfma_drain();
+        for_each<NMF>([&](auto ic) __attribute__((always_inline)) {
+            constexpr int x = decltype(ic)::value / FN, y = decltype(ic)::value % FN;
+            tie<(x >= kLastAcc)>(acc[x][y]);
+        });
     }
     __syncthreads();
 
