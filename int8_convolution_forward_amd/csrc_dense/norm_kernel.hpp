@@ -236,10 +236,15 @@ __global__ __launch_bounds__(norm_threads(P)) void norm_kernel(const NormArgs a)
             pin(b[i]);
             widen_group<TAIL, P>(w[i], a.D, i, t, wv);
             widen_group<TAIL, P>(b[i], a.D, i, t, bv);
+            if (Q8 && !whole) {  // past the row's end the value is 0, also where mean rstd is infinite
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    v[i][k] = (TAIL ? k < cnt : cnt > 0) ? v[i][k] : mean;
+            }
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 v[i][k] = __builtin_fmaf((v[i][k] - mean) * rstd, wv[k], bv[k]);
-                if constexpr (Q8) {  // past the row's end weight and bias, and so the value, are 0
+                if constexpr (Q8) {
                     top = fmaxf(top, fabsf(v[i][k]));
                     bad = __builtin_fmaf(v[i][k], 0.0f, bad);
                 }
@@ -499,6 +504,12 @@ __device__ __forceinline__ void backward_rows(const NormBackArgs &a, int block, 
             widen_group<TAIL, P>(w[i], a.D, i, t, wv);
             widen_group<TAIL, P>(cur.x[i], a.D, i, t, xh[i]);
             widen_group<TAIL, P>(cur.dy[i], a.D, i, t, dy);
+            if ((i + 1) * P * 8 > a.D) {  // past the row's end xh is 0, also where mean rstd is infinite
+                const int cnt = a.D - (i * P + t) * 8;
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    xh[i][k] = (TAIL ? k < cnt : cnt > 0) ? xh[i][k] : mean;
+            }
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 xh[i][k] = (xh[i][k] - mean) * rstd;
