@@ -50,12 +50,15 @@ __device__ __forceinline__ float row_reduce(float v, float *red, int set)
 }
 
 // Scale of an INT8 row whose largest magnitude is `top`, and its inverse (0 for
-// a row of zeros, finite for one whose values are below the normal range).  A
-// row with a value that is not finite gets the scale NaN; callers pass infinity
-// for a NaN, because a maximum skips NaN.
+// a row of zeros).  A row with a value that is not finite gets the scale NaN;
+// callers pass infinity for a NaN, because a maximum skips NaN.  The inverse of a
+// row below kTinyRow would not be finite: it is that of the row times kTinyUp,
+// by which callers multiply the values too.
+constexpr float kTinyRow = 0x1p-100f, kTinyUp = 0x1p64f;
+
 __device__ __forceinline__ float quant_scale(float top, float &inv)
 {
-    inv = top > 0.0f ? fminf(127.0f / top, 3.4028234e38f) : 0.0f;
+    inv = top > 0.0f ? 127.0f / (top < kTinyRow ? top * kTinyUp : top) : 0.0f;
     return top < INFINITY ? top / 127.0f : __builtin_nanf("");
 }
 
@@ -259,9 +262,17 @@ __global__ __launch_bounds__(norm_threads(P)) void norm_kernel(const NormArgs a)
         }
         if constexpr (Q8) {
             float inv;
-            const float scale = quant_scale(row_reduce<P, true>(bad == 0.0f ? top : INFINITY, redq[set], 0), inv);
+            top = row_reduce<P, true>(bad == 0.0f ? top : INFINITY, redq[set], 0);
+            const float scale = quant_scale(top, inv);
             if (t == 0)
                 a.scale[m] = scale;
+            if (top < kTinyRow) {
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        v[i][k] *= kTinyUp;
+            }
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const int c = (i * P + t) * 8, cnt = a.D - c;
@@ -357,7 +368,8 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(const NormArgs a)
         }
         if constexpr (Q8) {
             float inv;
-            const float scale = quant_scale(row_reduce<1024, true>(nan ? INFINITY : top, red, 2), inv);
+            top = row_reduce<1024, true>(nan ? INFINITY : top, red, 2);
+            const float scale = quant_scale(top, inv), up = top < kTinyRow ? kTinyUp : 1.0f;
             if (t == 0)
                 a.scale[m] = scale;
             for (int64_t c = t * 8; c < a.D; c += 8192) {
@@ -368,7 +380,7 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(const NormArgs a)
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
                     if (k < cnt)
-                        y[k] = quantise(v[k], inv);
+                        y[k] = quantise(v[k] * up, inv);
             }
         }
     }
@@ -420,11 +432,13 @@ __global__ __launch_bounds__(256) void norm_narrow_kernel(const NormArgs a)
         }
         if constexpr (Q8) {
             float inv;
-            a.scale[m] = quant_scale(nan ? INFINITY : top, inv);
+            top = nan ? INFINITY : top;
+            a.scale[m] = quant_scale(top, inv);
+            const float up = top < kTinyRow ? kTinyUp : 1.0f;
 #pragma unroll
             for (int k = 0; k < kNarrow; ++k)
                 if (k < D)
-                    ((int8_t *)a.y + m * a.ldy)[k] = quantise(v[k], inv);
+                    ((int8_t *)a.y + m * a.ldy)[k] = quantise(v[k] * up, inv);
         } else {
             store_n((T *)a.y + m * a.ldy, D, v);
         }

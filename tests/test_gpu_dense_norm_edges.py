@@ -41,3 +41,25 @@ def test_mean_times_rstd_past_the_largest_number(ci8, d, m):
     v = rstd.double()[:, None] * (c - c.mean(1, keepdim=True))
     e = rstd.double()[:, None] * (ref._steps(d) + 6) * ref.F32 * (c.abs() + c.abs().mean(1, keepdim=True))
     ref.check(got[0], v, e, "dx")
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("d", [7, 12, 600, 4096, 9004, 66000])
+@pytest.mark.parametrize("size", [2.0 ** -99, 2.0 ** -101, 2.0 ** -118, 2.0 ** -122, 2.0 ** -126])
+def test_int8_rows_of_tiny_values(ci8, dtype, d, size):
+    """Weights near the smallest normal number: the row still takes all of 8 bits, and q * scale gives it back.
+    Below the normal range numbers have steps of 2^-149, of which half may be lost in y and in 127 scales."""
+    g = torch.Generator(device="cuda").manual_seed(112)
+    x = torch.randn(5, d, generator=g, device="cuda").to(dtype)
+    w = torch.full((d,), size, dtype=dtype, device="cuda")
+    q, s = ci8.layer_norm_i8(x, w)
+    want = ref.layer_norm(x, w)
+    v, e = want["y"]
+    top = v.abs().amax(1)
+    es = e.amax(1) / 127 + 2 * ref.F32 * (top / 127) + 2.0 ** -149
+    ref.check(s, top / 127, es, "scale")
+    assert bool((q.abs().amax(1) == 127).all())
+    exact = v * 127 / top[:, None]  # what is rounded, off by its own error and that of the largest value
+    off = 127 * (e + 2.0 ** -149) / top[:, None] * 2 + 2 ** -10
+    ref.check(q.double(), exact, 0.5 + off, "q")
+    ref.check(q.double() * s.double()[:, None], v, (0.5 + off) * (top / 127)[:, None] + 127 * es[:, None], "q * scale")
