@@ -63,6 +63,9 @@ typedef enum {
     DENSE_ACT_SILU = 4       /* z / (1 + exp(-z)) */
 } dense_act_t;
 
+/* May be added to the activation of dense_linear_backward. */
+#define DENSE_WIDE_G 256
+
 /*
  * Dense layer.  x [M, K] and w [N, K] share one type: BF16, FP16 or INT8.
  * INT8 operands are summed exactly in 32-bit integers (K <= 131071,
@@ -104,7 +107,10 @@ conv_i8_status_t dense_linear_plan(const dense_linear_t *args, char *buf, size_t
  * Gradients of the dense layer.  All operands BF16, or all FP16.  dy [M, N]
  * and preact [M, N] (the z that dense_linear kept; not needed, and not read,
  * without an activation) give g, which is rounded to the operands' type for
- * the two products (dbias sums the unrounded g).  Any of dx [M, K], dw [N, K]
+ * the two products (dbias sums the unrounded g): in FP16, a g below 2^-14 has
+ * steps of 2^-24, and one below 2^-25 counts as zero.  With DENSE_WIDE_G the
+ * products take g as two values of that type, which together have 16 (BF16) or
+ * 22 (FP16) bits and no such loss above 2^-36, at twice the products' work.  Any of dx [M, K], dw [N, K]
  * and dbias (N) may be absent; outputs have col_stride 1.  The gradient of
  * the residual is dy itself.
  */

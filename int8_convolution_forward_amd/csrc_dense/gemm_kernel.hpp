@@ -713,10 +713,20 @@ __global__ __launch_bounds__(64 * WGM * WGN, OCC) void gemm_pair_kernel(const Pa
         column_sums<kCols>(p.sum, b - p.dx.tiles - p.dw.tiles, (float(*)[kCols + 1])smem);
 }
 
-// Sum of a split product's partial copies, in the order of the splits, and the
-// epilogue.  One thread takes eight columns of one row.
+template <bool INT> struct Choice { typedef float type; };
+template <> struct Choice<true> { typedef int8_t type; };
+
+// The partial copies of a product's sums, from the splits of its inner dimension
+// and the terms of its first operand.
+struct JoinArgs {
+    int copies, first;  // those from `first` on are of the second term
+    float scale;        // by which the second term is taken
+};
+
+// Sum of the partial copies, in their order, and the epilogue.  One thread takes
+// eight columns of one row.
 template <bool INT>
-__global__ __launch_bounds__(256) void split_finish_kernel(const GemmArgs g, int nsplit)
+__global__ __launch_bounds__(256) void split_finish_kernel(const GemmArgs g, const JoinArgs j)
 {
     const int cpr = g.part_ld / 8;
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -725,29 +735,26 @@ __global__ __launch_bounds__(256) void split_finish_kernel(const GemmArgs g, int
     if (m >= g.M || n >= g.N)
         return;
     const float *p = (const float *)g.part + m * g.part_ld + n;
+    typedef typename Acc4<typename Choice<INT>::type>::type vec;
+    auto sum = [&](int from, int to, vec (&s)[2]) {
+        s[0] = *(const vec *)(p + from * g.part_stride);
+        s[1] = *(const vec *)(p + from * g.part_stride + 4);
+        for (int z = from + 1; z < to; ++z) {
+            s[0] += *(const vec *)(p + z * g.part_stride);
+            s[1] += *(const vec *)(p + z * g.part_stride + 4);
+        }
+    };
+    vec s[2];
+    sum(0, j.first, s);
     float v[1][8];
-    if constexpr (INT) {
-        v4i s0 = *(const v4i *)p, s1 = *(const v4i *)(p + 4);
-        for (int z = 1; z < nsplit; ++z) {
-            s0 += *(const v4i *)(p + z * g.part_stride);
-            s1 += *(const v4i *)(p + z * g.part_stride + 4);
-        }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            v[0][k] = (float)s0[k];
-            v[0][4 + k] = (float)s1[k];
-        }
-    } else {
-        v4f s0 = *(const v4f *)p, s1 = *(const v4f *)(p + 4);
-        for (int z = 1; z < nsplit; ++z) {
-            s0 += *(const v4f *)(p + z * g.part_stride);
-            s1 += *(const v4f *)(p + z * g.part_stride + 4);
-        }
+    for (int k = 0; k < 8; ++k)
+        v[0][k] = (float)s[k / 4][k % 4];
+    if (!INT && j.copies > j.first) {
+        sum(j.first, j.copies, s);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            v[0][k] = s0[k];
-            v[0][4 + k] = s1[k];
-        }
+        for (int k = 0; k < 8; ++k)
+            v[0][k] = __builtin_fmaf((float)s[k / 4][k % 4], j.scale, v[0][k]);
     }
     float bs[8], ws[8];
     column_params(g.epi, n, g.N - n, bs, ws);

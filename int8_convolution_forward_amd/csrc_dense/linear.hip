@@ -112,8 +112,10 @@ bool launch_pack(const Operand &a, void *da, const Operand &b, void *db, hipStre
 struct GemmPlan {
     int tile = 0, splits = 1;
     int tiles_m = 0, tiles_n = 0, nstages = 0, kchunk = 0;
+    int terms = 1;  // of the first operand, each a product of its own
     int part_ld = 0;
     int64_t part_bytes = 0;
+    bool joined() const { return splits > 1 || terms > 1; }
 };
 
 // Microseconds a product takes with a tile and a split: the stages of the CU
@@ -202,6 +204,13 @@ void set_plan(int64_t M, int64_t N, int64_t K, int es, int tile, int splits, Gem
     p->part_bytes = p->splits > 1 ? round_up((int64_t)p->splits * M * p->part_ld * 4, kWsAlign) : 0;
 }
 
+// The plan of a product of M rows whose first operand has two terms: partial sums of both.
+void two_terms(int64_t M, GemmPlan *p)
+{
+    p->terms = 2;
+    p->part_bytes = round_up(2 * (int64_t)p->splits * M * p->part_ld * 4, kWsAlign);
+}
+
 // Returns the microseconds expected.
 double plan_gemm(int64_t M, int64_t N, int64_t K, int es, const Forced &forced, GemmPlan *p)
 {
@@ -241,7 +250,7 @@ double plan_gemm(int64_t M, int64_t N, int64_t K, int es, const Forced &forced, 
 bool grid_fits(const GemmPlan &p, int64_t M)
 {
     return launch_fits((int64_t)p.tiles_m * p.tiles_n, 256) &&
-           (p.splits <= 1 || launch_fits(ceil_div(M * (p.part_ld / 8), 256), 256));
+           (!p.joined() || launch_fits(ceil_div(M * (p.part_ld / 8), 256), 256));
 }
 
 // C[M, N] = A B^T over K with the epilogue.  kbytes: inner bytes of a rows-form
@@ -265,7 +274,7 @@ GemmArgs gemm_args(const Operand &a, const void *ap, const Operand &b, const voi
     g.tiles_n = p.tiles_n;
     g.tiles = p.tiles_m * p.tiles_n;
     g.group = 8;
-    g.part = p.splits > 1 ? part : nullptr;
+    g.part = p.joined() ? part : nullptr;
     g.part_ld = p.part_ld;
     g.part_stride = M * (int64_t)p.part_ld;
     g.epi = epi;
@@ -274,19 +283,37 @@ GemmArgs gemm_args(const Operand &a, const void *ap, const Operand &b, const voi
     return g;
 }
 
-bool run_gemm(int64_t dt, const Operand &a, const Operand &b, const GemmPlan &p, const GemmArgs &g, hipStream_t stream)
+bool launch_gemm_of(int64_t dt, const Operand &a, const Operand &b, const GemmPlan &p, const GemmArgs &g, hipStream_t stream)
 {
-    const bool ok = dt == DENSE_BF16 ? launch_gemm_bf16(p.tile, a.cols, b.cols, g, p.splits, stream)
-                  : dt == DENSE_FP16 ? launch_gemm_f16(p.tile, a.cols, b.cols, g, p.splits, stream)
-                                     : launch_gemm_i8(p.tile, a.cols, b.cols, g, p.splits, stream);
-    if (!ok || p.splits <= 1)
-        return ok;
+    return dt == DENSE_BF16 ? launch_gemm_bf16(p.tile, a.cols, b.cols, g, p.splits, stream)
+         : dt == DENSE_FP16 ? launch_gemm_f16(p.tile, a.cols, b.cols, g, p.splits, stream)
+                            : launch_gemm_i8(p.tile, a.cols, b.cols, g, p.splits, stream);
+}
+
+// a2: the first operand's second term, if the plan has two.
+bool run_gemm(int64_t dt, const Operand &a, const Operand &b, const GemmPlan &p, const GemmArgs &g, hipStream_t stream,
+              const void *a2 = nullptr)
+{
+    if (!launch_gemm_of(dt, a, b, p, g, stream))
+        return false;
+    if (!p.joined())
+        return true;
+    JoinArgs j = {p.splits, p.splits, 1.0f};
+    if (p.terms > 1) {
+        GemmArgs second = g;
+        second.a = (const uint8_t *)a2;
+        second.part = (float *)g.part + p.splits * g.part_stride;
+        if (!launch_gemm_of(dt, a, b, p, second, stream))
+            return false;
+        j.copies = 2 * p.splits;
+        j.scale = 1.0f / (dt == DENSE_BF16 ? second_term_up<bf16>() : second_term_up<f16>());
+    }
     const int64_t items = (int64_t)g.M * (p.part_ld / 8);
     const dim3 grid((unsigned)ceil_div(items, 256)), block(256);
     if (dt == DENSE_INT8)
-        hipLaunchKernelGGL(split_finish_kernel<true>, grid, block, 0, stream, g, p.splits);
+        hipLaunchKernelGGL(split_finish_kernel<true>, grid, block, 0, stream, g, j);
     else
-        hipLaunchKernelGGL(split_finish_kernel<false>, grid, block, 0, stream, g, p.splits);
+        hipLaunchKernelGGL(split_finish_kernel<false>, grid, block, 0, stream, g, j);
     return hipGetLastError() == hipSuccess;
 }
 
@@ -487,6 +514,7 @@ struct BackwardPlan {
     bool want_dx, want_dw, want_db;
     bool pass;                 // the pass over dy (and z) that writes g and the column sums
     bool write_g;
+    bool wide = false;         // g as two terms: every product twice, joined like a split
     int64_t ldg = 0;           // elements
     int64_t g_bytes = 0;
     int row_blocks = 0, rows = 0;
@@ -499,7 +527,7 @@ struct BackwardPlan {
     // Both products go out in one launch.
     bool pair() const
     {
-        return want_dx && want_dw && dx.tile == kPairTile && dw.tile == kPairTile && dx.splits == 1 && dw.splits == 1 &&
+        return !wide && want_dx && want_dw && dx.tile == kPairTile && dw.tile == kPairTile && dx.splits == 1 && dw.splits == 1 &&
                launch_fits((int64_t)dx.tiles_m * dx.tiles_n + (int64_t)dw.tiles_m * dw.tiles_n + ceil_div(N, 8), 256);
     }
 };
@@ -510,6 +538,8 @@ conv_i8_status_t analyze(const dense_linear_backward_t *args, BackwardPlan *p)
         return CONV_I8_ERR_NULL;
     p->d = *args;
     dense_linear_backward_t &d = p->d;
+    const bool wide = d.activation & DENSE_WIDE_G;
+    d.activation &= ~(int64_t)DENSE_WIDE_G;
     DENSE_TRY(check_mat(&d.dy, false));
     DENSE_TRY(check_mat(&d.x, false));
     DENSE_TRY(check_mat(&d.w, false));
@@ -573,6 +603,7 @@ conv_i8_status_t analyze(const dense_linear_backward_t *args, BackwardPlan *p)
     p->pass = any && (p->write_g || p->want_db);
     p->ldg = p->write_g ? round_up(p->N, 8) : p->M <= 1 ? round_up(p->N, 8) : d.dy.row_stride;
     p->g_bytes = p->write_g ? round_up(p->M * p->ldg * 2, kWsAlign) : 0;
+    p->wide = wide && act && p->write_g;  // without a slope g is dy, of one term
     if (p->pass || p->want_db) {
         // about two thousand workgroups of 512 columns, at least 16 rows each
         const int64_t strips = ceil_div(p->N > 0 ? p->N : 1, 512);
@@ -609,6 +640,8 @@ conv_i8_status_t analyze(const dense_linear_backward_t *args, BackwardPlan *p)
         DENSE_TRY(check_reach(p->ga));
         DENSE_TRY(check_reach(p->wb));
         apart += plan_gemm(p->M, p->K, p->N, 2, forced, &p->dx);
+        if (p->wide)
+            two_terms(p->M, &p->dx);
         if (!grid_fits(p->dx, p->M))
             return CONV_I8_ERR_UNSUPPORTED;
         p->part_bytes = p->dx.part_bytes;
@@ -624,7 +657,9 @@ conv_i8_status_t analyze(const dense_linear_backward_t *args, BackwardPlan *p)
         DENSE_TRY(check_reach(p->xb));
         apart += plan_gemm(p->N, p->K, p->M, 2, forced, &p->dw);
         // apart: a launch more, and the bias gradient's (320x400x7312: 26 us apart, 21 paired)
-        if (p->want_dx && !forced.on && pair_cost(p->M, p->N, p->K) < apart + 4.0) {
+        if (p->wide)
+            two_terms(p->N, &p->dw);
+        if (!p->wide && p->want_dx && !forced.on && pair_cost(p->M, p->N, p->K) < apart + 4.0) {
             set_plan(p->M, p->K, p->N, 2, kPairTile, 1, &p->dx);
             set_plan(p->N, p->K, p->M, 2, kPairTile, 1, &p->dw);
             p->part_bytes = 0;
@@ -636,7 +671,7 @@ conv_i8_status_t analyze(const dense_linear_backward_t *args, BackwardPlan *p)
     }
     if (!launch_fits(ceil_div(p->N, 512) * p->row_blocks + pack_wgs(p->wb) + pack_wgs(p->xb), 256))
         return CONV_I8_ERR_UNSUPPORTED;
-    p->ws_bytes = p->g_bytes + p->sum_bytes + p->wb.pack_bytes + p->xb.pack_bytes + p->part_bytes;
+    p->ws_bytes = (p->wide ? 2 : 1) * p->g_bytes + p->sum_bytes + p->wb.pack_bytes + p->xb.pack_bytes + p->part_bytes;
     return CONV_I8_OK;
 }
 
@@ -657,7 +692,7 @@ conv_i8_status_t run_backward(const BackwardPlan &p, void *ws, hipStream_t strea
 {
     const dense_linear_backward_t &d = p.d;
     const int64_t dt = d.dy.dtype;
-    uint8_t *g = (uint8_t *)ws, *sums = g + p.g_bytes, *pw = sums + p.sum_bytes, *px = pw + p.wb.pack_bytes;
+    uint8_t *g = (uint8_t *)ws, *g2 = g + (p.wide ? p.g_bytes : 0), *sums = g2 + p.g_bytes, *pw = sums + p.sum_bytes, *px = pw + p.wb.pack_bytes;
     uint8_t *part = px + p.xb.pack_bytes;
     if (p.pass) {
         ActGradArgs a;
@@ -670,6 +705,7 @@ conv_i8_status_t run_backward(const BackwardPlan &p, void *ws, hipStream_t strea
         a.N = (int)p.N;
         a.rows = p.rows;
         a.g = p.write_g ? g : nullptr;
+        a.g2 = p.wide ? g2 : nullptr;
         a.ldg = p.ldg;
         a.colsum = p.want_db ? (float *)sums : nullptr;
         a.sum_ld = p.sum_ld;
@@ -722,9 +758,9 @@ conv_i8_status_t run_backward(const BackwardPlan &p, void *ws, hipStream_t strea
         if (hipGetLastError() != hipSuccess)
             return CONV_I8_ERR_HIP;
     }
-    if (p.want_dx && !run_gemm(dt, p.ga, p.wb, p.dx, dx, stream))
+    if (p.want_dx && !run_gemm(dt, p.ga, p.wb, p.dx, dx, stream, g2))
         return CONV_I8_ERR_HIP;
-    if (p.want_dw && !run_gemm(dt, p.gt, p.xb, p.dw, dw, stream))
+    if (p.want_dw && !run_gemm(dt, p.gt, p.xb, p.dw, dw, stream, g2))
         return CONV_I8_ERR_HIP;
     return CONV_I8_OK;
 }
@@ -815,7 +851,7 @@ conv_i8_status_t dense_linear_backward_plan(const dense_linear_backward_t *args,
         describe(p.dx, p.ga, p.wb, dx, sizeof dx);
     if (p.want_dw)
         describe(p.dw, p.gt, p.xb, dw, sizeof dw);
-    snprintf(text, sizeof text, "g=%s launches=%s dx: %s; dw: %s", p.write_g ? "written" : "dy",
+    snprintf(text, sizeof text, "g=%s launches=%s dx: %s; dw: %s", p.wide ? "written_wide" : p.write_g ? "written" : "dy",
              p.pair() ? "paired" : "apart", dx, dw);
     if (strlen(text) + 1 > len)
         return CONV_I8_ERR_PARAM;

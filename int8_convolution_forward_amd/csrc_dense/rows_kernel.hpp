@@ -60,16 +60,23 @@ __global__ __launch_bounds__(256) void pack_kernel(const PackArgs a)
 // g = dy act'(z), written with a row pitch of whole 16-byte chunks (zeros past
 // N), and column sums of the unrounded g over a block of rows.  g is rounded to
 // the operands' type, since the matrix unit takes both of a product's operands in
-// it; the rounding is of the size of dy's and z's own.
+// it: relative errors of half a step, as dy's and z's own roundings have, and in
+// FP16, below 2^-14, errors of up to 2^-25, where g is smaller than both.  A
+// caller who needs g's further digits has it in two terms: what the rounding
+// takes away, raised by second_term_up, goes to g2.
 // 8192 x 8192 BF16 with the slope of gelu's tanh form: 75 us (403 MB, 5.4 TB/s);
 // with loads of one row at a time, each under a condition, 100.
+template <typename T> constexpr float second_term_up();
+template <> constexpr float second_term_up<bf16>() { return 1.0f; }
+template <> constexpr float second_term_up<f16>() { return 2048.0f; }  // at most half a step of 65504: 2^15
+
 struct ActGradArgs {
     const void *dy, *z;       // z null: g = dy
     int64_t ldy, ldz;
     int M, N;
     int rows;                 // rows per workgroup
     int strips, blocks;       // workgroups along a row, and of this pass
-    void *g;                  // null: only the column sums
+    void *g, *g2;             // g null: only the column sums; g2 null: one term
     int64_t ldg;
     float *colsum;            // [row block][sum_ld], or null
     int64_t sum_ld;
@@ -137,8 +144,18 @@ __global__ __launch_bounds__(256) void act_grad_kernel(const ActGradArgs a, cons
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (a.g && (FORM == 2 || cnt > 0))
+            if (a.g && (FORM == 2 || cnt > 0)) {
                 store_all((T *)a.g + (m + 4 * u) * a.ldg + n, v[u]);
+                if (ACT != DENSE_ACT_NONE && a.g2) {
+                    float rest[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float d = v[u][i] - (float)(T)v[u][i];
+                        rest[i] = fabsf(d) < INFINITY ? d * second_term_up<T>() : 0.0f;  // NaN, infinities: all in g
+                    }
+                    store_all((T *)a.g2 + (m + 4 * u) * a.ldg + n, rest);
+                }
+            }
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 sum[i] += v[u][i];

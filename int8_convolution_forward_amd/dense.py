@@ -84,6 +84,7 @@ _native.bind(*(ctypes.cast(getattr(lib, n), _P).value for n in (
 
 # The C structures as bytes, for the plans
 _UNKNOWN = 99  # a type code the library refuses
+_WIDE_G = 256  # DENSE_WIDE_G
 _RECORDED = -2  # the native side's: an operand takes part in automatic differentiation
 _CODES = {torch.int8: 1, torch.bfloat16: 3, torch.float16: 4, torch.float32: 5}
 _NO_MAT = (0, 0, 0, 0, 0, 0)
@@ -203,26 +204,31 @@ def _backward_args(dy, x, w, preact, activation, dx, dw, dbias) -> bytes:
 
 def linear_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, preact: Optional[torch.Tensor] = None,
                     activation: str = "none", need_dx: bool = True, need_dw: bool = True, need_dbias: bool = True,
-                    stream=None) -> Tuple[Optional[torch.Tensor], Optional[torch.Tensor], Optional[torch.Tensor]]:
+                    stream=None, wide_g: bool = False) -> Tuple[Optional[torch.Tensor], Optional[torch.Tensor], Optional[torch.Tensor]]:
     """(dx, dw, dbias) of linear for bf16 or fp16 operands of one type.
 
     g = dy * act'(preact); dx = g w, dw = g^T x, dbias = sum over rows of g.
     preact is what linear kept (not needed without an activation).  The
     gradient of linear's residual is dy.  None stands for what is not needed.
+
+    The products take g rounded to the operands' type; in fp16, a g below 2^-25
+    counts as zero there (small gradients are scaled up by the caller, as for
+    every fp16 tensor).  wide_g: they take it as two values of that type, 16
+    (bf16) or 22 (fp16) bits and no such loss, at twice the products' work.
     """
-    r = _call(_native.linear_backward, stream, dy, x, w, preact, _activation(activation), bool(need_dx), bool(need_dw),
-              bool(need_dbias))
+    r = _call(_native.linear_backward, stream, dy, x, w, preact, _activation(activation) | (_WIDE_G if wide_g else 0),
+              bool(need_dx), bool(need_dw), bool(need_dbias))
     if type(r) is int:
         _refuse(r, 3, dy=dy, x=x, w=w, preact=preact)
     return r
 
 
 def linear_backward_plan(dy, x, w, preact=None, activation="none", need_dx=True, need_dw=True,
-                         need_dbias=True) -> str:
+                         need_dbias=True, wide_g=False) -> str:
     """How linear_backward would run.  Host-only, matrices only."""
     new = lambda on, *shape: torch.empty(shape, dtype=dy.dtype, device=dy.device) if on else None  # noqa: E731
-    args = _backward_args(dy, x, w, preact, _activation(activation), new(need_dx, *x.shape), new(need_dw, *w.shape),
-                          new(need_dbias, w.shape[0]))
+    args = _backward_args(dy, x, w, preact, _activation(activation) | (_WIDE_G if wide_g else 0),
+                          new(need_dx, *x.shape), new(need_dw, *w.shape), new(need_dbias, w.shape[0]))
     buf = ctypes.create_string_buffer(512)
     _check(lib.dense_linear_backward_plan(args, buf, 512))
     return buf.value.decode()
