@@ -33,11 +33,6 @@ template <> struct Code<bf16> { static constexpr int v = DENSE_BF16; };
 template <> struct Code<f16> { static constexpr int v = DENSE_FP16; };
 template <> struct Code<float> { static constexpr int v = DENSE_FP32; };
 
-inline int dtype_size(int64_t dt)
-{
-    return dt == DENSE_INT8 ? 1 : dt == DENSE_FP32 ? 4 : dt == DENSE_BF16 || dt == DENSE_FP16 ? 2 : 0;
-}
-
 // C values at any element-aligned address.  gfx950 runs with unaligned vector
 // access enabled, so 16 bytes are one instruction whatever the address; an
 // address that is a multiple of 16 costs nothing extra.
@@ -233,7 +228,8 @@ __device__ __forceinline__ float gelu_tanh_gate(float z, float z2)
 
 // exp(-z^2/2) and the normal distribution function.  With t = 1 / (1 + c |z|) the
 // lower tail is t Q(t) exp(-z^2/2): Q, of degree 9, is a fit to
-// exp(z^2/2) cdf(-|z|) / t with the least relative error, 2^-24.9, over all z.
+// exp(z^2/2) cdf(-|z|) / t with the least relative error over all z: 2^-24.5 with
+// the constants as written, 2^-24.2 once they are rounded to 32 bits.
 // Rounded to 32 bits everything is within 3 2^-24, and the tail keeps its
 // relative precision (11 2^-24 down to z = -3; the rounding of z^2 in the
 // exponent).  About 20 operations, where the library's erfc takes several times

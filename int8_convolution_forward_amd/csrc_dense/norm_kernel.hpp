@@ -621,10 +621,12 @@ __global__ __launch_bounds__(norm_threads(P)) void norm_backward_kernel(const No
 // each over all rows, four threads to a row, the others take one row per thread
 // group.  x and dy are read twice, the second time from cache; what it saves is
 // the partial sums on their way out and back, and a launch.  With many rows the
-// walk down the columns lasts longest, in 16-bit types sooner, where a row's 32
-// columns are half a cache line: 256 x 4096 BF16 5.2 us (two launches 10.4),
-// 512 x 4096 9.7 (11.9), 1024 x 4096 18.8 (15.0); 1003 x 1537 FP32 11.4 (12.3).
-constexpr int64_t once_rows(int value_size) { return value_size == 4 ? 1024 : 640; }
+// walk down the columns lasts longest, sooner in wide rows, of which one launch
+// has few in flight: 256 x 4096 BF16 6.2 us (two launches 10.5), 1000 x 4096 11.6
+// (14.8), 1000 x 256 6.1 (7.7), 1000 x 1537 FP32 11.7 (12.5), 1000 x 8192 FP32 26.9
+// (27.3); but 1000 x 9001 BF16 41 (31), 1000 x 16384 FP32 66 (54), 512 x 16384 FP32
+// 33.8 (34.2).
+constexpr int64_t once_rows(int64_t D) { return D <= 8192 ? 1024 : 512; }
 constexpr int kOnceCols = 32;
 
 template <typename T, int P, int V, bool TAIL>
@@ -649,6 +651,10 @@ __global__ __launch_bounds__(norm_threads(P)) void norm_backward_once_kernel(con
             mean[u] = a.mean[r];
             rstd[u] = a.rstd[r];
         }
+        // without the branches of TAIL the loads would be moved to their uses, a wait for each
+        // (1000 x 2048 BF16 18.1 us; 10.4 with them together)
+        if constexpr (!TAIL)
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (m + u * G >= a.M)

@@ -123,3 +123,10 @@ def test_norm_gradients_of_a_very_wide_row(ci8):
     dx, dw, db = ci8.layer_norm_backward(dy, x, None, mean, rstd)
     for name, t, (v, b) in zip(("dx", "dweight", "dbias"), (dx, dw, db), ref.layer_norm_backward(dy, x, None, mean, rstd)):
         ref.check(t, v, b, name)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
+@pytest.mark.parametrize("m,d", [(1024, 64), (1024, 1000), (1023, 777), (1025, 777), (1000, 2048), (1024, 8192), (513, 8192),
+                                 (512, 8200), (513, 8200), (512, 16384), (511, 9001)])
+def test_gradients_on_both_sides_of_one_launch(ci8, dtype, m, d):
+    check_norm(ci8, m, d, dtype, pitch=m % 2)
