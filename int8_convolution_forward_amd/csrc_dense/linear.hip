@@ -675,16 +675,24 @@ conv_i8_status_t analyze(const dense_linear_backward_t *args, BackwardPlan *p)
     return CONV_I8_OK;
 }
 
+template <typename T, int ACT>
+void launch_prepare_act(dim3 grid, const ActGradArgs &a, const PackArgs &pack, hipStream_t stream)
+{
+    if (ACT != DENSE_ACT_NONE && a.g2)
+        hipLaunchKernelGGL((act_grad_kernel<T, ACT, ACT != DENSE_ACT_NONE>), grid, dim3(256), 0, stream, a, pack);
+    else
+        hipLaunchKernelGGL((act_grad_kernel<T, ACT, false>), grid, dim3(256), 0, stream, a, pack);
+}
+
 template <typename T>
 void launch_prepare(int64_t act, dim3 grid, const ActGradArgs &a, const PackArgs &pack, hipStream_t stream)
 {
-    auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, a, pack); };
     switch (act) {
-    case DENSE_ACT_RELU: launch(act_grad_kernel<T, DENSE_ACT_RELU>); break;
-    case DENSE_ACT_GELU: launch(act_grad_kernel<T, DENSE_ACT_GELU>); break;
-    case DENSE_ACT_GELU_TANH: launch(act_grad_kernel<T, DENSE_ACT_GELU_TANH>); break;
-    case DENSE_ACT_SILU: launch(act_grad_kernel<T, DENSE_ACT_SILU>); break;
-    default: launch(act_grad_kernel<T, DENSE_ACT_NONE>); break;
+    case DENSE_ACT_RELU: launch_prepare_act<T, DENSE_ACT_RELU>(grid, a, pack, stream); break;
+    case DENSE_ACT_GELU: launch_prepare_act<T, DENSE_ACT_GELU>(grid, a, pack, stream); break;
+    case DENSE_ACT_GELU_TANH: launch_prepare_act<T, DENSE_ACT_GELU_TANH>(grid, a, pack, stream); break;
+    case DENSE_ACT_SILU: launch_prepare_act<T, DENSE_ACT_SILU>(grid, a, pack, stream); break;
+    default: launch_prepare_act<T, DENSE_ACT_NONE>(grid, a, pack, stream); break;
     }
 }
 

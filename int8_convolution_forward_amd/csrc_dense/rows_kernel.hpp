@@ -76,7 +76,7 @@ struct ActGradArgs {
     int M, N;
     int rows;                 // rows per workgroup
     int strips, blocks;       // workgroups along a row, and of this pass
-    void *g, *g2;             // g null: only the column sums; g2 null: one term
+    void *g, *g2;             // g null: only the column sums; g2: the second term
     int64_t ldg;
     float *colsum;            // [row block][sum_ld], or null
     int64_t sum_ld;
@@ -84,8 +84,9 @@ struct ActGradArgs {
 
 // A wave takes 512 columns (eight per lane) of every fourth row of its block,
 // so that each load is one contiguous 1 KiB; the four waves' column sums are
-// added through LDS in order.  The workgroups after those copy operands.
-template <typename T, int ACT>
+// added through LDS in order.  The workgroups after those copy operands.  WIDE: g
+// has two terms (asked for at run time, one term pays 0.3 us for it).
+template <typename T, int ACT, bool WIDE>
 __global__ __launch_bounds__(256) void act_grad_kernel(const ActGradArgs a, const PackArgs pack)
 {
     if ((int)blockIdx.x >= a.blocks) {
@@ -146,7 +147,7 @@ __global__ __launch_bounds__(256) void act_grad_kernel(const ActGradArgs a, cons
         for (int u = 0; u < U; ++u) {
             if (a.g && (FORM == 2 || cnt > 0)) {
                 store_all((T *)a.g + (m + 4 * u) * a.ldg + n, v[u]);
-                if (ACT != DENSE_ACT_NONE && a.g2) {
+                if constexpr (WIDE) {
                     float rest[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
