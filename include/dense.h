@@ -8,6 +8,12 @@
  *   linear_backward      g = dy * act'(z); dx = g w; dw = g^T x; dbias = sum over rows of g
  *   layer_norm           y = (x - mean) * rstd * weight + bias, rstd = 1 / sqrt(var + eps)
  *   layer_norm_backward  dx, dweight and dbias of it
+ *   quantize, dequantize rows of 8-bit floating point with a scale for each block of 128, and back
+ *   linear_fp8           the dense layer on such operands
+ *   linear_fp8_backward  its gradients
+ *   residual_norm        r = scale x + gate norm(h) weight', y = norm(r) weight + bias
+ *   residual_norm_backward  its gradients
+ *   clip_grads           many gradients scaled so that their norm together stays within a limit
  *
  * A matrix is a device pointer, its dims and its strides in ELEMENTS; strides
  * must be >= 0 and outputs must not overlap themselves.  The kernels keep no
@@ -35,7 +41,10 @@ typedef enum {
     DENSE_INT8 = 1, /* CONV_I8_DT_INT8 */
     DENSE_BF16 = 3,
     DENSE_FP16 = 4,
-    DENSE_FP32 = 5
+    DENSE_FP32 = 5,
+    DENSE_E4M3 = 6, /* 8-bit floating point: up to 448, NaN, no infinities */
+    DENSE_E5M2 = 7, /* up to 57344, infinities and NaN */
+    DENSE_E8M0 = 8  /* a scale 2^(byte - 127); byte 255 is NaN */
 } dense_dtype_t;
 
 /* [rows, cols] of `dtype`; element (r, c) at ptr + r*row_stride + c*col_stride.
@@ -160,6 +169,159 @@ typedef struct {
 conv_i8_status_t dense_layer_norm_backward_workspace_size(const dense_layer_norm_backward_t *args, size_t *bytes);
 conv_i8_status_t dense_layer_norm_backward(const dense_layer_norm_backward_t *args, void *workspace, size_t bytes,
                                            void *stream);
+
+/*
+ * Rows of 8-bit floating point.  x [M, K] (BF16, FP16 or FP32, col_stride 1)
+ * becomes q [M, K] (E4M3 or E5M2) with a scale for each block: 128 values of a
+ * row (scale [M, ceil(K/128)]) or 128 x 128 values (scale [ceil(M/128),
+ * ceil(K/128)]); the blocks at the ends of rows and columns may have fewer.  A
+ * block's scale is 2^e, e the least exponent (at least -127) with which its
+ * largest magnitude times 2^-e does not exceed the type's largest value;
+ * q = x 2^-e, rounded half to even.  Dividing by such a scale is exact, so q is
+ * the rounding of x itself.  Values that are not finite become NaN and do not
+ * count for the scale.
+ *
+ * qt [K, M] and scale_t ([K, ceil(M/128)], or by tiles) are the same of the
+ * transpose of x, in one pass over it.  q with scale, or qt with scale_t, may be
+ * absent, not both.  One type for both.
+ */
+typedef struct {
+    dense_mat_t x;
+    dense_mat_t q, scale;      /* dtype DENSE_NONE: not written */
+    dense_mat_t qt, scale_t;   /* dtype DENSE_NONE: not written */
+} dense_quantize_t;
+
+conv_i8_status_t dense_quantize(const dense_quantize_t *args, void *stream);
+
+/* x = q 2^e, rounded to x's type (BF16, FP16 or FP32): exact where the value is in
+ * the type's range.  q and scale as above, both with col_stride 1. */
+typedef struct {
+    dense_mat_t q, scale, x;
+} dense_dequantize_t;
+
+conv_i8_status_t dense_dequantize(const dense_dequantize_t *args, void *stream);
+
+/*
+ * Dense layer on such operands: x [M, K] (E4M3 or E5M2) with scales for blocks
+ * of a row, w [N, K] (E4M3) with scales for blocks of a row or tiles:
+ *   z = sum over k of (x x_scale)(w w_scale) + bias; y = act(z) + residual
+ * Scales have col_stride 1.  y, preact and residual share one type: BF16, FP16
+ * or FP32; their strides, bias and the activation as in dense_linear.
+ *
+ * For a 16-bit y of more than 32 rows the matrix unit takes the operands as they
+ * are: it adds the products of eight consecutive k at a time, cutting off what is
+ * more than 13 bits below the largest of them, and sums those in 32 bits.  For a
+ * 32-bit y, and for few rows, the operands are taken to BF16 first, which holds
+ * them exactly (magnitudes of 2^-126 and more), and all sums are those of 32 bits;
+ * x and w then have col_stride 1.
+ */
+typedef struct {
+    dense_mat_t x, w, y;
+    dense_mat_t residual, preact;  /* dtype DENSE_NONE: none */
+    dense_mat_t x_scale;           /* [M, ceil(K/128)] of E8M0 */
+    dense_mat_t w_scale;           /* [N, ceil(K/128)] or [ceil(N/128), ceil(K/128)] of E8M0 */
+    dense_vec_t bias;
+    int64_t activation;
+} dense_linear_fp8_t;
+
+conv_i8_status_t dense_linear_fp8_workspace_size(const dense_linear_fp8_t *args, size_t *bytes);
+conv_i8_status_t dense_linear_fp8(const dense_linear_fp8_t *args, void *workspace, size_t bytes, void *stream);
+conv_i8_status_t dense_linear_fp8_plan(const dense_linear_fp8_t *args, char *buf, size_t len);
+
+/*
+ * Its gradients, from the operands transposed: xt [K, M] and wt [K, N] (E4M3,
+ * scales for blocks of a row or tiles).  dy and preact [M, N] (one type, BF16 or
+ * FP16; preact is not read without an activation) give g = dy act'(preact),
+ * which is quantised twice, to g_dtype (DENSE_E4M3 or DENSE_E5M2) with scales for
+ * blocks of a row: as it is for dx = g w, transposed for dw = g^T x.  dbias sums
+ * the unrounded g.  Any of dx [M, K], dw [N, K] and dbias (N), of dy's type, may
+ * be absent; xt (wt) is not needed without dw (dx).
+ */
+typedef struct {
+    dense_mat_t dy, preact;
+    dense_mat_t xt, xt_scale, wt, wt_scale;
+    dense_mat_t dx, dw;
+    dense_vec_t dbias;
+    int64_t activation;
+    int64_t g_dtype;
+} dense_linear_fp8_backward_t;
+
+conv_i8_status_t dense_linear_fp8_backward_workspace_size(const dense_linear_fp8_backward_t *args, size_t *bytes);
+conv_i8_status_t dense_linear_fp8_backward(const dense_linear_fp8_backward_t *args, void *workspace, size_t bytes,
+                                           void *stream);
+conv_i8_status_t dense_linear_fp8_backward_plan(const dense_linear_fp8_backward_t *args, char *buf, size_t len);
+
+/*
+ * The norm between two blocks, fused with the residual connection:
+ *   n = norm(h) post_weight, or h without it
+ *   r = alpha x + gate n, or x without h;  rounded to x's type
+ *   y = norm(r) weight + bias
+ * norm(v) = (v - mean) rstd, rstd = 1 / sqrt(mean((v - mean)^2) + eps); with
+ * kind DENSE_RMS_NORM mean stands for 0.  x, h, r and y are [M, D], all matrices
+ * and vectors of one type (BF16, FP16 or FP32), col_stride 1, D >= 1.  gate
+ * [G, D]: G divides M, and each of its rows is that of M / G consecutive rows.
+ * Without h, gate, post_weight and r are absent as well.  r may be x or h
+ * itself.  y may be E4M3, with a scale for each 128 of a row in y_scale
+ * [M, ceil(D/128)], as dense_quantize gives of the unrounded y.
+ */
+typedef enum { DENSE_LAYER_NORM = 0, DENSE_RMS_NORM = 1 } dense_norm_t;
+
+typedef struct {
+    dense_mat_t x, h, r, y;
+    dense_mat_t gate;               /* dtype DENSE_NONE: ones */
+    dense_mat_t y_scale;            /* E8M0, for an E4M3 y only */
+    dense_vec_t post_weight;        /* dtype DENSE_NONE: no norm of h */
+    dense_vec_t weight, bias;       /* dtype DENSE_NONE: ones, zeros */
+    dense_vec_t mean, rstd;         /* of r, M of FP32; dtype DENSE_NONE: not written */
+    dense_vec_t post_mean, post_rstd; /* of h */
+    double alpha, eps;              /* eps >= 0 */
+    int64_t kind;
+} dense_residual_norm_t;
+
+conv_i8_status_t dense_residual_norm(const dense_residual_norm_t *args, void *stream);
+
+/*
+ * Its gradients from those of r (dr; dtype DENSE_NONE: zero) and y (dy), r, h and
+ * the statistics of the forward pass (means are not read with DENSE_RMS_NORM):
+ *   t = dr + the gradient of norm(r) weight by r, applied to dy
+ *   dx = alpha t; dgate = sum over a gate row's rows of t n
+ *   dh = the gradient of n by h, applied to gate t
+ *   dweight = sum over rows of dy norm(r); dbias = sum over rows of dy;
+ *   dpost_weight = sum over rows of gate t norm(h)
+ * Without h, dh, dgate and dpost_weight are absent; h is not read without gate
+ * and post_weight.  dweight, dbias, dgate and dpost_weight are absent together
+ * with what they are the gradients of, or each where it is not wanted.
+ */
+typedef struct {
+    dense_mat_t dr, dy, r, h, dx, dh;
+    dense_mat_t gate, dgate;
+    dense_vec_t weight, post_weight;
+    dense_vec_t mean, rstd, post_mean, post_rstd;
+    dense_vec_t dweight, dbias, dpost_weight;
+    double alpha;
+    int64_t kind;
+} dense_residual_norm_backward_t;
+
+conv_i8_status_t dense_residual_norm_backward_workspace_size(const dense_residual_norm_backward_t *args, size_t *bytes);
+conv_i8_status_t dense_residual_norm_backward(const dense_residual_norm_backward_t *args, void *workspace, size_t bytes,
+                                              void *stream);
+
+/*
+ * norm = sqrt(sum of squares of all elements of all tensors), summed in 64 bits;
+ * out = in min(1, max_norm / norm).  A norm that is not finite leaves the values as they are
+ * (the caller sees it in `norm`).  in and out: `count` vectors of BF16, FP16 or
+ * FP32; an out is its in itself, or of the same type and size and overlaps
+ * no other vector.  No two vectors of `in` overlap where they are written.
+ */
+typedef struct {
+    const dense_vec_t *in, *out;
+    int64_t count;
+    double max_norm;   /* >= 0, not NaN */
+    float *norm;       /* device memory */
+} dense_clip_grads_t;
+
+conv_i8_status_t dense_clip_grads_workspace_size(const dense_clip_grads_t *args, size_t *bytes);
+conv_i8_status_t dense_clip_grads(const dense_clip_grads_t *args, void *workspace, size_t bytes, void *stream);
 
 #ifdef __cplusplus
 }

@@ -38,7 +38,8 @@ __all__ = [
     "status_string", "LIB_PATH", "DT_INT8", "DT_INT32", "MAX_REDUCTION", "lib",
 ]
 _DENSE = ("linear", "linear_plan", "linear_backward", "linear_backward_plan", "layer_norm", "layer_norm_i8",
-          "layer_norm_backward")
+          "layer_norm_backward", "quantize_fp8", "dequantize_fp8", "linear_fp8", "linear_fp8_plan", "linear_fp8_backward",
+          "linear_fp8_backward_plan", "residual_norm", "residual_norm_fp8", "residual_norm_backward", "clip_grad_norm")
 if all(map(os.path.exists, (os.environ.get("CONV_I8_DENSE_LIB") or _build.DENSE_LIB, _build.DENSE_BIND))):
     __all__ += _DENSE
 

@@ -1,0 +1,176 @@
+// The norm of many tensors together, and their scaling by it: two passes over the
+// values, bound by HBM.
+//
+// A launch takes a table of tensors as its argument; its workgroups walk over
+// chunks of kChunk values, numbered through all the table's tensors.  Squares are
+// summed in 64 bits, so that no finite value's square overflows or vanishes and the
+// sum is exact to about 2^-53 a term; the vector unit has more of that than HBM can
+// feed.  Workgroups leave a partial sum each, and every workgroup of the second
+// pass adds all of them in the same order: no atomics, and nothing between the
+// launches.  Gradients within the limit that stay where they are end the second
+// pass there.
+#pragma once
+
+#include "dense_common.hpp"
+
+namespace dense {
+
+constexpr int kClipTensors = 128, kClipThreads = 256;
+constexpr int kClipChunk = 16384;  // values
+constexpr int kClipWgs = 1024;     // of a launch, at most
+
+struct ClipTable {
+    const void *in[kClipTensors];
+    void *out[kClipTensors];
+    int64_t n[kClipTensors];
+    unsigned first[kClipTensors + 1];  // number of a tensor's first chunk; the last: of all
+    uint8_t dt[kClipTensors];
+    int count;
+};
+
+// Tensor of chunk b: the last whose first chunk is not beyond it (tensors of no values have none)
+__device__ __forceinline__ int clip_tensor(const ClipTable &t, unsigned b)
+{
+    int lo = 0, hi = t.count;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (t.first[mid] <= b)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
+}
+
+__device__ __forceinline__ double wave_sum64(double v)
+{
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1)
+        v += __shfl_xor(v, o, 64);
+    return v;
+}
+
+// The sum over the workgroup's threads, in all of them
+__device__ __forceinline__ double group_sum64(double v, double *red)
+{
+    v = wave_sum64(v);
+    if ((threadIdx.x & 63) == 0)
+        red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    return (red[0] + red[1]) + (red[2] + red[3]);
+}
+
+// f(element offset, how many values exist) for each group of eight of a chunk, U of them together
+template <typename F>
+__device__ __forceinline__ void clip_walk(const ClipTable &t, F f)
+{
+    for (unsigned b = blockIdx.x; b < t.first[t.count]; b += gridDim.x) {
+        const int i = __builtin_amdgcn_readfirstlane(clip_tensor(t, b));
+        f(i, (int64_t)(b - t.first[i]) * kClipChunk);
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ double chunk_squares(const T *p, int64_t at, int64_t n)
+{
+    constexpr int U = 4;
+    double s[2] = {0.0, 0.0};
+    const int64_t end = min(n, at + kClipChunk);
+    int64_t c = at + threadIdx.x * 8;
+    for (; c + (U - 1) * kClipThreads * 8 + 8 <= end; c += U * kClipThreads * 8) {
+        float v[U][8];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            load_all(p + c + u * kClipThreads * 8, v[u]);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                s[k & 1] = __builtin_fma((double)v[u][k], (double)v[u][k], s[k & 1]);
+    }
+    for (; c < end; c += kClipThreads * 8) {
+        float v[8];
+        load_n(p + c, (int)(end - c), v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            s[k & 1] = __builtin_fma((double)v[k], (double)v[k], s[k & 1]);
+    }
+    return s[0] + s[1];
+}
+
+__global__ __launch_bounds__(kClipThreads) void clip_squares_kernel(const ClipTable t, double *part)
+{
+    __shared__ double red[4];
+    double s = 0.0;
+    clip_walk(t, [&](int i, int64_t at) {
+        if (t.dt[i] == DENSE_BF16)
+            s += chunk_squares((const bf16 *)t.in[i], at, t.n[i]);
+        else if (t.dt[i] == DENSE_FP16)
+            s += chunk_squares((const f16 *)t.in[i], at, t.n[i]);
+        else
+            s += chunk_squares((const float *)t.in[i], at, t.n[i]);
+    });
+    s = group_sum64(s, red);
+    if (threadIdx.x == 0)
+        part[blockIdx.x] = s;
+}
+
+template <typename T>
+__device__ __forceinline__ void chunk_scale(const T *p, T *q, int64_t at, int64_t n, double factor)
+{
+    constexpr int U = 4;
+    const int64_t end = min(n, at + kClipChunk);
+    // 16-bit values in 32 bits, rounded once to 32 and once to 16; 32-bit ones in 64, rounded once
+    const float f = (float)factor;
+    auto scale = [&](float v) { return sizeof(T) == 2 ? v * f : (float)((double)v * factor); };
+    int64_t c = at + threadIdx.x * 8;
+    for (; c + (U - 1) * kClipThreads * 8 + 8 <= end; c += U * kClipThreads * 8) {
+        float v[U][8];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            load_all(p + c + u * kClipThreads * 8, v[u]);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                v[u][k] = scale(v[u][k]);
+            store_all(q + c + u * kClipThreads * 8, v[u]);
+        }
+    }
+    for (; c < end; c += kClipThreads * 8) {
+        float v[8];
+        load_n(p + c, (int)(end - c), v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            v[k] = scale(v[k]);
+        store_n(q + c, (int)(end - c), v);
+    }
+}
+
+// parts: the partial sums of all launches of the first pass
+__global__ __launch_bounds__(kClipThreads) void clip_scale_kernel(const ClipTable t, const double *part, int parts,
+                                                                  double max_norm, float *norm)
+{
+    __shared__ double red[4];
+    double s = 0.0;
+    for (int i = threadIdx.x; i < parts; i += kClipThreads)
+        s += part[i];
+    const double size = sqrt(group_sum64(s, red));
+    if (norm && blockIdx.x == 0 && threadIdx.x == 0)
+        *norm = (float)size;
+    // a norm that is not finite changes nothing, nor does one within the limit
+    const bool clips = size > max_norm && size < INFINITY;
+    const double factor = clips ? max_norm / size : 1.0;
+    clip_walk(t, [&](int i, int64_t at) {
+        if (!clips && t.in[i] == t.out[i])
+            return;
+        if (t.dt[i] == DENSE_BF16)
+            chunk_scale((const bf16 *)t.in[i], (bf16 *)t.out[i], at, t.n[i], factor);
+        else if (t.dt[i] == DENSE_FP16)
+            chunk_scale((const f16 *)t.in[i], (f16 *)t.out[i], at, t.n[i], factor);
+        else
+            chunk_scale((const float *)t.in[i], (float *)t.out[i], at, t.n[i], factor);
+    });
+}
+
+}  // namespace dense

@@ -17,6 +17,7 @@ typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef float v16f __attribute__((ext_vector_type(16)));
 typedef int v4i __attribute__((ext_vector_type(4)));
+typedef int v8i __attribute__((ext_vector_type(8)));
 typedef int v16i __attribute__((ext_vector_type(16)));
 typedef short v4s __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) v4s lds_v4s;
@@ -27,10 +28,18 @@ constexpr int kCUs = 256;
 // it returns zeros.
 constexpr int kOutOfRange = (int)0x80000000u;
 
+// 8-bit floating point, as bytes: e4m3 (3 bits of mantissa, NaN, no infinities) and e5m2
+struct f8e4 { uint8_t bits; };
+struct f8e5 { uint8_t bits; };
+template <typename T> constexpr bool is_int = __is_same(T, int8_t);
+template <typename T> constexpr bool is_f8 = __is_same(T, f8e4) || __is_same(T, f8e5);
+
 template <typename T> struct Code;
 template <> struct Code<int8_t> { static constexpr int v = DENSE_INT8; };
 template <> struct Code<bf16> { static constexpr int v = DENSE_BF16; };
 template <> struct Code<f16> { static constexpr int v = DENSE_FP16; };
+template <> struct Code<f8e4> { static constexpr int v = DENSE_E4M3; };
+template <> struct Code<f8e5> { static constexpr int v = DENSE_E5M2; };
 template <> struct Code<float> { static constexpr int v = DENSE_FP32; };
 
 // C values at any element-aligned address.  gfx950 runs with unaligned vector

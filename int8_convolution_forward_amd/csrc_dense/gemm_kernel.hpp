@@ -1,6 +1,6 @@
 // Tiled matrix product for gfx950: C[m, n] = sum_k A(m, k) B(n, k) with the
-// dense layer's epilogue, operands BF16, FP16 (32-bit float sums) or INT8
-// (32-bit integer sums).
+// dense layer's epilogue, operands BF16, FP16 (32-bit float sums), INT8
+// (32-bit integer sums) or 8-bit floating point with scales (32-bit float sums).
 //
 // A workgroup of four waves computes a TM x TN tile.  Both operands stream from
 // memory straight into rings of LDS stages (buffer_load ... lds, 16 bytes a
@@ -61,6 +61,11 @@ struct GemmArgs {
     int part_ld;
     void *part;            // split: partial sums [split][M][part_ld], or null
     Epilogue epi;
+    // 8-bit floating point: the exponents of the operands' scales, a byte for 128 inner elements
+    const uint8_t *sa, *sb;
+    int64_t ldsa, ldsb;    // bytes between rows
+    int sb_shift;          // 7: one row of them for 128 rows of B, 0: for each
+    int kblocks;           // bytes of a row
 };
 
 // acc += the 16x16 product, in place in accumulation registers.  Written as an
@@ -78,7 +83,7 @@ __device__ __forceinline__ void mfma16_acc(v4i a, v4i b, typename Acc4<T>::type 
         asm volatile("v_mfma_" NAME " %0, %1, %2, %0" : "+v"(c) : "v"(a), "v"(b));   \
     else                                                                             \
         asm volatile("v_mfma_" NAME " %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b))
-    if constexpr (sizeof(T) == 1) {
+    if constexpr (is_int<T>) {
         DENSE_MFMA("i32_16x16x64_i8");
     } else if constexpr (__is_same(T, bf16)) {
         DENSE_MFMA("f32_16x16x32_bf16");
@@ -88,7 +93,57 @@ __device__ __forceinline__ void mfma16_acc(v4i a, v4i b, typename Acc4<T>::type 
 #undef DENSE_MFMA
 }
 
-// More wait states than a result of the instruction above needs.
+// The same of 8-bit floating point: 128 bytes of the inner dimension, one
+// instruction of 32 cycles, and the two operands' scales.  A scale is a power of
+// two, 2^(byte - 127), which the matrix unit applies itself: the lowest byte of sa
+// and sb.  (With scales of 32 bits every block's sums would go through the vector
+// unit: four multiply-adds for each matrix instruction, and sums in ordinary
+// registers, of which a 256x256 tile has too few.)
+//
+// The instruction adds the products of eight consecutive inner elements with
+// their exponents aligned: what lies more than 13 bits below the largest of the
+// eight is cut off.  Beyond that its sums are those of 32 bits.  Against 64 bits
+// that leaves 2.7e-5 of a result's norm (K = 2048, Gaussian values), which the
+// rounding to a 16-bit output, 1.7e-3 or 2.1e-4, hides; products with a 32-bit
+// output take their operands as BF16 instead, which is exact.
+template <typename T, bool VGPR>
+__device__ __forceinline__ void mfma16_scaled(v8i a, v8i b, v4f &c, int sa, int sb)
+{
+#define DENSE_MFMA(WHERE, FORMAT)                                                                               \
+    asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0]" FORMAT            \
+                 : WHERE(c) : "v"(a), "v"(b), "v"(sa), "v"(sb))
+    if constexpr (__is_same(T, f8e4) && VGPR)
+        DENSE_MFMA("+v", "");
+    else if constexpr (__is_same(T, f8e4))
+        DENSE_MFMA("+a", "");
+    else if constexpr (VGPR)
+        DENSE_MFMA("+v", " cbsz:1");
+    else
+        DENSE_MFMA("+a", " cbsz:1");
+#undef DENSE_MFMA
+}
+
+// Bytes k .. k+3 of a row of n scales as a word (zeros past its end), from any
+// address, without reading outside the row.
+__device__ __forceinline__ int scale_word(const uint8_t *row, int k, int n)
+{
+    if (n >= 4) {
+        const int at = min(k, n - 4), by = k - at;
+        const Pack<uint8_t, 4> w = *(const Pack<uint8_t, 4> *)(row + at);
+        return by < 4 ? (int)(__builtin_bit_cast(unsigned, w) >> (8 * by)) : 0;
+    }
+    unsigned v = 0;
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+        if (k + i < n)
+            v |= (unsigned)row[k + i] << (8 * i);
+    return (int)v;
+}
+
+// Another lane's value by way of the LDS crossbar; `at`: four times its number
+__device__ __forceinline__ int from_lane(int at, int v) { return __builtin_amdgcn_ds_bpermute(at, v); }
+
+// More wait states than a result of the instructions above needs.
 __device__ __forceinline__ void mfma_drain()
 {
     asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
@@ -189,7 +244,7 @@ __device__ __forceinline__ void finish_whole(const Epilogue &e, typename Acc4<T>
                         res[i][u] = buffer_load<FN>(rsd, vr, (16 * (x + i) + u) * (int)e.ldr * 2);
         }
         float xs[4] = {1.0f, 1.0f, 1.0f, 1.0f};
-        if constexpr (sizeof(T) == 1) {
+        if constexpr (is_int<T>) {
             if (e.x_scale)
 #pragma unroll
                 for (int u = 0; u < 4; ++u)
@@ -200,7 +255,7 @@ __device__ __forceinline__ void finish_whole(const Epilogue &e, typename Acc4<T>
             float z[FN];
 #pragma unroll
             for (int y = 0; y < FN; ++y) {
-                if constexpr (sizeof(T) == 1)
+                if constexpr (is_int<T>)
                     z[y] = __builtin_fmaf((float)acc[x][y][u], xs[u] * ws[y], bs[y]);
                 else
                     z[y] = acc[x][y][u] + bs[y];
@@ -533,6 +588,133 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs &g, uint8_t *smem, int 
         }
     };
 
+    // 8-bit floating point: a matrix instruction takes all 128 bytes of a stage, so
+    // the fragments of one stage are as many registers as two of its halves have
+    // above.  A half of a stage is half of the rows' blocks: it goes through the
+    // columns' blocks one after the other, and once the second half is done with
+    // one, that fragment is read anew from the next stage.
+    //
+    // Scales: lane 16 g + r of a word va[x] (vb[y]) has those of four stages, 4 g .. 4 g + 3 of
+    // sixteen, of row r of a block.  The words are rotated by a byte at each stage,
+    // and the sixteen lanes whose turn it is give them to all (sa, sb).
+    // Loading them takes a wait for everything on its way, once in sixteen stages:
+    // their bytes have no room in LDS beside the rings of the 256x256 tile.
+    constexpr int HX = FM / 2;
+    v8i fa[FM], fb[FN];
+    int sa[FM], sb[FN], va[FM], vb[FN];
+    int perm = (lane & 15) * 4;
+    auto load_scales = [&](int it) __attribute__((always_inline)) {
+        const int k = stage0 + it + 4 * (lane >> 4);
+#pragma unroll
+        for (int x = 0; x < FM; ++x)
+            va[x] = scale_word(g.sa + (int64_t)min(m0 + wm + 16 * x + (lane & 15), g.M - 1) * g.ldsa, k, g.kblocks);
+#pragma unroll
+        for (int y = 0; y < FN; ++y)
+            vb[y] = scale_word(g.sb + (int64_t)(min(n0 + wn + FN * (lane & 15) + y, g.N - 1) >> g.sb_shift) * g.ldsb, k,
+                               g.kblocks);
+    };
+    auto f8_read_a = [&](int x, int slot) __attribute__((always_inline)) {
+        const uint8_t *base = smem + slot * A_BYTES;
+        const v4i lo = read_rows(base, wm + x * 16, 0), hi = read_rows(base, wm + x * 16, 1);
+        fa[x] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    };
+    auto f8_read_b = [&](int y, int slot) __attribute__((always_inline)) {
+        const uint8_t *base = smem + A_RING + slot * B_BYTES;
+        const v4i lo = read_b_rows(base, y, 0), hi = read_b_rows(base, y, 1);
+        fb[y] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    };
+    auto next_scale = [](int from, int &v) __attribute__((always_inline)) {
+        const int s = from_lane(from, v);
+        v = (int)__builtin_amdgcn_alignbyte(v, v, 1);
+        return s;
+    };
+    // what the first half of stage 0 takes
+    auto f8_first = [&]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int x = 0; x < HX; ++x) {
+            f8_read_a(x, 0);
+            sa[x] = next_scale(perm, va[x]);
+        }
+#pragma unroll
+        for (int y = 0; y < FN; ++y) {
+            f8_read_b(y, 0);
+            sb[y] = next_scale(perm, vb[y]);
+        }
+    };
+    auto f8_stage = [&](auto it) __attribute__((always_inline)) {
+        constexpr int NH = HX * FN, EARLY = NH / 4;
+        const int next = (it & 3) == 3 ? (perm + 64) & 255 : perm;  // whose scales are the next stage's
+        const int an = a_slot + 1 == NSA ? 0 : a_slot + 1, bn = b_slot + 1 == NSB ? 0 : b_slot + 1;
+        for_each<2 * NH>([&](auto ic) __attribute__((always_inline)) {
+            constexpr int h = decltype(ic)::value / NH, i = decltype(ic)::value % NH;
+            constexpr bool last = h == 1;
+            constexpr int first = last ? EARLY : 0, np = NH - first;
+            constexpr int l0 = last ? 0 : LH, nl = last ? LH : LPS - LH;
+            constexpr int y = i / HX, x = h * HX + i % HX;
+            if constexpr (last && i == 0) {  // this stage's scales are out of the words: the next sixteen stages'
+                if ((it & 15) == 15 && stage0 + it + 1 < stage_end)
+                    load_scales(it + 1);
+            }
+            if constexpr (last && i == EARLY) {
+                wait_vm_lgkm0<(NSA - 2) * AL + (NSB - 2) * BL>();
+                __builtin_amdgcn_s_barrier();
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            mfma16_scaled<T, (x >= kLastAcc)>(fa[x], fb[y], acc[x][y], sa[x], sb[y]);
+            if constexpr (last && i == 0) {  // the stage whose loads start after the barrier
+                advance(b_rsrc, b_step);
+                next_b();
+                open_b();
+                advance(a_rsrc, a_step);
+                next_a();
+                open_a();
+            }
+            if constexpr (i == (first > 0 ? first - 1 : 0) && nl > 0)
+                aim(Size<l0>{});
+            if constexpr (!last) {
+                // the second half's rows of this stage
+                for_each<HX>([&](auto rc) __attribute__((always_inline)) {
+                    constexpr int r = decltype(rc)::value;
+                    if constexpr (i == r * NH * 3 / 4 / HX) {
+                        f8_read_a(HX + r, a_slot);
+                        sa[HX + r] = next_scale(perm, va[HX + r]);
+                    }
+                });
+            } else {
+                // the next stage's: columns as they are done with, the first half's rows
+                for_each<FN>([&](auto rc) __attribute__((always_inline)) {
+                    constexpr int r = decltype(rc)::value;
+                    constexpr int done = (r + 1) * HX - 1, at = done > EARLY + r ? done : EARLY + r;
+                    if constexpr (i == (at < NH ? at : NH - 1)) {
+                        f8_read_b(r, bn);
+                        sb[r] = next_scale(next, vb[r]);
+                    }
+                });
+                for_each<HX>([&](auto rc) __attribute__((always_inline)) {
+                    constexpr int r = decltype(rc)::value, at = EARLY + 2 + 2 * r;
+                    if constexpr (i == (at < NH ? at : NH - 1)) {
+                        f8_read_a(r, an);
+                        sa[r] = next_scale(next, va[r]);
+                    }
+                });
+            }
+            if constexpr (i >= first) {
+                constexpr int p = i - first;
+                constexpr int d0 = p * nl / np, d1 = (p + 1) * nl / np;
+                for_each<d1 - d0>([&](auto oc) __attribute__((always_inline)) {
+                    constexpr int o = l0 + d0 + decltype(oc)::value;
+                    load_one(Size<o>{});
+                    if constexpr (o + 1 < l0 + nl)
+                        aim(Size<o + 1>{});
+                });
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        });
+        a_slot = an;
+        b_slot = bn;
+        perm = next;
+    };
+
     const int nloop = max(stage_end - stage0, 0);
     if (nloop > 0) {
         // The rings filled in the order of the loop: stage by stage, B before
@@ -562,15 +744,24 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs &g, uint8_t *smem, int 
             open_a();
             load_part(Size<0>{}, Size<(decltype(sc)::value < NSB - 1 ? LPS : LH)>{});
         });
+        // the scales' loads, which the compiler waits for, come before stage 0 is waited for
+        if constexpr (is_f8<T>)
+            load_scales(0);
         // everything but the loads after stage 0's
         wait_vm_lgkm0<(NSB - 2) * LPS + LH + (NSA > NSB ? AL : 0)>();
         __builtin_amdgcn_s_barrier();
+        if constexpr (is_f8<T>) {
+            f8_first();
+            for (int it = 0; it < nloop; ++it)
+                f8_stage(it);
+        } else {
 #pragma unroll
-        for (int i = 0; i < NRD; ++i)
-            read_one(0, 0, 0, 0, i);
-        for (int it = 0; it < nloop; ++it) {
-            half(Size<0>{});
-            half(Size<1>{});
+            for (int i = 0; i < NRD; ++i)
+                read_one(0, 0, 0, 0, i);
+            for (int it = 0; it < nloop; ++it) {
+                half(Size<0>{});
+                half(Size<1>{});
+            }
         }
         wait_vm_lgkm0<0>();  // the trailing loads of zeros still write to the rings
         mfma_drain();
@@ -632,7 +823,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs &g, uint8_t *smem, int 
             constexpr int x = decltype(bc)::value / FN, y = decltype(bc)::value % FN;
             const typename Acc4<T>::type v = acc[x0 + x][y];
             v4f o;
-            if constexpr (ES == 1)  // partial sums stay integers (their bits travel as floats)
+            if constexpr (is_int<T>)  // partial sums stay integers (their bits travel as floats)
                 o = g.part ? __builtin_bit_cast(v4f, v) : v4f{(float)v.x, (float)v.y, (float)v.z, (float)v.w};
             else
                 o = v;
@@ -672,7 +863,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs &g, uint8_t *smem, int 
                         *(v4f *)(p + 4) = *(v4f *)&v[u][4];
                     }
             } else {
-                finish<ES == 1, U, 8>(e, m, RS, g.M, n, cnt, v, bs, ws);
+                finish<is_int<T>, U, 8>(e, m, RS, g.M, n, cnt, v, bs, ws);
             }
         }
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");

@@ -27,6 +27,8 @@ constexpr Tile kTile[kTiles] = {
 // rows only); false if the combination does not exist or the launch failed.
 bool launch_gemm_bf16(int tile, bool a_cols, bool b_cols, const GemmArgs &g, int splits, hipStream_t stream);
 bool launch_gemm_f16(int tile, bool a_cols, bool b_cols, const GemmArgs &g, int splits, hipStream_t stream);
+bool launch_gemm_f8e4(int tile, const GemmArgs &g, int splits, hipStream_t stream);  // the first operand's type
+bool launch_gemm_f8e5(int tile, const GemmArgs &g, int splits, hipStream_t stream);
 bool launch_gemm_i8(int tile, bool a_cols, bool b_cols, const GemmArgs &g, int splits, hipStream_t stream);
 
 // Both gradients' products with tile kPairTile, unsplit, and the bias gradient's

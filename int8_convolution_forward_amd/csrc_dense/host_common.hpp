@@ -22,11 +22,10 @@ inline bool launch_fits(int64_t wgs, int threads) { return wgs < ((int64_t)1 << 
 // Largest stride: a byte offset of kMaxDim rows then stays within 63 bits.
 constexpr int64_t kMaxStride = (int64_t)1 << 30;
 
-// dims and strides of a matrix; strides along dims of size 1 become 1 (columns) or the packed pitch (rows)
-inline conv_i8_status_t check_mat(dense_mat_t *m, bool output)
+// dims and strides of a matrix of elements of `size` bytes; strides along dims of size 1 become 1 (columns) or the
+// packed pitch (rows)
+inline conv_i8_status_t check_mat_of(dense_mat_t *m, bool output, int64_t size)
 {
-    if (size_of(m->dtype) == 0)
-        return CONV_I8_ERR_DTYPE;
     if (m->rows < 0 || m->cols < 0)
         return CONV_I8_ERR_DIMS;
     if (m->rows > kMaxDim || m->cols > kMaxDim)
@@ -44,10 +43,37 @@ inline conv_i8_status_t check_mat(dense_mat_t *m, bool output)
     if (m->rows > 0 && m->cols > 0) {
         if (!m->ptr)
             return CONV_I8_ERR_NULL;
-        if ((uintptr_t)m->ptr % size_of(m->dtype))
+        if ((uintptr_t)m->ptr % size)
             return CONV_I8_ERR_PARAM;
     }
     return CONV_I8_OK;
+}
+
+inline conv_i8_status_t check_mat(dense_mat_t *m, bool output)
+{
+    return size_of(m->dtype) == 0 ? CONV_I8_ERR_DTYPE : check_mat_of(m, output, size_of(m->dtype));
+}
+
+inline bool is_fp8(int64_t dt) { return dt == DENSE_E4M3 || dt == DENSE_E5M2; }
+
+// Values of a block share a scale.
+constexpr int64_t kBlock = 128;
+
+// The scales of a matrix of `rows` rows and `cols` columns: for blocks of a row
+// or, where `tiles` is given, for either kind of block, which it then says.
+inline conv_i8_status_t check_scales(dense_mat_t *s, int64_t rows, int64_t cols, bool output, bool *tiles)
+{
+    if (s->dtype != DENSE_E8M0)
+        return CONV_I8_ERR_DTYPE;
+    const conv_i8_status_t st = check_mat_of(s, output, 1);
+    if (st != CONV_I8_OK)
+        return st;
+    const int64_t blocks = (rows + kBlock - 1) / kBlock;
+    if (s->cols != (cols + kBlock - 1) / kBlock || (s->rows != rows && !(tiles && s->rows == blocks)))
+        return CONV_I8_ERR_OUT_DIMS;
+    if (tiles)
+        *tiles = s->rows != rows;
+    return s->col_stride == 1 ? CONV_I8_OK : CONV_I8_ERR_STRIDES;
 }
 
 // a vector of n elements; an absent one (DENSE_NONE) gets a null pointer

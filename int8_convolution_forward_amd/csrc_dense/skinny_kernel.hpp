@@ -68,7 +68,7 @@ __device__ __forceinline__ void skinny_finish(const SkinnyArgs &g, typename Acc4
         if (m >= g.M || n >= g.N)
             continue;
         float z;
-        if constexpr (sizeof(T) == 1) {
+        if constexpr (is_int<T>) {
             int s = 0;
 #pragma unroll
             for (int k = 0; k < W; ++k)
