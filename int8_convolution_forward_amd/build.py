@@ -24,7 +24,8 @@ HEADERS = [os.path.join(CSRC, f) for f in ("kernel_common.hpp", "igemm_kernel.hp
 DENSE_CSRC = os.path.join(PKG, "csrc_dense")
 DENSE_LIB = os.path.join(LIB_DIR, "libdense.so")
 DENSE_SOURCES = [os.path.join(DENSE_CSRC, f) for f in ("linear.hip", "gemm_bf16.hip", "gemm_f16.hip", "gemm_i8.hip",
-                                                      "norm.hip", "gemm_f8.hip", "fp8.hip", "residual_norm.hip", "clip.hip")]
+                                                      "norm.hip", "gemm_f8.hip", "fp8.hip", "residual_norm.hip", "residual_norm_bf16.hip", "residual_norm_f16.hip",
+                                                      "residual_norm_f32.hip", "clip.hip")]
 # ... and the Python module that hands tensors to it (host code only)
 DENSE_BIND_SOURCE = os.path.join(DENSE_CSRC, "bind.cpp")
 DENSE_BIND = os.path.join(LIB_DIR, "_dense.so")

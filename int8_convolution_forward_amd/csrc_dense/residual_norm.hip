@@ -3,30 +3,45 @@
 #include <string.h>
 
 #include "host_common.hpp"
-#include "residual_norm_kernel.hpp"
+#include "residual_norm_launch.hpp"
 
 namespace dense {
 namespace {
 
 constexpr int64_t kWsAlign = 256;
-// Longest rows that stay in registers, forward and backward.
-constexpr int64_t kRow = 16384, kBackRow = 8192;
 
-template <typename T> struct As { typedef T type; };
-template <bool B> struct Flag { static constexpr bool value = B; };
+// The sums over workgroups: blockIdx.y 0 dweight, 1 dbias, 2 dpost_weight, 3 + g row g of dgate.
+struct ResNormSumArgs {
+    const float *part;
+    int64_t part_ld;
+    int wgs, chunks, D, dt;
+    void *out[3], *dgate;             // null: not wanted
+    int64_t lddg;
+};
 
-// f(As<type>, Flag<RMS>)
-template <typename F>
-void by_type(int64_t dt, bool rms, F f)
+__global__ __launch_bounds__(32 * kSumGroups) void residual_norm_sums_kernel(const ResNormSumArgs a)
 {
-    auto with = [&](auto t) { rms ? f(t, Flag<true>{}) : f(t, Flag<false>{}); };
-    if (dt == DENSE_BF16)
-        with(As<bf16>{});
-    else if (dt == DENSE_FP16)
-        with(As<f16>{});
-    else
-        with(As<float>{});
+    __shared__ float red[kSumGroups][33];
+    const int job = blockIdx.y;
+    ColSumArgs c;
+    c.ld = 4 * a.part_ld;
+    c.cols = c.split = c.valid = a.D;
+    c.out1 = nullptr;
+    c.dt = a.dt;
+    if (job < 3) {
+        c.part = a.part + job * a.part_ld;
+        c.rows = a.wgs;
+        c.out0 = a.out[job];
+    } else {
+        const int g = job - 3;
+        c.part = a.part + ((int64_t)g * a.chunks * 4 + 3) * a.part_ld;
+        c.rows = a.chunks;
+        c.out0 = (char *)a.dgate + g * a.lddg * (a.dt == DENSE_FP32 ? 4 : 2);
+    }
+    if (c.out0)
+        column_sums<32>(c, blockIdx.x, red);
 }
+
 
 // Present, [M, D] of type dt, rows contiguous
 conv_i8_status_t check_rows(dense_mat_t *m, int64_t M, int64_t D, int64_t dt, bool output)
@@ -52,12 +67,6 @@ conv_i8_status_t check_gate(dense_mat_t *g, int64_t M, int64_t D, int64_t dt, bo
     if (g->rows < 1 ? M > 0 || g->rows < 0 : M % g->rows != 0)
         return CONV_I8_ERR_DIMS;
     return CONV_I8_OK;
-}
-
-inline unsigned capped(int64_t wgs, int threads)
-{
-    const int64_t most = threads <= 256 ? 1 << 21 : 1 << 16;
-    return (unsigned)(wgs < most ? wgs : most);
 }
 
 conv_i8_status_t analyze(const dense_residual_norm_t *args, dense_residual_norm_t *d)
@@ -107,55 +116,14 @@ conv_i8_status_t analyze(const dense_residual_norm_t *args, dense_residual_norm_
     return CONV_I8_OK;
 }
 
-template <typename T, bool RMS, bool Q8, int P, int V>
-void launch_rows(const ResNormArgs &a, hipStream_t s)
-{
-    constexpr int rows = norm_threads(P) / P;
-    constexpr bool hold = P <= 512;
-    int64_t wgs = ceil_div(a.M, rows);
-    if (hold && wgs > 1024)
-        wgs = P > 256 || wgs <= 2048 ? 1024 : ceil_div(wgs, 2);
-    const dim3 grid(capped(wgs, norm_threads(P))), block(norm_threads(P));
-    if (a.D % 8 == 0)
-        hipLaunchKernelGGL((residual_norm_kernel<T, P, V, hold, false, RMS, Q8>), grid, block, 0, s, a);
-    else
-        hipLaunchKernelGGL((residual_norm_kernel<T, P, V, hold, true, RMS, Q8>), grid, block, 0, s, a);
-}
-
-template <typename T, bool RMS, bool Q8>
-void launch(const ResNormArgs &a, hipStream_t s)
-{
-    const int D = a.D;
-    // a wave per row while that gives each CU a few waves, else a workgroup per row
-    const bool few = a.M < 4 * kCUs;
-    if (D < 8)
-        hipLaunchKernelGGL((residual_norm_any_kernel<T, 64, RMS, Q8>), dim3(capped(a.M, 64)), dim3(64), 0, s, a);
-    else if (D > kRow)
-        hipLaunchKernelGGL((residual_norm_any_kernel<T, 1024, RMS, Q8>), dim3(capped(a.M, 1024)), dim3(1024), 0, s, a);
-    else if (D <= 512)
-        launch_rows<T, RMS, Q8, 64, 1>(a, s);
-    else if (D <= 1024 && !few)
-        launch_rows<T, RMS, Q8, 64, 2>(a, s);
-    else if (D <= 2048)
-        launch_rows<T, RMS, Q8, 256, 1>(a, s);
-    else if (D <= 4096)
-        launch_rows<T, RMS, Q8, 512, 1>(a, s);
-    else if (D <= 8192)
-        launch_rows<T, RMS, Q8, 512, 2>(a, s);
-    else
-        launch_rows<T, RMS, Q8, 1024, 2>(a, s);
-}
-
 struct BackPlan {
     dense_residual_norm_backward_t d;
     int64_t M, D;
     bool sums;
-    int groups = 1, chunks = 1, each = 1, wgs = 0;
+    int groups = 1, chunks = 1, wgs = 0;
     int64_t part_ld = 0, part_bytes = 0, ws_bytes = 0;
-    bool any() const { return D < 8 || D > kBackRow; }
+    bool any() const { return !back_in_registers(D); }
 };
-
-constexpr int back_threads(int64_t D) { return D <= 1024 ? 64 : D <= 2048 ? 256 : 512; }
 
 conv_i8_status_t analyze(const dense_residual_norm_backward_t *args, BackPlan *p)
 {
@@ -218,56 +186,19 @@ conv_i8_status_t analyze(const dense_residual_norm_backward_t *args, BackPlan *p
     p->sums = dgate || d.dweight.dtype != DENSE_NONE || d.dbias.dtype != DENSE_NONE || d.dpost_weight.dtype != DENSE_NONE;
     p->part_ld = round_up(D, 8);
     p->groups = gate ? (int)d.gate.rows : 1;
-    // Workgroups: one or two on a CU, but four rows at least for each of their groups of
+    // Workgroups: one or two on a CU, but two rows at least for each of their groups of
     // threads; more leave more partial sums.  One takes part of the rows of a row of the gate or
     // those of several.
     const int threads = norm_threads(back_threads(D)), rpw = threads / back_threads(D);
-    const int64_t most = threads <= 256 ? 2 * kCUs : kCUs, rows = p->any() ? 64 : 4 * rpw;
+    const int64_t most = threads <= 256 ? 2 * kCUs : kCUs, rows = p->any() ? 64 : 2 * rpw;
     const int64_t want = ceil_div(M, rows) < most ? ceil_div(M, rows) : most;
     if (M > 0) {
-        if (want >= 2 * p->groups)
-            p->chunks = (int)(want / p->groups);
-        else
-            p->each = (int)ceil_div(p->groups, want);
-        p->wgs = (int)(p->chunks > 1 ? (int64_t)p->groups * p->chunks : ceil_div(p->groups, p->each));
+        p->chunks = want >= 2 * p->groups ? (int)(want / p->groups) : 1;
+        p->wgs = p->chunks > 1 || want > p->groups ? p->groups * p->chunks : (int)want;
     }
     p->part_bytes = p->sums && p->wgs ? round_up((int64_t)p->wgs * 4 * p->part_ld * 4, kWsAlign) : 0;
     p->ws_bytes = p->part_bytes + (p->sums && p->any() ? round_up(M * 8, kWsAlign) : 0);
     return CONV_I8_OK;
-}
-
-template <typename T, bool RMS, bool POST, int P, int V, int AHEAD>
-void launch_back_rows(const ResNormBackArgs &a, int wgs, hipStream_t s)
-{
-    const dim3 grid((unsigned)wgs), block(norm_threads(P));
-    if (a.D % 8 == 0)
-        hipLaunchKernelGGL((residual_norm_backward_kernel<T, P, V, AHEAD, false, RMS, POST>), grid, block, 0, s, a);
-    else
-        hipLaunchKernelGGL((residual_norm_backward_kernel<T, P, V, AHEAD, true, RMS, POST>), grid, block, 0, s, a);
-}
-
-template <typename T, bool RMS, bool POST>
-void launch_back(const ResNormBackArgs &a, const BackPlan &p, hipStream_t s)
-{
-    if (p.any()) {
-        if (p.D < 8)
-            hipLaunchKernelGGL((residual_norm_backward_any_kernel<T, 64, RMS, POST>), dim3(capped(a.M, 64)), dim3(64), 0, s, a);
-        else
-            hipLaunchKernelGGL((residual_norm_backward_any_kernel<T, 1024, RMS, POST>), dim3(capped(a.M, 1024)), dim3(1024), 0, s, a);
-        if (p.sums)
-            hipLaunchKernelGGL((residual_norm_columns_kernel<T, RMS, POST>), dim3((unsigned)ceil_div(p.D, 2048), (unsigned)p.wgs),
-                               dim3(256), 0, s, a);
-    } else if (p.D <= 512) {
-        launch_back_rows<T, RMS, POST, 64, 1, 1>(a, p.wgs, s);
-    } else if (p.D <= 1024) {
-        launch_back_rows<T, RMS, POST, 64, 2, (sizeof(T) == 2)>(a, p.wgs, s);
-    } else if (p.D <= 2048) {
-        launch_back_rows<T, RMS, POST, 256, 1, 1>(a, p.wgs, s);
-    } else if (p.D <= 4096) {
-        launch_back_rows<T, RMS, POST, 512, 1, 1>(a, p.wgs, s);
-    } else {
-        launch_back_rows<T, RMS, POST, 512, 2, 0>(a, p.wgs, s);
-    }
 }
 
 }  // namespace
@@ -318,11 +249,14 @@ conv_i8_status_t dense_residual_norm(const dense_residual_norm_t *args, void *st
     a.rstd = (float *)const_cast<void *>(d.rstd.ptr);
     a.post_mean = (float *)const_cast<void *>(d.post_mean.ptr);
     a.post_rstd = (float *)const_cast<void *>(d.post_rstd.ptr);
-    by_type(d.x.dtype, d.kind == DENSE_RMS_NORM, [&](auto t, auto rms) {
-        typedef typename decltype(t)::type T;
-        constexpr bool RMS = decltype(rms)::value;
-        q8 ? launch<T, RMS, true>(a, (hipStream_t)stream) : launch<T, RMS, false>(a, (hipStream_t)stream);
-    });
+    const bool rms = d.kind == DENSE_RMS_NORM;
+    hipStream_t s = (hipStream_t)stream;
+    if (d.x.dtype == DENSE_BF16)
+        launch_residual_norm_bf16(a, rms, q8, s);
+    else if (d.x.dtype == DENSE_FP16)
+        launch_residual_norm_f16(a, rms, q8, s);
+    else
+        launch_residual_norm_f32(a, rms, q8, s);
     return hipGetLastError() == hipSuccess ? CONV_I8_OK : CONV_I8_ERR_HIP;
 }
 
@@ -381,10 +315,10 @@ conv_i8_status_t dense_residual_norm_backward(const dense_residual_norm_backward
     a.M = (int)p.M;
     a.D = (int)p.D;
     a.d = (float)a.D;
+    a.inv_d = 1.0f / a.d;
     a.alpha = (float)d.alpha;
     a.groups = p.groups;
     a.chunks = p.chunks;
-    a.each = p.each;
     a.gate_rows = p.M > 0 ? (int)(p.M / p.groups) : 1;
     a.part = p.sums ? (float *)workspace : nullptr;
     a.part_ld = p.part_ld;
@@ -392,11 +326,13 @@ conv_i8_status_t dense_residual_norm_backward(const dense_residual_norm_backward
     hipStream_t s = (hipStream_t)stream;
     const bool post = d.post_weight.dtype != DENSE_NONE;
     if (p.M > 0) {
-        by_type(d.r.dtype, d.kind == DENSE_RMS_NORM, [&](auto t, auto rms) {
-            typedef typename decltype(t)::type T;
-            constexpr bool RMS = decltype(rms)::value;
-            post ? launch_back<T, RMS, true>(a, p, s) : launch_back<T, RMS, false>(a, p, s);
-        });
+        const bool rms = d.kind == DENSE_RMS_NORM;
+        if (d.r.dtype == DENSE_BF16)
+            launch_residual_norm_backward_bf16(a, rms, post, p.wgs, s);
+        else if (d.r.dtype == DENSE_FP16)
+            launch_residual_norm_backward_f16(a, rms, post, p.wgs, s);
+        else
+            launch_residual_norm_backward_f32(a, rms, post, p.wgs, s);
         if (hipGetLastError() != hipSuccess)
             return CONV_I8_ERR_HIP;
     }

@@ -30,6 +30,36 @@ struct ResNormArgs {
     float *mean, *rstd, *post_mean, *post_rstd;  // null: not written
 };
 
+// Two numbers a lane become one: lanes of the lower half then hold the sum of a's
+// halves, those of the upper half that of b's.
+__device__ __forceinline__ float fold_halves(float a, float b)
+{
+    const auto s = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(unsigned, a), __builtin_bit_cast(unsigned, b), false, false);
+    const unsigned x = s[0], y = s[1];
+    return __builtin_bit_cast(float, x) + __builtin_bit_cast(float, y);
+}
+
+// The same of the odd and even rows of sixteen lanes: rows 0 and 2 hold sums of a's, 1 and 3 of b's.
+__device__ __forceinline__ float fold_rows(float a, float b)
+{
+    const auto s = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(unsigned, a), __builtin_bit_cast(unsigned, b), false, false);
+    const unsigned x = s[0], y = s[1];
+    return __builtin_bit_cast(float, x) + __builtin_bit_cast(float, y);
+}
+
+template <int CTRL>
+__device__ __forceinline__ float add_dpp(float v)
+{
+    const int i = __builtin_bit_cast(int, v);
+    return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, i, CTRL, 0xf, 0xf, true));
+}
+
+// Sum of the sixteen lanes of a row, in all of them
+__device__ __forceinline__ float row16_sum(float v)
+{
+    return add_dpp<0x140>(add_dpp<0x141>(add_dpp<0x4E>(add_dpp<0xB1>(v))));
+}
+
 // Mean and sum of squared distances from it; RMS: 0 and the sum of squares.
 template <int P, int V, bool RMS>
 __device__ __forceinline__ void moments(float (&v)[V][8], int D, int t, float cols, float d, float2 *red, float &mean,
@@ -55,11 +85,11 @@ __global__ __launch_bounds__(norm_threads(P)) void residual_norm_kernel(const Re
     constexpr int NW = P > 64 ? P / 64 : 1;
     __shared__ float2 red[2][NW];
     const int t = threadIdx.x % P;
-    int64_t m = (int64_t)blockIdx.x * RPW + threadIdx.x / P;
+    int64_t m = (int64_t)blockIdx.x * RPW + (RPW > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / P) : 0);
     if (m >= a.M)
         return;  // whole waves; with P > 64 there is one row per workgroup
     const int64_t step = (int64_t)gridDim.x * RPW;
-    const float cols = (float)wave_columns<P, V>(a.D, P > 64 ? threadIdx.x >> 6 : 0);
+    const float cols = (float)wave_columns<P, V>(a.D, P > 64 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0);
 
     Raw8<T> x[V], h[V], g[V], w[V], b[V], pw[V];
     auto load = [&](int64_t m) __attribute__((always_inline)) {
@@ -315,6 +345,15 @@ __global__ __launch_bounds__(P) void residual_norm_any_kernel(const ResNormArgs 
 // either part of those of one row of the gate (chunks > 1; the partial sums are
 // added by residual_norm_sums_kernel) or those of whole rows of the gate, for which
 // it writes dgate itself.
+//
+// Bound by HBM and, nearly as much, by the vector unit (about 40 operations a value
+// with the widening of four inputs): 16384 x 4096 BF16 with both norms and eight
+// gates 154 us, 806 MB, 5.2 TB/s.  What took it there from 176: sums of a wave
+// folded two into one register before they are added up (a lane permutation for
+// each sum by itself takes four times the operations), means by a product instead
+// of a division, no condition per value inside a row.  A second workgroup on a CU
+// instead of the next row's loads in flight is slower (279 us: 128 registers spill),
+// so are two rows at a time (158).
 
 struct ResNormBackArgs {
     const void *dr, *dy, *r, *h, *gate, *weight, *post_weight;  // null: absent (dr: zeros)
@@ -323,22 +362,34 @@ struct ResNormBackArgs {
     int64_t lddr, lddy, ldr, ldh, ldg, lddx, lddh, lddg;
     int M, D;
     int gate_rows;                    // rows of a group: those that share a row of the gate, or all
-    int groups, chunks, each;         // workgroups of a group; groups of a workgroup (one of them is 1)
-    float alpha, d;
+    int groups, chunks;               // groups; workgroups of a group (1: a workgroup takes every so many groups)
+    float alpha, d, inv_d;
     float *part;                      // [workgroup][4][part_ld]: dweight, dbias, dpost_weight, dgate; null: not computed
     int64_t part_ld;
     float2 *row_sums;                 // residual_norm_backward_any_kernel: both means of a row's first norm
 };
 
-template <typename T, int P, int V, int AHEAD, bool TAIL, bool RMS, bool POST>
-__global__ __launch_bounds__(norm_threads(P)) void residual_norm_backward_kernel(const ResNormBackArgs a)
+// A thread group takes U rows at a time, so that one barrier joins the sums of all
+// of them, and has the next ones' loads in flight (AHEAD).  Between its steps it
+// keeps the rows as they lie in memory and widens them again: the values in 32
+// bits would take twice the registers.
+template <typename T>
+__device__ __forceinline__ void as_in_memory(Raw8<T> &r)
+{
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(T) / 2); ++i)
+        asm volatile("" : "+v"(r.w[i]));
+}
+
+template <typename T, int P, int V, int U, bool AHEAD, int OCC, bool TAIL, bool RMS, bool POST>
+__global__ __launch_bounds__(norm_threads(P), OCC) void residual_norm_backward_kernel(const ResNormBackArgs a)
 {
     constexpr int RPW = norm_threads(P) / P;
     constexpr int NW = P > 64 ? P / 64 : 1;
     constexpr int NS = POST ? 4 : 3;      // sums: dweight, dbias, dgate, dpost_weight
-    __shared__ float2 red[2][NW];
+    __shared__ __attribute__((aligned(16))) float red[2][NW][4];
     __shared__ float cs[RPW > 1 ? RPW : 1][RPW > 1 ? P * 8 : 1];
-    const int t = threadIdx.x % P, sub = threadIdx.x / P;
+    const int t = threadIdx.x % P, sub = RPW > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / P) : 0;
     const bool use_h = POST || a.gate;
 
     Raw8<T> w[V], pw[V], g[V];
@@ -382,170 +433,216 @@ __global__ __launch_bounds__(norm_threads(P)) void residual_norm_backward_kernel
         }
     };
 
-    struct Rows {
+    struct Row {
         Raw8<T> r[V], dy[V], dr[V], h[V];
         float mean, rstd, post_mean, post_rstd;
-    } ring;
-    auto load = [&](int64_t m) __attribute__((always_inline)) {
-        load_row<T, P, V>((const T *)a.r + m * a.ldr, a.D, t, ring.r);
-        load_row<T, P, V>((const T *)a.dy + m * a.lddy, a.D, t, ring.dy);
-        if (a.dr)
-            load_row<T, P, V>((const T *)a.dr + m * a.lddr, a.D, t, ring.dr);
-        if (use_h)
-            load_row<T, P, V>((const T *)a.h + m * a.ldh, a.D, t, ring.h);
-        ring.rstd = a.rstd[m];
-        ring.mean = RMS ? 0.0f : a.mean[m];
-        if constexpr (POST) {
-            ring.post_rstd = a.post_rstd[m];
-            ring.post_mean = RMS ? 0.0f : a.post_mean[m];
+    } ring[U];
+    auto load = [&](int64_t m, int64_t end) __attribute__((always_inline)) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {  // rows past the end repeat the last one
+            const int64_t at = min(m + u, end - 1);
+            load_row<T, P, V>((const T *)a.r + at * a.ldr, a.D, t, ring[u].r);
+            load_row<T, P, V>((const T *)a.dy + at * a.lddy, a.D, t, ring[u].dy);
+            if (a.dr)
+                load_row<T, P, V>((const T *)a.dr + at * a.lddr, a.D, t, ring[u].dr);
+            if (use_h)
+                load_row<T, P, V>((const T *)a.h + at * a.ldh, a.D, t, ring[u].h);
+            ring[u].rstd = a.rstd[at];
+            ring[u].mean = RMS ? 0.0f : a.mean[at];
+            if constexpr (POST) {
+                ring[u].post_rstd = a.post_rstd[at];
+                ring[u].post_mean = RMS ? 0.0f : a.post_mean[at];
+            }
         }
     };
     int set = 0;
-    // the sums of a row of two numbers a lane, and their means
-    auto means = [&](float &s1, float &s2) __attribute__((always_inline)) {
-        if constexpr (!RMS)
-            s1 = wave_sum(s1);
-        s2 = wave_sum(s2);
+    // Both sums of a lane's numbers of each row over its threads, as means.  A wave folds two numbers
+    // into one register and four of those into one, so that four sums cost little more than one.
+    auto means = [&](float (&s1)[U], float (&s2)[U]) __attribute__((always_inline)) {
+        static_assert(U == 1 || U == 2, "rows at a time");
+        float v = fold_halves(s1[0], s2[0]);
+        v = row16_sum(U == 2 ? fold_rows(v, fold_halves(s1[U - 1], s2[U - 1])) : v);
+        // U 1: rows of lanes 0, 1: s1's parts, 2, 3: s2's; U 2: s1 of both rows, then s2
+        float r[4];
         if constexpr (P > 64) {
-            if ((threadIdx.x & 63) == 0)
-                red[set][threadIdx.x >> 6] = make_float2(s1, s2);
+            if ((threadIdx.x & 15) == 0)
+                red[set][threadIdx.x >> 6][(threadIdx.x >> 4) & 3] = v;
             __syncthreads();
-            s1 = s2 = 0.0f;
 #pragma unroll
-            for (int i = 0; i < NW; ++i) {
-                s1 += red[set][i].x;
-                s2 += red[set][i].y;
-            }
+            for (int q = 0; q < 4; ++q)
+                r[q] = red[set][0][q];
+#pragma unroll
+            for (int i = 1; i < NW; ++i)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    r[q] += red[set][i][q];
             set ^= 1;  // the other set: a slow wave may still read this one
+        } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                r[q] = lane_value(v, 16 * q);
         }
-        s1 = RMS ? 0.0f : s1 / a.d;
-        s2 /= a.d;
+        if constexpr (U == 1) {
+            s1[0] = RMS ? 0.0f : (r[0] + r[1]) * a.inv_d;
+            s2[0] = (r[2] + r[3]) * a.inv_d;
+        } else {
+            s1[0] = RMS ? 0.0f : r[0] * a.inv_d;
+            s1[U - 1] = RMS ? 0.0f : r[1] * a.inv_d;
+            s2[0] = r[2] * a.inv_d;
+            s2[U - 1] = r[3] * a.inv_d;
+        }
+    };
+    // (v - mean) rstd of group i, 0 past the row's end, also where mean rstd is infinite
+    auto normed = [&](const Raw8<T> &raw, int i, float mean, float rstd, float (&v)[8]) __attribute__((always_inline)) {
+        widen_group<TAIL, P>(raw, a.D, i, t, v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            v[k] = (v[k] - mean) * rstd;
+        if ((i + 1) * P * 8 > a.D) {
+            asm volatile("");  // keeps the branch
+            const int cnt = a.D - (i * P + t) * 8;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                v[k] = (TAIL ? k < cnt : cnt > 0) ? v[k] : 0.0f;
+        }
     };
 
-    const int first = a.chunks > 1 ? blockIdx.x / a.chunks : blockIdx.x * a.each;
-    const int last = a.chunks > 1 ? first + 1 : min(first + a.each, a.groups);
-    const int chunk = a.chunks > 1 ? blockIdx.x - first * a.chunks : 0;
-    for (int grp = first; grp < last; ++grp) {
-        const int64_t base = (int64_t)grp * a.gate_rows;
-        const int64_t m0 = base + (int64_t)a.gate_rows * chunk / a.chunks;
-        const int64_t m1 = base + (int64_t)a.gate_rows * (chunk + 1) / a.chunks;
+    const int step = RPW * U * a.chunks;
+    for (int grp = blockIdx.x / a.chunks; grp < a.groups; grp += gridDim.x / a.chunks) {
+        const int64_t base = (int64_t)grp * a.gate_rows, m1 = base + a.gate_rows;
+        const int64_t m0 = base + (blockIdx.x % a.chunks * RPW + sub) * U;
         if (a.gate)
             load_row<T, P, V>((const T *)a.gate + (int64_t)grp * a.ldg, a.D, t, g);
-        if (AHEAD > 0 && m0 + sub < m1)
-            load(m0 + sub);
-        for (int64_t m = m0 + sub; m < m1; m += RPW) {
-            if constexpr (AHEAD == 0)
-                load(m);
-            const Rows cur = ring;
-            if (AHEAD > 0 && m + RPW < m1)
-                load(m + RPW);
-            float rh[V][8], c[V][8], s1 = 0.0f, s2 = 0.0f;
+        if (AHEAD && m0 < m1)
+            load(m0, m1);
+        for (int64_t m = m0; m < m1; m += step) {
+            if constexpr (!AHEAD)
+                load(m, m1);
+            Row cur[U];
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                float wv[8], dy[8];
-                pin(w[i]);
-                widen_group<TAIL, P>(w[i], a.D, i, t, wv);
-                widen_group<TAIL, P>(cur.r[i], a.D, i, t, rh[i]);
-                widen_group<TAIL, P>(cur.dy[i], a.D, i, t, dy);
-                if ((i + 1) * P * 8 > a.D) {  // past the row's end rh is 0, also where mean rstd is infinite
-                    const int cnt = a.D - (i * P + t) * 8;
+            for (int u = 0; u < U; ++u)
+                cur[u] = ring[u];
+            if (AHEAD && m + step < m1)
+                load(m + step, m1);
+            float s1[U], s2[U], p1[U], p2[U], e[U][V][8];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        rh[i][k] = (TAIL ? k < cnt : cnt > 0) ? rh[i][k] : cur.mean;
-                }
+            for (int u = 0; u < U; ++u) {
+                s1[u] = s2[u] = p1[u] = p2[u] = 0.0f;
+                if (m + u >= m1)
+                    continue;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    rh[i][k] = (rh[i][k] - cur.mean) * cur.rstd;
-                    c[i][k] = dy[k] * wv[k];
-                    s1 += c[i][k];
-                    s2 = __builtin_fmaf(c[i][k], rh[i][k], s2);
-                    sum[0][i][k] = __builtin_fmaf(dy[k], rh[i][k], sum[0][i][k]);
-                    sum[1][i][k] += dy[k];
+                for (int i = 0; i < V; ++i) {
+                    float wv[8], dy[8], rh[8];
+                    as_in_memory(w[i]);
+                    widen_group<TAIL, P>(w[i], a.D, i, t, wv);
+                    widen_group<TAIL, P>(cur[u].dy[i], a.D, i, t, dy);
+                    normed(cur[u].r[i], i, cur[u].mean, cur[u].rstd, rh);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const float c = dy[k] * wv[k];
+                        s1[u] += c;
+                        s2[u] = __builtin_fmaf(c, rh[k], s2[u]);
+                        sum[0][i][k] = __builtin_fmaf(dy[k], rh[k], sum[0][i][k]);
+                        sum[1][i][k] += dy[k];
+                    }
                 }
             }
             means(s1, s2);
-            float p1 = 0.0f, p2 = 0.0f;
-            float hh[V][8];
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int at = (i * P + t) * 8, cnt = a.D - at;
-                const bool whole = (i + 1) * P * 8 <= a.D;
-                auto put = [&](void *p, int64_t ld, const float (&o)[8]) __attribute__((always_inline)) {
-                    T *q = (T *)p + m * ld + at;
-                    if (whole || (!TAIL && cnt > 0))
-                        store_all(q, o);
-                    else if constexpr (TAIL)
-                        store_n(q, cnt, o);
-                };
-                float dr[8], o[8];
-                if (a.dr)
-                    widen_group<TAIL, P>(cur.dr[i], a.D, i, t, dr);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    c[i][k] = cur.rstd * (c[i][k] - s1 - rh[i][k] * s2);  // t
-                    if (a.dr)
-                        c[i][k] += dr[k];
-                    o[k] = a.alpha * c[i][k];
-                }
-                put(a.dx, a.lddx, o);
-                if (!a.dh)
+            for (int u = 0; u < U; ++u) {
+                if (m + u >= m1)
                     continue;
-                if (!whole) {  // what mean(c) leaves past the row's end
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        c[i][k] = (TAIL ? k < cnt : cnt > 0) ? c[i][k] : 0.0f;
-                }
-                float gv[8], pv[8];
-                if (use_h)
-                    widen_group<TAIL, P>(cur.h[i], a.D, i, t, hh[i]);
-                if (a.gate)
-                    widen_group<TAIL, P>(g[i], a.D, i, t, gv);
-                if constexpr (POST) {
-                    pin(pw[i]);
-                    widen_group<TAIL, P>(pw[i], a.D, i, t, pv);
-                    if (!whole) {
+                for (int i = 0; i < V; ++i) {
+                    const int at = (i * P + t) * 8, cnt = a.D - at;
+                    const bool whole = (i + 1) * P * 8 <= a.D;
+                    auto put = [&](void *p, int64_t ld, const float (&o)[8]) __attribute__((always_inline)) {
+                        T *q = (T *)p + (m + u) * ld + at;
+                        if (whole || (!TAIL && cnt > 0))
+                            store_all(q, o);
+                        else if constexpr (TAIL)
+                            store_n(q, cnt, o);
+                    };
+                    float tv[8], o[8], wv[8], rh[8];
+                    as_in_memory(w[i]);
+                    as_in_memory(cur[u].r[i]);
+                    as_in_memory(cur[u].dy[i]);
+                    widen_group<TAIL, P>(w[i], a.D, i, t, wv);
+                    widen_group<TAIL, P>(cur[u].dy[i], a.D, i, t, tv);
+                    normed(cur[u].r[i], i, cur[u].mean, cur[u].rstd, rh);
+                    if (a.dr) {
+                        widen_group<TAIL, P>(cur[u].dr[i], a.D, i, t, o);
+                    } else {
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
-                            hh[i][k] = (TAIL ? k < cnt : cnt > 0) ? hh[i][k] : cur.post_mean;
+                            o[k] = 0.0f;
                     }
-                }
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    float n = 0.0f;
+                    for (int k = 0; k < 8; ++k) {
+                        tv[k] = __builtin_fmaf(tv[k], wv[k], -s1[u]);
+                        tv[k] = __builtin_fmaf(cur[u].rstd, __builtin_fmaf(-rh[k], s2[u], tv[k]), o[k]);
+                        o[k] = a.alpha * tv[k];
+                    }
+                    put(a.dx, a.lddx, o);
+                    if (!a.dh)
+                        continue;
+                    if (!whole) {  // what mean(c) leaves past the row's end
+                        asm volatile("");
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            tv[k] = (TAIL ? k < cnt : cnt > 0) ? tv[k] : 0.0f;
+                    }
+                    float hh[8], gv[8], pv[8];
                     if constexpr (POST) {
-                        hh[i][k] = (hh[i][k] - cur.post_mean) * cur.post_rstd;
-                        n = hh[i][k] * pv[k];
+                        normed(cur[u].h[i], i, cur[u].post_mean, cur[u].post_rstd, hh);
+                        as_in_memory(pw[i]);
+                        widen_group<TAIL, P>(pw[i], a.D, i, t, pv);
                     } else if (use_h) {
-                        n = hh[i][k];
+                        widen_group<TAIL, P>(cur[u].h[i], a.D, i, t, hh);
                     }
                     if (a.gate) {
-                        sum[2][i][k] = __builtin_fmaf(c[i][k], n, sum[2][i][k]);
-                        c[i][k] *= gv[k];  // u
+                        as_in_memory(g[i]);
+                        widen_group<TAIL, P>(g[i], a.D, i, t, gv);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            sum[2][i][k] = __builtin_fmaf(tv[k], POST ? hh[k] * pv[k] : hh[k], sum[2][i][k]);
+                            tv[k] *= gv[k];  // u
+                        }
                     }
                     if constexpr (POST) {
-                        sum[NS - 1][i][k] = __builtin_fmaf(c[i][k], hh[i][k], sum[NS - 1][i][k]);
-                        c[i][k] *= pv[k];  // e
-                        p1 += c[i][k];
-                        p2 = __builtin_fmaf(c[i][k], hh[i][k], p2);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            sum[NS - 1][i][k] = __builtin_fmaf(tv[k], hh[k], sum[NS - 1][i][k]);
+                            e[u][i][k] = tv[k] * pv[k];
+                            p1[u] += e[u][i][k];
+                            p2[u] = __builtin_fmaf(e[u][i][k], hh[k], p2[u]);
+                        }
+                    } else {
+                        put(a.dh, a.lddh, tv);
                     }
                 }
-                if constexpr (!POST)
-                    put(a.dh, a.lddh, c[i]);
             }
             if constexpr (POST) {
                 means(p1, p2);
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const int at = (i * P + t) * 8;
-                    float o[8];
+                for (int u = 0; u < U; ++u) {
+                    if (m + u >= m1)
+                        continue;
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        o[k] = cur.post_rstd * (c[i][k] - p1 - hh[i][k] * p2);
-                    T *q = (T *)a.dh + m * a.lddh + at;
-                    if ((i + 1) * P * 8 <= a.D || (!TAIL && at < a.D))
-                        store_all(q, o);
-                    else if constexpr (TAIL)
-                        store_n(q, a.D - at, o);
+                    for (int i = 0; i < V; ++i) {
+                        const int at = (i * P + t) * 8;
+                        float o[8], hh[8];
+                        as_in_memory(cur[u].h[i]);
+                        normed(cur[u].h[i], i, cur[u].post_mean, cur[u].post_rstd, hh);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            o[k] = cur[u].post_rstd * (e[u][i][k] - p1[u] - hh[k] * p2[u]);
+                        T *q = (T *)a.dh + (m + u) * a.lddh + at;
+                        if ((i + 1) * P * 8 <= a.D || (!TAIL && at < a.D))
+                            store_all(q, o);
+                        else if constexpr (TAIL)
+                            store_n(q, a.D - at, o);
+                    }
                 }
             }
         }
@@ -693,9 +790,6 @@ __global__ __launch_bounds__(256) void residual_norm_columns_kernel(const ResNor
     if (cnt <= 0)
         return;
     const int wg = blockIdx.y;
-    const int first = a.chunks > 1 ? wg / a.chunks : wg * a.each;
-    const int last = a.chunks > 1 ? first + 1 : min(first + a.each, a.groups);
-    const int chunk = a.chunks > 1 ? wg - first * a.chunks : 0;
     float w[8], pw[8], sum[4][8] = {};
 #pragma unroll
     for (int k = 0; k < 8; ++k)
@@ -704,17 +798,15 @@ __global__ __launch_bounds__(256) void residual_norm_columns_kernel(const ResNor
         load_n((const T *)a.weight + c, cnt, w);
     if constexpr (POST)
         load_n((const T *)a.post_weight + c, cnt, pw);
-    for (int grp = first; grp < last; ++grp) {
-        const int64_t base = (int64_t)grp * a.gate_rows;
-        const int64_t m0 = base + (int64_t)a.gate_rows * chunk / a.chunks;
-        const int64_t m1 = base + (int64_t)a.gate_rows * (chunk + 1) / a.chunks;
+    for (int grp = wg / a.chunks; grp < a.groups; grp += gridDim.y / a.chunks) {
+        const int64_t base = (int64_t)grp * a.gate_rows, m1 = base + a.gate_rows;
         float g[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k)
             g[k] = 1.0f;
         if (a.gate)
             load_n((const T *)a.gate + (int64_t)grp * a.ldg + c, cnt, g);
-        for (int64_t m = m0; m < m1; ++m) {
+        for (int64_t m = base + wg % a.chunks; m < m1; m += a.chunks) {
             const float mean = RMS ? 0.0f : a.mean[m], rstd = a.rstd[m];
             const float2 s = a.row_sums[m];
             float r[8], dy[8], dr[8] = {}, h[8] = {};
@@ -752,38 +844,6 @@ __global__ __launch_bounds__(256) void residual_norm_columns_kernel(const ResNor
 #pragma unroll
     for (int s = 0; s < 4; ++s)
         store_n(p + s * a.part_ld, cnt, sum[s]);
-}
-
-// The sums over workgroups: blockIdx.y 0 dweight, 1 dbias, 2 dpost_weight, 3 + g row g of dgate.
-struct ResNormSumArgs {
-    const float *part;
-    int64_t part_ld;
-    int wgs, chunks, D, dt;
-    void *out[3], *dgate;             // null: not wanted
-    int64_t lddg;
-};
-
-__global__ __launch_bounds__(32 * kSumGroups) void residual_norm_sums_kernel(const ResNormSumArgs a)
-{
-    __shared__ float red[kSumGroups][33];
-    const int job = blockIdx.y;
-    ColSumArgs c;
-    c.ld = 4 * a.part_ld;
-    c.cols = c.split = c.valid = a.D;
-    c.out1 = nullptr;
-    c.dt = a.dt;
-    if (job < 3) {
-        c.part = a.part + job * a.part_ld;
-        c.rows = a.wgs;
-        c.out0 = a.out[job];
-    } else {
-        const int g = job - 3;
-        c.part = a.part + ((int64_t)g * a.chunks * 4 + 3) * a.part_ld;
-        c.rows = a.chunks;
-        c.out0 = (char *)a.dgate + g * a.lddg * (a.dt == DENSE_FP32 ? 4 : 2);
-    }
-    if (c.out0)
-        column_sums<32>(c, blockIdx.x, red);
 }
 
 }  // namespace dense
