@@ -425,6 +425,25 @@ __device__ __forceinline__ float wave_max(float v)
     return wave_reduce(v, [](float a, float b) { return fmaxf(a, b); });
 }
 
+// Two numbers a lane become one: lanes of the lower half of a wave then hold f of
+// a's halves, those of the upper half f of b's.
+template <typename F>
+__device__ __forceinline__ float fold_halves(float a, float b, F f)
+{
+    const auto s = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(unsigned, a), __builtin_bit_cast(unsigned, b), false, false);
+    const unsigned x = s[0], y = s[1];  // a bit_cast of an element takes the first one
+    return f(__builtin_bit_cast(float, x), __builtin_bit_cast(float, y));
+}
+
+// The same of the rows of sixteen lanes: rows 0 and 2 hold f of a's pairs, 1 and 3 of b's.
+template <typename F>
+__device__ __forceinline__ float fold_rows(float a, float b, F f)
+{
+    const auto s = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(unsigned, a), __builtin_bit_cast(unsigned, b), false, false);
+    const unsigned x = s[0], y = s[1];
+    return f(__builtin_bit_cast(float, x), __builtin_bit_cast(float, y));
+}
+
 // Workgroups are dealt round-robin to the 8 XCDs; each XCD gets one contiguous
 // run of tiles.
 __device__ __forceinline__ int xcd_tile(int bid, int tiles)

@@ -51,7 +51,7 @@ conv_i8_status_t analyze(const dense_quantize_t *args, QuantPlan *p)
     if (d.x.col_stride != 1)
         return CONV_I8_ERR_STRIDES;
     const bool rows = !qt && !p->tiles;
-    if (!launch_fits(rows ? ceil_div(M, 16) * ceil_div(K, 512) : ceil_div(M, kBlock) * ceil_div(K, kBlock), 256))
+    if (!launch_fits(rows ? ceil_div(M, 16) * ceil_div(K, 512) : ceil_div(M, kBlock) * ceil_div(K, kBlock), kTileThreads))
         return CONV_I8_ERR_UNSUPPORTED;
     return CONV_I8_OK;
 }
@@ -90,7 +90,7 @@ void run_quantize(const QuantPlan &p, hipStream_t s)
         if (rows)
             hipLaunchKernelGGL(quantize_rows_kernel<T>, grid, block, 0, s, a);
         else
-            hipLaunchKernelGGL((quantize_tile_kernel<T, DENSE_ACT_NONE>), grid, block, 0, s, a);
+            hipLaunchKernelGGL((quantize_tile_kernel<T, DENSE_ACT_NONE>), grid, dim3(kTileThreads), 0, s, a);
     };
     if (d.x.dtype == DENSE_BF16)
         launch(Type<bf16>{});
@@ -458,7 +458,7 @@ conv_i8_status_t analyze(const dense_linear_fp8_backward_t *args, BackwardF8Plan
         p->sum_ld = round_up(N, 32);
         p->sum_bytes = round_up(ceil_div(M, kBlock) * p->sum_ld * 4, kWsAlign);
     }
-    if (!launch_fits(ceil_div(M, kBlock) * ceil_div(N, kBlock), 256) || !launch_fits(pack_wgs(p->wb) + pack_wgs(p->xb), 256))
+    if (!launch_fits(ceil_div(M, kBlock) * ceil_div(N, kBlock), kTileThreads) || !launch_fits(pack_wgs(p->wb) + pack_wgs(p->xb), 256))
         return CONV_I8_ERR_UNSUPPORTED;
     p->ws_bytes = p->g_bytes + p->gs_bytes + p->gt_bytes + p->gts_bytes + p->sum_bytes + p->wb.pack_bytes + p->xb.pack_bytes +
                   p->part_bytes;
@@ -469,11 +469,11 @@ template <typename T>
 void launch_pass(int64_t act, dim3 grid, const QuantArgs &a, hipStream_t s)
 {
     switch (act) {
-    case DENSE_ACT_RELU: hipLaunchKernelGGL((quantize_tile_kernel<T, DENSE_ACT_RELU>), grid, dim3(256), 0, s, a); break;
-    case DENSE_ACT_GELU: hipLaunchKernelGGL((quantize_tile_kernel<T, DENSE_ACT_GELU>), grid, dim3(256), 0, s, a); break;
-    case DENSE_ACT_GELU_TANH: hipLaunchKernelGGL((quantize_tile_kernel<T, DENSE_ACT_GELU_TANH>), grid, dim3(256), 0, s, a); break;
-    case DENSE_ACT_SILU: hipLaunchKernelGGL((quantize_tile_kernel<T, DENSE_ACT_SILU>), grid, dim3(256), 0, s, a); break;
-    default: hipLaunchKernelGGL((quantize_tile_kernel<T, DENSE_ACT_NONE>), grid, dim3(256), 0, s, a); break;
+    case DENSE_ACT_RELU: hipLaunchKernelGGL((quantize_tile_kernel<T, DENSE_ACT_RELU>), grid, dim3(kTileThreads), 0, s, a); break;
+    case DENSE_ACT_GELU: hipLaunchKernelGGL((quantize_tile_kernel<T, DENSE_ACT_GELU>), grid, dim3(kTileThreads), 0, s, a); break;
+    case DENSE_ACT_GELU_TANH: hipLaunchKernelGGL((quantize_tile_kernel<T, DENSE_ACT_GELU_TANH>), grid, dim3(kTileThreads), 0, s, a); break;
+    case DENSE_ACT_SILU: hipLaunchKernelGGL((quantize_tile_kernel<T, DENSE_ACT_SILU>), grid, dim3(kTileThreads), 0, s, a); break;
+    default: hipLaunchKernelGGL((quantize_tile_kernel<T, DENSE_ACT_NONE>), grid, dim3(kTileThreads), 0, s, a); break;
     }
 }
 

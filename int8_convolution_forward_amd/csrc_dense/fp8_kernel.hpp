@@ -28,28 +28,19 @@ __device__ __forceinline__ float inverse_scale(int byte) { return __builtin_bit_
 // The magnitude that counts for a scale: 0 for what is not finite
 __device__ __forceinline__ float finite_size(float v) { return fabsf(v) < INFINITY ? fabsf(v) : 0.0f; }
 
-// Eight values times `inv`, rounded half to even; what is not finite becomes NaN
+// Four values times `inv`, rounded half to even; what is not finite becomes NaN
+__device__ __forceinline__ int encode4(float v0, float v1, float v2, float v3, float inv, bool e5)
+{
+    auto scaled = [&](float v) { return fabsf(v) < INFINITY ? v * inv : __builtin_nanf(""); };
+    const float s0 = scaled(v0), s1 = scaled(v1), s2 = scaled(v2), s3 = scaled(v3);
+    return e5 ? __builtin_amdgcn_cvt_pk_bf8_f32(s2, s3, __builtin_amdgcn_cvt_pk_bf8_f32(s0, s1, 0, false), true)
+              : __builtin_amdgcn_cvt_pk_fp8_f32(s2, s3, __builtin_amdgcn_cvt_pk_fp8_f32(s0, s1, 0, false), true);
+}
+
 __device__ __forceinline__ Pack<uint8_t, 8> encode8(const float (&v)[8], float inv, bool e5)
 {
-    float s[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-        s[k] = fabsf(v[k]) < INFINITY ? v[k] * inv : __builtin_nanf("");
     typedef int v2i __attribute__((ext_vector_type(2)));
-    v2i w = {0, 0};
-    if (e5) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            w[i] = __builtin_amdgcn_cvt_pk_bf8_f32(s[4 * i], s[4 * i + 1], w[i], false);
-            w[i] = __builtin_amdgcn_cvt_pk_bf8_f32(s[4 * i + 2], s[4 * i + 3], w[i], true);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            w[i] = __builtin_amdgcn_cvt_pk_fp8_f32(s[4 * i], s[4 * i + 1], w[i], false);
-            w[i] = __builtin_amdgcn_cvt_pk_fp8_f32(s[4 * i + 2], s[4 * i + 3], w[i], true);
-        }
-    }
+    const v2i w = {encode4(v[0], v[1], v[2], v[3], inv, e5), encode4(v[4], v[5], v[6], v[7], inv, e5)};
     return __builtin_bit_cast(Pack<uint8_t, 8>, w);
 }
 
@@ -136,83 +127,104 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(const QuantArgs a)
     }
 }
 
-// A 128 x 128 tile a workgroup: a thread holds eight rows of eight columns, from
+// A 128 x 128 tile a workgroup: a thread holds four rows of eight columns, from
 // which it has the largest magnitudes of its rows (by lane permutations), of its
 // columns and of the tile (through LDS).  The transposed values turn as bytes in LDS.
+constexpr int kTileThreads = 512;
+
 template <typename T, int ACT>
-__global__ __launch_bounds__(256) void quantize_tile_kernel(const QuantArgs a)
+__global__ __launch_bounds__(kTileThreads) void quantize_tile_kernel(const QuantArgs a)
 {
-    constexpr int PITCH = 136;
-    __shared__ __attribute__((aligned(16))) float cols[16][128];
+    constexpr int R = 4, W = kTileThreads / 64, PITCH = 136;
+    __shared__ __attribute__((aligned(16))) float cols[W][128];
     __shared__ __attribute__((aligned(16))) float inv[128];
     __shared__ __attribute__((aligned(16))) uint8_t turned[128 * PITCH];
-    __shared__ float wave_top[4];
+    __shared__ float wave_top[W];
     const int tr = blockIdx.x / a.strips, tc = blockIdx.x - tr * a.strips;
-    const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4;
-    const int m0 = tr * 128 + rg * 8, c = tc * 128 + cg * 8;
-    float v[8][8];
-    auto read = [&](const void *p, int64_t ld, float (&w)[8][8]) __attribute__((always_inline)) {
+    const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4, wave = threadIdx.x >> 6, q = rg & 3;
+    const int m0 = tr * 128 + rg * R, c = tc * 128 + cg * 8;
+    float v[R][8];
+    {
+        Raw8<T> x[R], z[R];
         if (a.K >= 8) {
-            Raw8<T> r[8];
 #pragma unroll
-            for (int p8 = 0; p8 < 8; ++p8)
-                r[p8] = load_raw((const T *)p + (int64_t)min(m0 + p8, a.M - 1) * ld, c, a.K);
-            if (tc * 128 + 128 <= a.K) {
-#pragma unroll
-                for (int p8 = 0; p8 < 8; ++p8)
-                    widen(r[p8], w[p8]);
-            } else {
-#pragma unroll
-                for (int p8 = 0; p8 < 8; ++p8)
-                    widen_part<true>(r[p8], c, a.K, w[p8]);
+            for (int p = 0; p < R; ++p) {
+                const int64_t m = min(m0 + p, a.M - 1);
+                x[p] = load_raw((const T *)a.x + m * a.ldx, c, a.K);
+                if constexpr (ACT != DENSE_ACT_NONE)
+                    z[p] = load_raw((const T *)a.z + m * a.ldz, c, a.K);
             }
-        } else {
-#pragma unroll
-            for (int p8 = 0; p8 < 8; ++p8)
-                load_n((const T *)p + (int64_t)min(m0 + p8, a.M - 1) * ld + c, a.K - c, w[p8]);
         }
-    };
-    read(a.x, a.ldx, v);
-    if constexpr (ACT != DENSE_ACT_NONE) {
-        float z[8][8];
-        read(a.z, a.ldz, z);
 #pragma unroll
-        for (int p = 0; p < 8; ++p)
+        for (int p = 0; p < R; ++p) {
+            const int64_t m = min(m0 + p, a.M - 1);
+            float s[8];
+            if (a.K < 8) {
+                load_n((const T *)a.x + m * a.ldx + c, a.K - c, v[p]);
+                if constexpr (ACT != DENSE_ACT_NONE)
+                    load_n((const T *)a.z + m * a.ldz + c, a.K - c, s);
+            } else if (tc * 128 + 128 <= a.K) {
+                widen(x[p], v[p]);
+                if constexpr (ACT != DENSE_ACT_NONE)
+                    widen(z[p], s);
+            } else {
+                widen_part<true>(x[p], c, a.K, v[p]);
+                if constexpr (ACT != DENSE_ACT_NONE)
+                    widen_part<true>(z[p], c, a.K, s);
+            }
+            if constexpr (ACT != DENSE_ACT_NONE) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                v[p][k] *= act_slope<ACT>(z[p][k]);
+                for (int k = 0; k < 8; ++k)
+                    v[p][k] *= act_slope<ACT>(s[k]);
+            }
+        }
     }
     if (tr * 128 + 128 > a.M) {
 #pragma unroll
-        for (int p = 0; p < 8; ++p)
+        for (int p = 0; p < R; ++p)
 #pragma unroll
             for (int k = 0; k < 8; ++k)
                 v[p][k] = m0 + p < a.M ? v[p][k] : 0.0f;
     }
 
+    // f over the rows of each column, of a wave's rows by folding two columns into one register and four
+    // into one (lane 16 q + cg then holds columns 8 cg + 2 q' and the next, q' = q with its bits as they
+    // fold), then of the waves through LDS: thread i < 128 has column i's
+    auto columns = [&](float (&s)[8], auto f) __attribute__((always_inline)) {
+        float h[4], w[2];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            h[k] = fold_halves(s[k], s[k + 4], f);
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            w[k] = fold_rows(h[k], h[k + 2], f);
+        store_all(&cols[wave][cg * 8 + (q >> 1) * 4 + (q & 1) * 2], w);
+        __syncthreads();
+        float t = 0.0f;
+        if (threadIdx.x < 128) {
+            t = cols[0][threadIdx.x];
+#pragma unroll
+            for (int i = 1; i < W; ++i)
+                t = f(t, cols[i][threadIdx.x]);
+        }
+        return t;
+    };
     if (a.colsum) {
         float s[8] = {};
 #pragma unroll
-        for (int p = 0; p < 8; ++p)
+        for (int p = 0; p < R; ++p)
 #pragma unroll
             for (int k = 0; k < 8; ++k)
                 s[k] += v[p][k];
-        store_all(&cols[rg][cg * 8], s);
-        __syncthreads();
-        if (threadIdx.x < 128) {
-            float t = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                t += cols[i][threadIdx.x];
-            if (tc * 128 + (int)threadIdx.x < a.K)
-                a.colsum[tr * a.sum_ld + tc * 128 + threadIdx.x] = t;
-        }
+        const float t = columns(s, [](float x, float y) { return x + y; });
+        if (threadIdx.x < 128 && tc * 128 + (int)threadIdx.x < a.K)
+            a.colsum[tr * a.sum_ld + tc * 128 + threadIdx.x] = t;
         __syncthreads();
     }
 
-    float row_top[8], col_top[8] = {}, all = 0.0f;
+    float row_top[R], col_top[8] = {}, all = 0.0f;
 #pragma unroll
-    for (int p = 0; p < 8; ++p) {
+    for (int p = 0; p < R; ++p) {
         row_top[p] = 0.0f;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
@@ -223,21 +235,22 @@ __global__ __launch_bounds__(256) void quantize_tile_kernel(const QuantArgs a)
         all = fmaxf(all, row_top[p]);
         row_top[p] = block_max(row_top[p]);
     }
+    int tile_byte = 0;
     if (a.tiles || a.tiles_t) {
         all = wave_max(all);
         if ((threadIdx.x & 63) == 0)
-            wave_top[threadIdx.x >> 6] = all;
+            wave_top[wave] = all;
+        __syncthreads();
+        all = wave_top[0];
+#pragma unroll
+        for (int i = 1; i < W; ++i)
+            all = fmaxf(all, wave_top[i]);
+        tile_byte = scale_byte(all, a.e5);
     }
-    if (a.qt && !a.tiles_t)
-        store_all(&cols[rg][cg * 8], col_top);
-    __syncthreads();
-    if (a.tiles || a.tiles_t)
-        all = fmaxf(fmaxf(wave_top[0], wave_top[1]), fmaxf(wave_top[2], wave_top[3]));
-    const int tile_byte = scale_byte(all, a.e5);
 
     if (a.q) {
 #pragma unroll
-        for (int p = 0; p < 8; ++p) {
+        for (int p = 0; p < R; ++p) {
             const int byte = a.tiles ? tile_byte : scale_byte(row_top[p], a.e5);
             if (m0 + p < a.M) {
                 const int64_t m = m0 + p;
@@ -251,40 +264,31 @@ __global__ __launch_bounds__(256) void quantize_tile_kernel(const QuantArgs a)
     }
     if (!a.qt)
         return;
-    if (!a.tiles_t && threadIdx.x < 128) {
-        float t = cols[0][threadIdx.x];
-#pragma unroll
-        for (int i = 1; i < 16; ++i)
-            t = fmaxf(t, cols[i][threadIdx.x]);
-        const int byte = scale_byte(t, a.e5);
-        inv[threadIdx.x] = inverse_scale(byte);
-        if (tc * 128 + (int)threadIdx.x < a.K)
-            a.scale_t[(int64_t)(tc * 128 + threadIdx.x) * a.ldst + tr] = (uint8_t)byte;
-    } else if (a.tiles_t && threadIdx.x == 0) {
-        a.scale_t[tc * a.ldst + tr] = (uint8_t)tile_byte;
-    }
-    __syncthreads();
     float by[8];
     if (a.tiles_t) {
+        if (threadIdx.x == 0)
+            a.scale_t[tc * a.ldst + tr] = (uint8_t)tile_byte;
 #pragma unroll
         for (int k = 0; k < 8; ++k)
             by[k] = inverse_scale(tile_byte);
     } else {
+        const float t = columns(col_top, [](float x, float y) { return fmaxf(x, y); });
+        if (threadIdx.x < 128) {
+            const int byte = scale_byte(t, a.e5);
+            inv[threadIdx.x] = inverse_scale(byte);
+            if (tc * 128 + (int)threadIdx.x < a.K)
+                a.scale_t[(int64_t)(tc * 128 + threadIdx.x) * a.ldst + tr] = (uint8_t)byte;
+        }
+        __syncthreads();
         load_all(&inv[cg * 8], by);
     }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        float t[8];
-#pragma unroll
-        for (int p = 0; p < 8; ++p)
-            t[p] = v[p][k];
-        typedef int v2i __attribute__((ext_vector_type(2)));
-        *(v2i *)&turned[(cg * 8 + k) * PITCH + rg * 8] = __builtin_bit_cast(v2i, encode8(t, by[k], a.e5));
-    }
+    for (int k = 0; k < 8; ++k)
+        *(int *)&turned[(cg * 8 + k) * PITCH + rg * R] = encode4(v[0][k], v[1][k], v[2][k], v[3][k], by[k], a.e5);
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int row = i * 16 + rg, n = tc * 128 + row, m = tr * 128 + cg * 8;
+    for (int i = 0; i < 4; ++i) {
+        const int row = i * 32 + rg, n = tc * 128 + row, m = tr * 128 + cg * 8;
         typedef int v2i __attribute__((ext_vector_type(2)));
         const v2i w = *(const v2i *)&turned[row * PITCH + cg * 8];
         if (n < a.K)

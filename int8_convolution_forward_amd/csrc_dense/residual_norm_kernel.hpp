@@ -30,23 +30,6 @@ struct ResNormArgs {
     float *mean, *rstd, *post_mean, *post_rstd;  // null: not written
 };
 
-// Two numbers a lane become one: lanes of the lower half then hold the sum of a's
-// halves, those of the upper half that of b's.
-__device__ __forceinline__ float fold_halves(float a, float b)
-{
-    const auto s = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(unsigned, a), __builtin_bit_cast(unsigned, b), false, false);
-    const unsigned x = s[0], y = s[1];
-    return __builtin_bit_cast(float, x) + __builtin_bit_cast(float, y);
-}
-
-// The same of the odd and even rows of sixteen lanes: rows 0 and 2 hold sums of a's, 1 and 3 of b's.
-__device__ __forceinline__ float fold_rows(float a, float b)
-{
-    const auto s = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(unsigned, a), __builtin_bit_cast(unsigned, b), false, false);
-    const unsigned x = s[0], y = s[1];
-    return __builtin_bit_cast(float, x) + __builtin_bit_cast(float, y);
-}
-
 template <int CTRL>
 __device__ __forceinline__ float add_dpp(float v)
 {
@@ -460,8 +443,9 @@ __global__ __launch_bounds__(norm_threads(P), OCC) void residual_norm_backward_k
     // into one register and four of those into one, so that four sums cost little more than one.
     auto means = [&](float (&s1)[U], float (&s2)[U]) __attribute__((always_inline)) {
         static_assert(U == 1 || U == 2, "rows at a time");
-        float v = fold_halves(s1[0], s2[0]);
-        v = row16_sum(U == 2 ? fold_rows(v, fold_halves(s1[U - 1], s2[U - 1])) : v);
+        auto add = [](float x, float y) { return x + y; };
+        float v = fold_halves(s1[0], s2[0], add);
+        v = row16_sum(U == 2 ? fold_rows(v, fold_halves(s1[U - 1], s2[U - 1], add), add) : v);
         // U 1: rows of lanes 0, 1: s1's parts, 2, 3: s2's; U 2: s1 of both rows, then s2
         float r[4];
         if constexpr (P > 64) {
