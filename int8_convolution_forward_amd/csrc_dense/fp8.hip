@@ -84,13 +84,16 @@ void run_quantize(const QuantPlan &p, hipStream_t s)
     }
     const bool rows = !a.qt && !a.tiles;
     a.strips = (int)ceil_div(a.K, rows ? 512 : kBlock);
-    const dim3 grid((unsigned)(a.strips * ceil_div(a.M, rows ? 16 : kBlock))), block(256);
+    a.blocks = (int)(a.strips * ceil_div(a.M, rows ? 16 : kBlock));
+    PackArgs none;
+    memset(&none, 0, sizeof none);
+    const dim3 grid((unsigned)a.blocks), block(256);
     auto launch = [&](auto t) {
         typedef typename decltype(t)::type T;
         if (rows)
             hipLaunchKernelGGL(quantize_rows_kernel<T>, grid, block, 0, s, a);
         else
-            hipLaunchKernelGGL((quantize_tile_kernel<T, DENSE_ACT_NONE>), grid, dim3(kTileThreads), 0, s, a);
+            hipLaunchKernelGGL((quantize_tile_kernel<T, DENSE_ACT_NONE>), grid, dim3(kTileThreads), 0, s, a, none);
     };
     if (d.x.dtype == DENSE_BF16)
         launch(Type<bf16>{});
@@ -358,6 +361,13 @@ struct BackwardF8Plan {
     int64_t g_bytes = 0, gs_bytes = 0, gt_bytes = 0, gts_bytes = 0, sum_bytes = 0, sum_ld = 0;
     GemmPlan dx, dw;
     int64_t part_bytes = 0, ws_bytes = 0;
+
+    // Both products go out in one launch.
+    bool pair() const
+    {
+        return want_dx && want_dw && dx.tile == kPairTile && dw.tile == kPairTile && dx.splits == 1 && dw.splits == 1 &&
+               launch_fits((int64_t)dx.tiles_m * dx.tiles_n + (int64_t)dw.tiles_m * dw.tiles_n + ceil_div(N, 8), 256);
+    }
 };
 
 conv_i8_status_t analyze(const dense_linear_fp8_backward_t *args, BackwardF8Plan *p)
@@ -437,10 +447,11 @@ conv_i8_status_t analyze(const dense_linear_fp8_backward_t *args, BackwardF8Plan
     Forced forced;
     DENSE_TRY(forced_tile(&forced));
     p->wb.es = p->xb.es = 1;  // both are copied by one launch, also where one is absent
+    double apart = 0.0;
     if (p->want_dx) {
         DENSE_TRY(quantised(M, N, &p->ga, &p->g_bytes, &p->gs_bytes));
         DENSE_TRY(plan_bytes(d.wt, &p->wb));
-        plan_gemm(M, p->K, N, 1, forced, &p->dx);
+        apart += plan_gemm(M, p->K, N, 1, forced, &p->dx);
         if (!grid_fits(p->dx, M))
             return CONV_I8_ERR_UNSUPPORTED;
         p->part_bytes = p->dx.part_bytes;
@@ -448,7 +459,13 @@ conv_i8_status_t analyze(const dense_linear_fp8_backward_t *args, BackwardF8Plan
     if (p->want_dw) {
         DENSE_TRY(quantised(N, M, &p->gt, &p->gt_bytes, &p->gts_bytes));
         DENSE_TRY(plan_bytes(d.xt, &p->xb));
-        plan_gemm(N, p->K, M, 1, forced, &p->dw);
+        apart += plan_gemm(N, p->K, M, 1, forced, &p->dw);
+        // apart: a launch more, and the bias gradient's
+        if (p->want_dx && !forced.on && pair_cost(M, N, p->K, 1) < apart + 4.0) {
+            set_plan(M, p->K, N, 1, kPairTile, 1, &p->dx);
+            set_plan(N, p->K, M, 1, kPairTile, 1, &p->dw);
+            p->part_bytes = 0;
+        }
         if (!grid_fits(p->dw, N))
             return CONV_I8_ERR_UNSUPPORTED;
         if (p->dw.part_bytes > p->part_bytes)
@@ -458,7 +475,7 @@ conv_i8_status_t analyze(const dense_linear_fp8_backward_t *args, BackwardF8Plan
         p->sum_ld = round_up(N, 32);
         p->sum_bytes = round_up(ceil_div(M, kBlock) * p->sum_ld * 4, kWsAlign);
     }
-    if (!launch_fits(ceil_div(M, kBlock) * ceil_div(N, kBlock), kTileThreads) || !launch_fits(pack_wgs(p->wb) + pack_wgs(p->xb), 256))
+    if (!launch_fits(ceil_div(M, kBlock) * ceil_div(N, kBlock) + pack_wgs(p->wb) + pack_wgs(p->xb), kTileThreads))
         return CONV_I8_ERR_UNSUPPORTED;
     p->ws_bytes = p->g_bytes + p->gs_bytes + p->gt_bytes + p->gts_bytes + p->sum_bytes + p->wb.pack_bytes + p->xb.pack_bytes +
                   p->part_bytes;
@@ -466,14 +483,14 @@ conv_i8_status_t analyze(const dense_linear_fp8_backward_t *args, BackwardF8Plan
 }
 
 template <typename T>
-void launch_pass(int64_t act, dim3 grid, const QuantArgs &a, hipStream_t s)
+void launch_pass(int64_t act, dim3 grid, const QuantArgs &a, const PackArgs &pack, hipStream_t s)
 {
     switch (act) {
-    case DENSE_ACT_RELU: hipLaunchKernelGGL((quantize_tile_kernel<T, DENSE_ACT_RELU>), grid, dim3(kTileThreads), 0, s, a); break;
-    case DENSE_ACT_GELU: hipLaunchKernelGGL((quantize_tile_kernel<T, DENSE_ACT_GELU>), grid, dim3(kTileThreads), 0, s, a); break;
-    case DENSE_ACT_GELU_TANH: hipLaunchKernelGGL((quantize_tile_kernel<T, DENSE_ACT_GELU_TANH>), grid, dim3(kTileThreads), 0, s, a); break;
-    case DENSE_ACT_SILU: hipLaunchKernelGGL((quantize_tile_kernel<T, DENSE_ACT_SILU>), grid, dim3(kTileThreads), 0, s, a); break;
-    default: hipLaunchKernelGGL((quantize_tile_kernel<T, DENSE_ACT_NONE>), grid, dim3(kTileThreads), 0, s, a); break;
+    case DENSE_ACT_RELU: hipLaunchKernelGGL((quantize_tile_kernel<T, DENSE_ACT_RELU>), grid, dim3(kTileThreads), 0, s, a, pack); break;
+    case DENSE_ACT_GELU: hipLaunchKernelGGL((quantize_tile_kernel<T, DENSE_ACT_GELU>), grid, dim3(kTileThreads), 0, s, a, pack); break;
+    case DENSE_ACT_GELU_TANH: hipLaunchKernelGGL((quantize_tile_kernel<T, DENSE_ACT_GELU_TANH>), grid, dim3(kTileThreads), 0, s, a, pack); break;
+    case DENSE_ACT_SILU: hipLaunchKernelGGL((quantize_tile_kernel<T, DENSE_ACT_SILU>), grid, dim3(kTileThreads), 0, s, a, pack); break;
+    default: hipLaunchKernelGGL((quantize_tile_kernel<T, DENSE_ACT_NONE>), grid, dim3(kTileThreads), 0, s, a, pack); break;
     }
 }
 
@@ -509,48 +526,58 @@ conv_i8_status_t run_backward(const BackwardF8Plan &p, void *ws, hipStream_t str
         }
         a.colsum = p.want_db ? (float *)sums : nullptr;
         a.sum_ld = p.sum_ld;
-        const dim3 grid((unsigned)(a.strips * ceil_div(p.M, kBlock)));
+        a.blocks = (int)(a.strips * ceil_div(p.M, kBlock));
+        PackArgs pack;
+        const dim3 grid((unsigned)(a.blocks + pack_jobs(p.wb, pw, p.xb, px, &pack, kTileThreads)));
         if (d.dy.dtype == DENSE_BF16)
-            launch_pass<bf16>(d.activation, grid, a, stream);
+            launch_pass<bf16>(d.activation, grid, a, pack, stream);
         else
-            launch_pass<f16>(d.activation, grid, a, stream);
+            launch_pass<f16>(d.activation, grid, a, pack, stream);
         if (hipGetLastError() != hipSuccess)
             return CONV_I8_ERR_HIP;
+    } else if (!launch_pack(p.wb, pw, p.xb, px, stream)) {
+        return CONV_I8_ERR_HIP;
     }
+    ColSumArgs c;
+    memset(&c, 0, sizeof c);
     if (p.want_db) {
-        ColSumArgs c;
-        memset(&c, 0, sizeof c);
         c.part = (const float *)sums;
         c.ld = p.sum_ld;
         c.rows = (int)ceil_div(p.M, kBlock);  // none: zeros
         c.cols = c.split = c.valid = p.N;
         c.out0 = const_cast<void *>(d.dbias.ptr);
         c.dt = (int)d.dy.dtype;
-        hipLaunchKernelGGL(colsum_kernel<>, colsum_grid(p.N), dim3(32 * kSumGroups), 0, stream, c);
-        if (hipGetLastError() != hipSuccess)
-            return CONV_I8_ERR_HIP;
     }
-    if (!launch_pack(p.wb, pw, p.xb, px, stream))
-        return CONV_I8_ERR_HIP;
     Epilogue e;
     memset(&e, 0, sizeof e);
     e.out_dt = (int)d.dy.dtype;
+    GemmArgs dx, dw;
     if (p.want_dx) {
         e.out = const_cast<void *>(d.dx.ptr);
         e.ldo = d.dx.row_stride;
-        GemmArgs g = gemm_args(p.ga, gq, p.wb, p.wb.packed ? pw : p.wb.src, p.M, p.K, p.N, p.dx, part, e);
-        set_scales(&g, gs, ceil_div(p.N, kBlock), d.wt_scale.ptr, d.wt_scale.row_stride, p.wt_tiles, p.N);
-        if (!run_gemm(d.g_dtype, p.ga, p.wb, p.dx, g, stream))
-            return CONV_I8_ERR_HIP;
+        dx = gemm_args(p.ga, gq, p.wb, p.wb.packed ? pw : p.wb.src, p.M, p.K, p.N, p.dx, part, e);
+        set_scales(&dx, gs, ceil_div(p.N, kBlock), d.wt_scale.ptr, d.wt_scale.row_stride, p.wt_tiles, p.N);
     }
     if (p.want_dw) {
         e.out = const_cast<void *>(d.dw.ptr);
         e.ldo = d.dw.row_stride;
-        GemmArgs g = gemm_args(p.gt, gtq, p.xb, p.xb.packed ? px : p.xb.src, p.N, p.K, p.M, p.dw, part, e);
-        set_scales(&g, gts, ceil_div(p.M, kBlock), d.xt_scale.ptr, d.xt_scale.row_stride, p.xt_tiles, p.M);
-        if (!run_gemm(d.g_dtype, p.gt, p.xb, p.dw, g, stream))
+        dw = gemm_args(p.gt, gtq, p.xb, p.xb.packed ? px : p.xb.src, p.N, p.K, p.M, p.dw, part, e);
+        set_scales(&dw, gts, ceil_div(p.M, kBlock), d.xt_scale.ptr, d.xt_scale.row_stride, p.xt_tiles, p.M);
+    }
+    if (p.pair()) {
+        const PairArgs both = {dx, dw, c};
+        const bool ok = d.g_dtype == DENSE_E4M3 ? launch_gemm_pair_f8e4(both, stream) : launch_gemm_pair_f8e5(both, stream);
+        return ok ? CONV_I8_OK : CONV_I8_ERR_HIP;
+    }
+    if (p.want_db) {
+        hipLaunchKernelGGL(colsum_kernel<>, colsum_grid(p.N), dim3(32 * kSumGroups), 0, stream, c);
+        if (hipGetLastError() != hipSuccess)
             return CONV_I8_ERR_HIP;
     }
+    if (p.want_dx && !run_gemm(d.g_dtype, p.ga, p.wb, p.dx, dx, stream))
+        return CONV_I8_ERR_HIP;
+    if (p.want_dw && !run_gemm(d.g_dtype, p.gt, p.xb, p.dw, dw, stream))
+        return CONV_I8_ERR_HIP;
     return CONV_I8_OK;
 }
 
@@ -659,7 +686,7 @@ conv_i8_status_t dense_linear_fp8_backward_plan(const dense_linear_fp8_backward_
         describe(p.dx, p.ga, p.wb, dx, sizeof dx);
     if (p.want_dw)
         describe(p.dw, p.gt, p.xb, dw, sizeof dw);
-    snprintf(text, sizeof text, "dx: %s; dw: %s", dx, dw);
+    snprintf(text, sizeof text, "launches=%s dx: %s; dw: %s", p.pair() ? "paired" : "apart", dx, dw);
     return answer(text, buf, len);
 }
 

@@ -10,7 +10,7 @@
 // All are bound by HBM.
 #pragma once
 
-#include "dense_common.hpp"
+#include "rows_kernel.hpp"
 
 namespace dense {
 
@@ -70,7 +70,7 @@ struct QuantArgs {
     const void *x, *z;        // z: where the values are x act'(z)
     int64_t ldx, ldz;
     int M, K;
-    int strips;               // workgroups along a row
+    int strips, blocks;       // workgroups along a row, and of all rows
     bool e5, tiles, tiles_t;
     uint8_t *q, *scale;       // null: not written
     int64_t ldq, lds;
@@ -132,9 +132,16 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(const QuantArgs a)
 // columns and of the tile (through LDS).  The transposed values turn as bytes in LDS.
 constexpr int kTileThreads = 512;
 
+//
+// The workgroups after those of the tiles copy operands of the products that
+// follow (none where it only quantises).
 template <typename T, int ACT>
-__global__ __launch_bounds__(kTileThreads) void quantize_tile_kernel(const QuantArgs a)
+__global__ __launch_bounds__(kTileThreads) void quantize_tile_kernel(const QuantArgs a, const PackArgs pack)
 {
+    if ((int)blockIdx.x >= a.blocks) {
+        pack_chunk<uint8_t, kTileThreads>(pack, blockIdx.x - a.blocks);
+        return;
+    }
     constexpr int R = 4, W = kTileThreads / 64, PITCH = 136;
     __shared__ __attribute__((aligned(16))) float cols[W][128];
     __shared__ __attribute__((aligned(16))) float inv[128];

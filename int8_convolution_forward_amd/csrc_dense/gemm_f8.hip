@@ -14,4 +14,7 @@ bool launch_gemm_f8e5(int tile, const GemmArgs &g, int splits, hipStream_t strea
     return launch_gemm_form<f8e5, false, false>(tile, g, splits, stream);
 }
 
+bool launch_gemm_pair_f8e4(const PairArgs &p, hipStream_t stream) { return launch_gemm_pair_f8<f8e4>(p, stream); }
+bool launch_gemm_pair_f8e5(const PairArgs &p, hipStream_t stream) { return launch_gemm_pair_f8<f8e5>(p, stream); }
+
 }  // namespace dense

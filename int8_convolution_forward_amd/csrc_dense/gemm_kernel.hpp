@@ -904,6 +904,22 @@ __global__ __launch_bounds__(64 * WGM * WGN, OCC) void gemm_pair_kernel(const Pa
         column_sums<kCols>(p.sum, b - p.dx.tiles - p.dw.tiles, (float(*)[kCols + 1])smem);
 }
 
+// The same of 8-bit floating point, whose operands are both in rows form.
+template <typename T, int TM, int TN, int WGM, int WGN, int NSA, int NSB, int LH, int OCC>
+__global__ __launch_bounds__(64 * WGM * WGN, OCC) void gemm_pair_f8_kernel(const PairArgs p)
+{
+    constexpr int kCols = 64 * WGM * WGN / kSumGroups;
+    __shared__ __attribute__((aligned(1024)))
+    uint8_t smem[TileCfg<T, TM, TN, WGM, WGN, NSA, NSB, LH, false, false>::LDS_BYTES];
+    const int b = blockIdx.x, products = p.dx.tiles + p.dw.tiles;
+    if (b < products) {
+        const bool second = b >= p.dx.tiles;
+        gemm_tile<T, TM, TN, WGM, WGN, NSA, NSB, LH, false, false>(second ? p.dw : p.dx, smem, second ? b - p.dx.tiles : b, 0);
+    } else {
+        column_sums<kCols>(p.sum, b - products, (float(*)[kCols + 1])smem);
+    }
+}
+
 template <bool INT> struct Choice { typedef float type; };
 template <> struct Choice<true> { typedef int8_t type; };
 

@@ -46,6 +46,18 @@ bool launch_gemm_pair(const PairArgs &p, hipStream_t stream)
     return hipGetLastError() == hipSuccess;
 }
 
+bool launch_gemm_pair_f8e4(const PairArgs &p, hipStream_t stream);
+bool launch_gemm_pair_f8e5(const PairArgs &p, hipStream_t stream);
+
+template <typename T>
+bool launch_gemm_pair_f8(const PairArgs &p, hipStream_t stream)
+{
+    const int sums = (int)(p.sum.cols + 256 / kSumGroups - 1) / (256 / kSumGroups);
+    const dim3 grid((unsigned)(p.dx.tiles + p.dw.tiles + sums)), block(256);
+    hipLaunchKernelGGL((gemm_pair_f8_kernel<T, 64, 64, 2, 2, 3, 3, 4, 3>), grid, block, 0, stream, p);
+    return hipGetLastError() == hipSuccess;
+}
+
 template <typename T, bool ASTR, bool BSTR>
 bool launch_gemm_form(int tile, const GemmArgs &g, int splits, hipStream_t stream)
 {

@@ -59,8 +59,11 @@ void plan_operand(Operand *o, bool allow_rows, bool allow_cols)
     }
 }
 
-// Workgroups that copy an operand.
-int64_t pack_wgs(const Operand &o) { return o.packed ? ceil_div((o.cols ? o.inner : o.dim) * (o.ld / 16), 256) : 0; }
+// Workgroups of so many threads that copy an operand.
+int64_t pack_wgs(const Operand &o, int threads = 256)
+{
+    return o.packed ? ceil_div((o.cols ? o.inner : o.dim) * (o.ld / 16), threads) : 0;
+}
 
 conv_i8_status_t check_reach(const Operand &o)
 {
@@ -87,12 +90,12 @@ PackJob pack_job(const Operand &o, void *dst)
 }
 
 // Both jobs of a launch; returns its workgroups.
-int64_t pack_jobs(const Operand &a, void *da, const Operand &b, void *db, PackArgs *p)
+int64_t pack_jobs(const Operand &a, void *da, const Operand &b, void *db, PackArgs *p, int threads = 256)
 {
     p->job[0] = pack_job(a, da);
     p->job[1] = pack_job(b, db);
-    p->first = (int)pack_wgs(a);
-    return pack_wgs(a) + pack_wgs(b);
+    p->first = (int)pack_wgs(a, threads);
+    return pack_wgs(a, threads) + pack_wgs(b, threads);
 }
 
 bool launch_pack(const Operand &a, void *da, const Operand &b, void *db, hipStream_t stream)
@@ -154,11 +157,11 @@ double gemm_cost(int tile, int64_t M, int64_t N, int64_t kbytes, int splits)
 
 // The same of both gradients' products in one launch with tile kPairTile:
 // either all CUs work through both, or the longer reduction lasts longest.
-double pair_cost(int64_t M, int64_t N, int64_t K)
+double pair_cost(int64_t M, int64_t N, int64_t K, int es = 2)
 {
     const Tile &t = kTile[kPairTile];
     const TileCost &c = kCost[kPairTile];
-    const double sx = (double)ceil_div(2 * N, 64), sw = (double)ceil_div(2 * M, 64);
+    const double sx = (double)ceil_div(es * N, 64), sw = (double)ceil_div(es * M, 64);
     const double all = (sx * (double)ceil_div(M, t.tm) + sw * (double)ceil_div(N, t.tm)) * (double)ceil_div(K, t.tn) / kCUs;
     const double longest = sx > sw ? sx : sw;
     return (all > longest ? all : longest) * c.stage + c.round + c.out * 1.0e-6 * (double)(M + N) * (double)K;

@@ -25,15 +25,15 @@ struct PackArgs {
 };
 
 // One thread copies one chunk; both operands of a product go in one launch.
-// U is an unsigned integer of the element's size.
-template <typename U>
+// U is an unsigned integer of the element's size, THREADS those of a workgroup.
+template <typename U, int THREADS = 256>
 __device__ __forceinline__ void pack_chunk(const PackArgs &a, int block)
 {
     constexpr int E = 16 / sizeof(U);
     struct __attribute__((packed, aligned(sizeof(U)))) Piece { U e[E]; };
     const bool second = block >= a.first;
     const PackJob &j = a.job[second];
-    const int64_t i = (int64_t)(second ? block - a.first : block) * 256 + threadIdx.x;
+    const int64_t i = (int64_t)(second ? block - a.first : block) * THREADS + threadIdx.x;
     if (i >= j.items)
         return;
     // a 64-bit division costs more than the copy
