@@ -123,21 +123,40 @@ __device__ __forceinline__ void mfma16_scaled(v8i a, v8i b, v4f &c, int sa, int 
 #undef DENSE_MFMA
 }
 
-// Bytes k .. k+3 of a row of n scales as a word (zeros past its end), from any
-// address, without reading outside the row.
-__device__ __forceinline__ int scale_word(const uint8_t *row, int k, int n)
+// Bytes k .. k+3 of rows of n scales (n >= 1) as words, zeros past a row's end, from
+// any addresses and without reading outside a row.  The loads go out one after the
+// other straight into v (an address at a time: the tile's sums and fragments leave
+// no registers for all of them), then they are shifted without a condition.
+template <int N, typename F>
+__device__ __forceinline__ void load_scale_words(F row, int k, int n, int (&v)[N])
 {
     if (n >= 4) {
-        const int at = min(k, n - 4), by = k - at;
-        const Pack<uint8_t, 4> w = *(const Pack<uint8_t, 4> *)(row + at);
-        return by < 4 ? (int)(__builtin_bit_cast(unsigned, w) >> (8 * by)) : 0;
-    }
-    unsigned v = 0;
+        const int at = min(k, n - 4);
+        for_each<N>([&](auto ic) __attribute__((always_inline)) {
+            constexpr int i = decltype(ic)::value;
+            v[i] = __builtin_bit_cast(int, *(const Pack<uint8_t, 4> *)(row(i) + at));
+            __builtin_amdgcn_sched_barrier(0);
+        });
+    } else {
+        uint8_t b[3][N];
 #pragma unroll
-    for (int i = 0; i < 3; ++i)
-        if (k + i < n)
-            v |= (unsigned)row[k + i] << (8 * i);
-    return (int)v;
+        for (int j = 0; j < 3; ++j)
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                b[j][i] = row(i)[min(j, n - 1)];
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            v[i] = (int)(((unsigned)b[0][i] | (unsigned)b[1][i] << 8 | (unsigned)b[2][i] << 16) & ((1u << (8 * n)) - 1));
+    }
+}
+
+template <int N>
+__device__ __forceinline__ void shift_scale_words(int k, int n, int (&v)[N])
+{
+    const int by = 8 * min(n >= 4 ? k - min(k, n - 4) : k, 4);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        v[i] = (int)(unsigned)((uint64_t)(unsigned)v[i] >> by);
 }
 
 // Another lane's value by way of the LDS crossbar; `at`: four times its number
@@ -605,13 +624,17 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs &g, uint8_t *smem, int 
     int perm = (lane & 15) * 4;
     auto load_scales = [&](int it) __attribute__((always_inline)) {
         const int k = stage0 + it + 4 * (lane >> 4);
-#pragma unroll
-        for (int x = 0; x < FM; ++x)
-            va[x] = scale_word(g.sa + (int64_t)min(m0 + wm + 16 * x + (lane & 15), g.M - 1) * g.ldsa, k, g.kblocks);
-#pragma unroll
-        for (int y = 0; y < FN; ++y)
-            vb[y] = scale_word(g.sb + (int64_t)(min(n0 + wn + FN * (lane & 15) + y, g.N - 1) >> g.sb_shift) * g.ldsb, k,
-                               g.kblocks);
+        int r = lane & 15;
+        asm volatile("" : "+v"(r));  // addresses are computed here, not kept (in memory) over the loop
+        __builtin_amdgcn_sched_barrier(0);
+        load_scale_words([&](int x) { return g.sa + (int64_t)min(m0 + wm + 16 * x + r, g.M - 1) * g.ldsa; }, k, g.kblocks, va);
+        load_scale_words([&](int y) { return g.sb + (int64_t)(min(n0 + wn + FN * r + y, g.N - 1) >> g.sb_shift) * g.ldsb; }, k,
+                         g.kblocks, vb);
+        // in the registers from here on: else every later use waits for all loads, those to LDS among them
+        __builtin_amdgcn_s_waitcnt(0 | (7 << 4) | (15 << 8));
+        shift_scale_words(k, g.kblocks, va);
+        shift_scale_words(k, g.kblocks, vb);
+        __builtin_amdgcn_sched_barrier(0);
     };
     auto f8_read_a = [&](int x, int slot) __attribute__((always_inline)) {
         const uint8_t *base = smem + slot * A_BYTES;

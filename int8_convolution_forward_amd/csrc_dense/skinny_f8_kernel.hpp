@@ -128,12 +128,9 @@ __global__ __launch_bounds__(64 * W) void skinny_f8_kernel(const SkinnyF8Args a)
     for (int grp = wave; grp * D < a.kblocks; grp += W) {
         // the compiler counts these loads but not those to LDS: they go first
         int sx[G], sw[R];
-#pragma unroll
-        for (int i = 0; i < G; ++i)
-            sx[i] = scale_word(a.sx + (int64_t)min(16 * i + r, g.M - 1) * a.ldsx, grp * D, a.kblocks);
-#pragma unroll
-        for (int i = 0; i < R; ++i)
-            sw[i] = scale_word(a.sw + (int64_t)(min(n0 + 16 * i + r, g.N - 1) >> a.sw_shift) * a.ldsw, grp * D, a.kblocks);
+        load_scale_words([&](int i) { return a.sx + (int64_t)min(16 * i + r, g.M - 1) * a.ldsx; }, grp * D, a.kblocks, sx);
+        load_scale_words([&](int i) { return a.sw + (int64_t)(min(n0 + 16 * i + r, g.N - 1) >> a.sw_shift) * a.ldsw; }, grp * D,
+                         a.kblocks, sw);
         v4i xv[XL ? 1 : D][2][G];
         if constexpr (!XL)
 #pragma unroll
@@ -141,6 +138,8 @@ __global__ __launch_bounds__(64 * W) void skinny_f8_kernel(const SkinnyF8Args a)
                 load_x(grp * D + d, xv[d]);
         __builtin_amdgcn_sched_barrier(0);
         for_each<D>([&](auto dc) __attribute__((always_inline)) { issue(grp * D + decltype(dc)::value, dc); });
+        shift_scale_words(grp * D, a.kblocks, sx);
+        shift_scale_words(grp * D, a.kblocks, sw);
         for_each<D>([&](auto dc) __attribute__((always_inline)) {
             constexpr int d = decltype(dc)::value;
             __builtin_amdgcn_sched_barrier(0);
