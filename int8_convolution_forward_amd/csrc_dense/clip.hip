@@ -80,14 +80,17 @@ int64_t table(const dense_clip_grads_t &a, int64_t l, ClipTable *t)
     memset(t, 0, sizeof *t);
     const int64_t from = l * kClipTensors;
     t->count = (int)std::min<int64_t>(a.count - from, kClipTensors);
-    int64_t chunks = 0;
+    int64_t total = 0, chunks = 0;
+    for (int i = 0; i < t->count; ++i)
+        total += std::min(a.in[from + i].n, (int64_t)kClipWgs * kClipChunk);
+    t->chunk = (int)std::min<int64_t>(kClipChunk, std::max<int64_t>(1, ceil_div(total, (int64_t)kClipWgs * kClipStep)) * kClipStep);
     for (int i = 0; i < t->count; ++i) {
         t->in[i] = a.in[from + i].ptr;
         t->out[i] = const_cast<void *>(a.out[from + i].ptr);
         t->n[i] = a.in[from + i].n;
         t->dt[i] = (uint8_t)a.in[from + i].dtype;
         t->first[i] = (unsigned)chunks;
-        chunks += ceil_div(t->n[i], kClipChunk);
+        chunks += ceil_div(t->n[i], t->chunk);
         if (chunks >= kMaxChunks)
             return chunks;
     }

@@ -2,7 +2,7 @@
 // values, bound by HBM.
 //
 // A launch takes a table of tensors as its argument; its workgroups walk over
-// chunks of kChunk values, numbered through all the table's tensors.  Squares are
+// chunks of up to kClipChunk values, numbered through all the table's tensors.  Squares are
 // summed in 64 bits, so that no finite value's square overflows or vanishes and the
 // sum is exact to about 2^-53 a term; the vector unit has more of that than HBM can
 // feed.  Workgroups leave a partial sum each, and every workgroup of the second
@@ -16,7 +16,7 @@
 namespace dense {
 
 constexpr int kClipTensors = 128, kClipThreads = 256;
-constexpr int kClipChunk = 16384;  // values
+constexpr int kClipStep = kClipThreads * 8, kClipChunk = 8 * kClipStep;  // values: of a workgroup's load, the most of a chunk
 constexpr int kClipWgs = 1024;     // of a launch, at most
 
 struct ClipTable {
@@ -26,21 +26,8 @@ struct ClipTable {
     unsigned first[kClipTensors + 1];  // number of a tensor's first chunk; the last: of all
     uint8_t dt[kClipTensors];
     int count;
+    int chunk;                         // values: kClipChunk, or less where that would leave CUs without one
 };
-
-// Tensor of chunk b: the last whose first chunk is not beyond it (tensors of no values have none)
-__device__ __forceinline__ int clip_tensor(const ClipTable &t, unsigned b)
-{
-    int lo = 0, hi = t.count;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (t.first[mid] <= b)
-            lo = mid;
-        else
-            hi = mid;
-    }
-    return lo;
-}
 
 __device__ __forceinline__ double wave_sum64(double v)
 {
@@ -60,40 +47,46 @@ __device__ __forceinline__ double group_sum64(double v, double *red)
     return (red[0] + red[1]) + (red[2] + red[3]);
 }
 
-// f(element offset, how many values exist) for each group of eight of a chunk, U of them together
+// f(tensor, first value) for each of the workgroup's chunks, in order.  Tensors of no values have no chunks.
 template <typename F>
 __device__ __forceinline__ void clip_walk(const ClipTable &t, F f)
 {
+    int i = 0;
     for (unsigned b = blockIdx.x; b < t.first[t.count]; b += gridDim.x) {
-        const int i = __builtin_amdgcn_readfirstlane(clip_tensor(t, b));
-        f(i, (int64_t)(b - t.first[i]) * kClipChunk);
+        while (b >= t.first[i + 1])
+            ++i;
+        f(i, (int64_t)(b - t.first[i]) * t.chunk);
     }
 }
 
+// The loads of a whole chunk, or of a quarter of its values in 32 bits, go out together, as they lie in memory.
 template <typename T>
-__device__ __forceinline__ double chunk_squares(const T *p, int64_t at, int64_t n)
+__device__ __forceinline__ double chunk_squares(const T *p, int64_t at, int64_t end)
 {
-    constexpr int U = 4;
+    constexpr int U = 16 / sizeof(T), STEP = kClipStep;
     double s[2] = {0.0, 0.0};
-    const int64_t end = min(n, at + kClipChunk);
-    int64_t c = at + threadIdx.x * 8;
-    for (; c + (U - 1) * kClipThreads * 8 + 8 <= end; c += U * kClipThreads * 8) {
-        float v[U][8];
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            load_all(p + c + u * kClipThreads * 8, v[u]);
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                s[k & 1] = __builtin_fma((double)v[u][k], (double)v[u][k], s[k & 1]);
-    }
-    for (; c < end; c += kClipThreads * 8) {
-        float v[8];
-        load_n(p + c, (int)(end - c), v);
+    auto add = [&](const float (&v)[8]) {
 #pragma unroll
         for (int k = 0; k < 8; ++k)
             s[k & 1] = __builtin_fma((double)v[k], (double)v[k], s[k & 1]);
+    };
+    int64_t c = at + threadIdx.x * 8;
+    for (; c + (U - 1) * STEP + 8 <= end; c += U * STEP) {
+        Raw8<T> r[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            r[u] = __builtin_bit_cast(Raw8<T>, *(const Pack<T, 8> *)(p + c + u * STEP));
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float v[8];
+            widen(r[u], v);
+            add(v);
+        }
+    }
+    for (; c < end; c += STEP) {
+        float v[8];
+        load_n(p + c, (int)(end - c), v);
+        add(v);
     }
     return s[0] + s[1];
 }
@@ -104,11 +97,11 @@ __global__ __launch_bounds__(kClipThreads) void clip_squares_kernel(const ClipTa
     double s = 0.0;
     clip_walk(t, [&](int i, int64_t at) {
         if (t.dt[i] == DENSE_BF16)
-            s += chunk_squares((const bf16 *)t.in[i], at, t.n[i]);
+            s += chunk_squares((const bf16 *)t.in[i], at, min(t.n[i], at + t.chunk));
         else if (t.dt[i] == DENSE_FP16)
-            s += chunk_squares((const f16 *)t.in[i], at, t.n[i]);
+            s += chunk_squares((const f16 *)t.in[i], at, min(t.n[i], at + t.chunk));
         else
-            s += chunk_squares((const float *)t.in[i], at, t.n[i]);
+            s += chunk_squares((const float *)t.in[i], at, min(t.n[i], at + t.chunk));
     });
     s = group_sum64(s, red);
     if (threadIdx.x == 0)
@@ -116,10 +109,9 @@ __global__ __launch_bounds__(kClipThreads) void clip_squares_kernel(const ClipTa
 }
 
 template <typename T>
-__device__ __forceinline__ void chunk_scale(const T *p, T *q, int64_t at, int64_t n, double factor)
+__device__ __forceinline__ void chunk_scale(const T *p, T *q, int64_t at, int64_t end, double factor)
 {
     constexpr int U = 4;
-    const int64_t end = min(n, at + kClipChunk);
     // 16-bit values in 32 bits, rounded once to 32 and once to 16; 32-bit ones in 64, rounded once
     const float f = (float)factor;
     auto scale = [&](float v) { return sizeof(T) == 2 ? v * f : (float)((double)v * factor); };
@@ -165,11 +157,11 @@ __global__ __launch_bounds__(kClipThreads) void clip_scale_kernel(const ClipTabl
         if (!clips && t.in[i] == t.out[i])
             return;
         if (t.dt[i] == DENSE_BF16)
-            chunk_scale((const bf16 *)t.in[i], (bf16 *)t.out[i], at, t.n[i], factor);
+            chunk_scale((const bf16 *)t.in[i], (bf16 *)t.out[i], at, min(t.n[i], at + t.chunk), factor);
         else if (t.dt[i] == DENSE_FP16)
-            chunk_scale((const f16 *)t.in[i], (f16 *)t.out[i], at, t.n[i], factor);
+            chunk_scale((const f16 *)t.in[i], (f16 *)t.out[i], at, min(t.n[i], at + t.chunk), factor);
         else
-            chunk_scale((const float *)t.in[i], (float *)t.out[i], at, t.n[i], factor);
+            chunk_scale((const float *)t.in[i], (float *)t.out[i], at, min(t.n[i], at + t.chunk), factor);
     });
 }
 
