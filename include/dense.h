@@ -1,18 +1,19 @@
 /*
- * dense.h -- the dense layer and layer norm, forward and backward, for AMD
- * Instinct MI355X (gfx950): the operators of a feed-forward block, beside the
- * INT8 convolution of conv_i8.h.
+ * dense.h -- the operators of a feed-forward block and of its training, for AMD
+ * Instinct MI355X (gfx950), beside the INT8 convolution of conv_i8.h: the dense
+ * layer in 16, 32 and 8 bits, norms, the quantiser, the clipping of gradients.
  *
  *   linear               z = (x w^T) * x_scale[m] * w_scale[n] + bias[n]
  *                        y = act(z) + residual
  *   linear_backward      g = dy * act'(z); dx = g w; dw = g^T x; dbias = sum over rows of g
  *   layer_norm           y = (x - mean) * rstd * weight + bias, rstd = 1 / sqrt(var + eps)
  *   layer_norm_backward  dx, dweight and dbias of it
- *   quantize, dequantize rows of 8-bit floating point with a scale for each block of 128, and back
+ *   quantize             x to 8-bit floating point with a scale for each block of 128
+ *   dequantize           and back
  *   linear_fp8           the dense layer on such operands
  *   linear_fp8_backward  its gradients
- *   residual_norm        r = scale x + gate norm(h) weight', y = norm(r) weight + bias
- *   residual_norm_backward  its gradients
+ *   residual_norm        r = alpha x + gate n, n = norm(h) post_weight or h; y = norm(r) weight + bias
+ *   residual_norm_backward its gradients
  *   clip_grads           many gradients scaled so that their norm together stays within a limit
  *
  * A matrix is a device pointer, its dims and its strides in ELEMENTS; strides
@@ -23,8 +24,9 @@
  * Argument errors are found on the host before any device work.  Results do
  * not depend on the order in which workgroups run: no sum uses atomics.
  *
- * Sums, norms and products accumulate in 32 bits; each output is rounded once
- * (half to even) to its type.  NaN and infinities propagate as in the formulas.
+ * Sums, norms and products accumulate in 32 bits, the norm of many gradients in
+ * 64 (what 8-bit products lose before that: see dense_linear_fp8); each output is
+ * rounded once (half to even) to its type.  NaN and infinities propagate as in the formulas.
  */
 #ifndef DENSE_H
 #define DENSE_H
@@ -311,7 +313,8 @@ conv_i8_status_t dense_residual_norm_backward(const dense_residual_norm_backward
  * out = in min(1, max_norm / norm).  A norm that is not finite leaves the values as they are
  * (the caller sees it in `norm`).  in and out: `count` vectors of BF16, FP16 or
  * FP32; an out is its in itself, or of the same type and size and overlaps
- * no other vector.  No two vectors of `in` overlap where they are written.
+ * no other vector.  No two vectors of `in` overlap where they are written, and
+ * `norm` lies in none of them.
  */
 typedef struct {
     const dense_vec_t *in, *out;

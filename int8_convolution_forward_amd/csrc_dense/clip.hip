@@ -22,10 +22,11 @@ struct Span {
 // Memory that is written has to be of one vector alone.
 conv_i8_status_t check_overlap(const dense_clip_grads_t &a)
 {
-    Span *spans = new (std::nothrow) Span[2 * (size_t)a.count];
+    Span *spans = new (std::nothrow) Span[2 * (size_t)a.count + 1];
     if (!spans)
         return CONV_I8_ERR_SCRATCH;
-    int64_t count = 0;
+    int64_t count = 1;
+    spans[0] = {(uintptr_t)a.norm, (uintptr_t)a.norm + sizeof(float), true};
     for (int64_t i = 0; i < a.count; ++i) {
         const int64_t bytes = a.in[i].n * size_of(a.in[i].dtype);
         if (bytes == 0)

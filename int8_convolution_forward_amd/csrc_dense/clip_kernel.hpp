@@ -112,9 +112,10 @@ template <typename T>
 __device__ __forceinline__ void chunk_scale(const T *p, T *q, int64_t at, int64_t end, double factor)
 {
     constexpr int U = 4;
-    // 16-bit values in 32 bits, rounded once to 32 and once to 16; 32-bit ones in 64, rounded once
-    const float f = (float)factor;
-    auto scale = [&](float v) { return sizeof(T) == 2 ? v * f : (float)((double)v * factor); };
+    // 16-bit values in 32 bits, rounded once to 32 and once to 16; 32-bit ones in 64, rounded once.
+    // A factor that 32 bits would round to fewer digits, or to zero, comes in two.
+    const float low = factor < 0x1p-100 ? 0x1p-96f : 1.0f, f = (float)(factor / low);
+    auto scale = [&](float v) { return sizeof(T) == 2 ? v * f * low : (float)((double)v * factor); };
     int64_t c = at + threadIdx.x * 8;
     for (; c + (U - 1) * kClipThreads * 8 + 8 <= end; c += U * kClipThreads * 8) {
         float v[U][8];

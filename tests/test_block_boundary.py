@@ -50,7 +50,7 @@ def norm_backward(dr=M8, dy=M8, r=M8, h=M8, dx=M8, dh=M8, gate=NM, dgate=NM, wei
                                               *prstd, *dw, *db, *dp, alpha, kind)
 
 
-def clip(a, b=None, max_norm=1.0, norm=FAKE, count=None):
+def clip(a, b=None, max_norm=1.0, norm=FAKE - 256, count=None):
     """(argument, what it points to)."""
     held = [b"".join(dense.struct.pack("=Q2q", *v) for v in t) for t in (a, a if b is None else b)]
     ptrs = [ctypes.cast(ctypes.c_char_p(h), ctypes.c_void_p).value for h in held]
@@ -235,6 +235,26 @@ def test_residual_norm_backward_refusals(over, status):
     assert name(dense.lib.dense_residual_norm_backward(args, None, 0, None)) == want
 
 
+def wide_backward(m, d, **over):
+    """Gradients of the scale alone of m rows of d columns."""
+    r = mat(m, d, BF16)
+    return norm_backward(**dict(dict(dr=NM, dy=r, r=r, h=NM, dx=r, dh=NM, mean=vec(m, FP32), rstd=vec(m, FP32),
+                                     dw=vec(d, BF16), db=NV), **over))
+
+
+def test_residual_norm_backward_larger_than_a_launch():
+    """The sums over rows take a launch of at most 2^32 threads and 65535 jobs."""
+    assert size("dense_residual_norm_backward", wide_backward(1, 1 << 25))[0] == "CONV_I8_OK"
+    assert size("dense_residual_norm_backward", wide_backward(1, 1 << 26))[0] == "CONV_I8_ERR_UNSUPPORTED"
+    assert size("dense_residual_norm_backward", wide_backward(1, 1 << 26, dw=NV))[0] == "CONV_I8_OK"
+    # no rows, and the gradients of many rows of the gate to be cleared
+    e = mat(0, 40, BF16)
+    for gates, want in ((1 << 15, "CONV_I8_OK"), (1 << 16, "CONV_I8_ERR_UNSUPPORTED")):
+        gate = mat(gates, 40, BF16)
+        args = norm_backward(dr=e, dy=e, r=e, h=e, dx=e, dh=e, gate=gate, dgate=gate, mean=vec(0, FP32), rstd=vec(0, FP32))
+        assert size("dense_residual_norm_backward", args)[0] == want
+
+
 A, B = FAKE, FAKE + (1 << 20)
 
 
@@ -254,6 +274,9 @@ A, B = FAKE, FAKE + (1 << 20)
     ([vec(8, FP32, ptr=A), vec(8, FP32, ptr=A + 16)], None, {}, "PARAM"),                # overlapping, in place
     ([vec(8, FP32, ptr=A), vec(8, FP32, ptr=B)], [vec(8, FP32, ptr=B), vec(8, FP32, ptr=A)], {}, "PARAM"),
     ([vec(8, FP32, ptr=A)], [vec(8, FP32, ptr=A + 4)], {}, "PARAM"),                     # into itself, shifted
+    ([vec(8, FP32, ptr=A)], None, dict(norm=A + 28), "PARAM"),                           # the norm in a gradient
+    ([vec(8, FP32, ptr=A)], [vec(8, FP32, ptr=B)], dict(norm=A), "PARAM"),
+    ([vec(8, FP32, ptr=A)], [vec(8, FP32, ptr=B)], dict(norm=A + 32), "OK"),
     ([vec(1 << 40, BF16)] , None, {}, "OK"),
 ])
 def test_clip_refusals(a, b, over, status):

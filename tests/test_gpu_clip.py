@@ -63,6 +63,18 @@ def test_norm_and_values(ci8, sizes):
         assert torch.equal(again, got) and all(torch.equal(a, b) for a, b in zip(out, mine))
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+def test_factors_that_32_bits_do_not_hold(ci8, dtype):
+    """Norms so far above the limit that their quotient is below 2^-126."""
+    for up, limit in ((100, 2.0 ** -4), (100, 2.0 ** -40), (120, 2.0 ** 30), (120, 2.0 ** -60)):
+        grads = make([1000, 9], 4, dtype, 2.0 ** up)
+        norm, want = expected(grads, limit)
+        got = ci8.clip_grad_norm(grads, limit)
+        assert abs(float(got) - norm) <= 2 ** -23 * norm
+        for a, b in zip(grads, want):
+            close(a, b)
+
+
 def test_shapes_and_strides(ci8):
     g = torch.Generator(device="cuda").manual_seed(1)
     base = torch.randn(40, 60, generator=g, device="cuda")
