@@ -9,6 +9,7 @@ namespace dense {
 namespace {
 
 constexpr int64_t kWsAlign = 256;
+constexpr int64_t kMaxGridY = 65535;
 
 // The sums over workgroups: blockIdx.y 0 dweight, 1 dbias, 2 dpost_weight, 3 + g row g of dgate.
 struct ResNormSumArgs {
@@ -41,7 +42,6 @@ __global__ __launch_bounds__(32 * kSumGroups) void residual_norm_sums_kernel(con
     if (c.out0)
         column_sums<32>(c, blockIdx.x, red);
 }
-
 
 // Present, [M, D] of type dt, rows contiguous
 conv_i8_status_t check_rows(dense_mat_t *m, int64_t M, int64_t D, int64_t dt, bool output)
@@ -123,6 +123,9 @@ struct BackPlan {
     int groups = 1, chunks = 1, wgs = 0;
     int64_t part_ld = 0, part_bytes = 0, ws_bytes = 0;
     bool any() const { return !back_in_registers(D); }
+    // Rows of the gate whose gradients residual_norm_sums_kernel writes: a workgroup that takes
+    // all rows of one has written it.
+    int64_t gate_sums() const { return d.dgate.dtype != DENSE_NONE && (chunks > 1 || M == 0) ? groups : 0; }
 };
 
 conv_i8_status_t analyze(const dense_residual_norm_backward_t *args, BackPlan *p)
@@ -197,6 +200,9 @@ conv_i8_status_t analyze(const dense_residual_norm_backward_t *args, BackPlan *p
         p->wgs = p->chunks > 1 || want > p->groups ? p->groups * p->chunks : (int)want;
     }
     p->part_bytes = p->sums && p->wgs ? round_up((int64_t)p->wgs * 4 * p->part_ld * 4, kWsAlign) : 0;
+    // residual_norm_columns_kernel takes fewer threads
+    if (p->sums && (3 + p->gate_sums() > kMaxGridY || !launch_fits(ceil_div(D, 32) * (3 + p->gate_sums()), 32 * kSumGroups)))
+        return CONV_I8_ERR_UNSUPPORTED;
     p->ws_bytes = p->part_bytes + (p->sums && p->any() ? round_up(M * 8, kWsAlign) : 0);
     return CONV_I8_OK;
 }
@@ -350,9 +356,7 @@ conv_i8_status_t dense_residual_norm_backward(const dense_residual_norm_backward
         c.out[2] = const_cast<void *>(d.dpost_weight.ptr);
         c.dgate = a.dgate;
         c.lddg = a.lddg;
-        // a workgroup that takes all rows of a row of the gate has written it
-        const bool gates = a.dgate && (p.chunks > 1 || p.M == 0);
-        const dim3 grid((unsigned)ceil_div(p.D, 32), (unsigned)(3 + (gates ? p.groups : 0)));
+        const dim3 grid((unsigned)ceil_div(p.D, 32), (unsigned)(3 + p.gate_sums()));
         hipLaunchKernelGGL(residual_norm_sums_kernel, grid, dim3(32 * kSumGroups), 0, s, c);
         if (hipGetLastError() != hipSuccess)
             return CONV_I8_ERR_HIP;

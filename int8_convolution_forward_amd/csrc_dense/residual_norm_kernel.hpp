@@ -209,11 +209,14 @@ template <typename T, int P, bool RMS, bool Q8>
 __global__ __launch_bounds__(P) void residual_norm_any_kernel(const ResNormArgs a)
 {
     constexpr int NW = P > 64 ? P / 64 : 1;
-    __shared__ float red[4 * NW];  // a set's next use comes after another set's barrier
+    __shared__ float red[2 * NW];
     const int t = threadIdx.x;
+    int set = 0;
+    // the sets take turns: a slow wave may still read the last one
+    auto sum = [&](float v) __attribute__((always_inline)) { return row_reduce<P>(v, red, set ^= 1); };
     for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x) {
         const T *x = (const T *)a.x + m * a.ldx;
-        auto stats = [&](const T *p, int set, float &mean, float &rstd) {
+        auto stats = [&](const T *p, float &mean, float &rstd) {
             mean = 0.0f;
             if constexpr (!RMS) {
                 float s = 0.0f;
@@ -224,7 +227,7 @@ __global__ __launch_bounds__(P) void residual_norm_any_kernel(const ResNormArgs 
                     for (int k = 0; k < 8; ++k)
                         s += v[k];
                 }
-                mean = row_reduce<P>(s, red, set) / a.d;
+                mean = sum(s) / a.d;
             }
             float s = 0.0f;
             for (int64_t c = t * 8; c < a.D; c += P * 8) {
@@ -234,14 +237,14 @@ __global__ __launch_bounds__(P) void residual_norm_any_kernel(const ResNormArgs 
                 for (int k = 0; k < 8; ++k)
                     s = __builtin_fmaf(v[k] - mean, v[k] - mean, s);
             }
-            rstd = 1.0f / sqrtf(row_reduce<P>(s, red, set + 1) / a.d + a.eps);
+            rstd = 1.0f / sqrtf(sum(s) / a.d + a.eps);
         };
         float mean, rstd;
         const T *src = x;
         if (a.h) {
             const T *h = (const T *)a.h + m * a.ldh;
             if (a.post_weight) {
-                stats(h, 0, mean, rstd);
+                stats(h, mean, rstd);
                 if (t == 0) {
                     if (a.post_mean)
                         a.post_mean[m] = mean;
@@ -275,7 +278,7 @@ __global__ __launch_bounds__(P) void residual_norm_any_kernel(const ResNormArgs 
             }
             src = r;
         }
-        stats(src, 2, mean, rstd);
+        stats(src, mean, rstd);
         if (t == 0) {
             if (a.mean)
                 a.mean[m] = mean;
@@ -352,10 +355,9 @@ struct ResNormBackArgs {
     float2 *row_sums;                 // residual_norm_backward_any_kernel: both means of a row's first norm
 };
 
-// A thread group takes U rows at a time, so that one barrier joins the sums of all
-// of them, and has the next ones' loads in flight (AHEAD).  Between its steps it
-// keeps the rows as they lie in memory and widens them again: the values in 32
-// bits would take twice the registers.
+// A thread group has the next row's loads in flight (AHEAD).  Between its steps it
+// keeps a row as it lies in memory and widens it again: the values in 32 bits would
+// take twice the registers.
 template <typename T>
 __device__ __forceinline__ void as_in_memory(Raw8<T> &r)
 {
@@ -364,7 +366,7 @@ __device__ __forceinline__ void as_in_memory(Raw8<T> &r)
         asm volatile("" : "+v"(r.w[i]));
 }
 
-template <typename T, int P, int V, int U, bool AHEAD, int OCC, bool TAIL, bool RMS, bool POST>
+template <typename T, int P, int V, bool AHEAD, int OCC, bool TAIL, bool RMS, bool POST>
 __global__ __launch_bounds__(norm_threads(P), OCC) void residual_norm_backward_kernel(const ResNormBackArgs a)
 {
     constexpr int RPW = norm_threads(P) / P;
@@ -419,34 +421,27 @@ __global__ __launch_bounds__(norm_threads(P), OCC) void residual_norm_backward_k
     struct Row {
         Raw8<T> r[V], dy[V], dr[V], h[V];
         float mean, rstd, post_mean, post_rstd;
-    } ring[U];
-    auto load = [&](int64_t m, int64_t end) __attribute__((always_inline)) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {  // rows past the end repeat the last one
-            const int64_t at = min(m + u, end - 1);
-            load_row<T, P, V>((const T *)a.r + at * a.ldr, a.D, t, ring[u].r);
-            load_row<T, P, V>((const T *)a.dy + at * a.lddy, a.D, t, ring[u].dy);
-            if (a.dr)
-                load_row<T, P, V>((const T *)a.dr + at * a.lddr, a.D, t, ring[u].dr);
-            if (use_h)
-                load_row<T, P, V>((const T *)a.h + at * a.ldh, a.D, t, ring[u].h);
-            ring[u].rstd = a.rstd[at];
-            ring[u].mean = RMS ? 0.0f : a.mean[at];
-            if constexpr (POST) {
-                ring[u].post_rstd = a.post_rstd[at];
-                ring[u].post_mean = RMS ? 0.0f : a.post_mean[at];
-            }
+    } ring;
+    auto load = [&](int64_t m) __attribute__((always_inline)) {
+        load_row<T, P, V>((const T *)a.r + m * a.ldr, a.D, t, ring.r);
+        load_row<T, P, V>((const T *)a.dy + m * a.lddy, a.D, t, ring.dy);
+        if (a.dr)
+            load_row<T, P, V>((const T *)a.dr + m * a.lddr, a.D, t, ring.dr);
+        if (use_h)
+            load_row<T, P, V>((const T *)a.h + m * a.ldh, a.D, t, ring.h);
+        ring.rstd = a.rstd[m];
+        ring.mean = RMS ? 0.0f : a.mean[m];
+        if constexpr (POST) {
+            ring.post_rstd = a.post_rstd[m];
+            ring.post_mean = RMS ? 0.0f : a.post_mean[m];
         }
     };
     int set = 0;
-    // Both sums of a lane's numbers of each row over its threads, as means.  A wave folds two numbers
-    // into one register and four of those into one, so that four sums cost little more than one.
-    auto means = [&](float (&s1)[U], float (&s2)[U]) __attribute__((always_inline)) {
-        static_assert(U == 1 || U == 2, "rows at a time");
-        auto add = [](float x, float y) { return x + y; };
-        float v = fold_halves(s1[0], s2[0], add);
-        v = row16_sum(U == 2 ? fold_rows(v, fold_halves(s1[U - 1], s2[U - 1], add), add) : v);
-        // U 1: rows of lanes 0, 1: s1's parts, 2, 3: s2's; U 2: s1 of both rows, then s2
+    // Both sums of a lane's numbers over a row's threads, as means.  A wave folds them into one register
+    // first, so that two sums cost little more than one.
+    auto means = [&](float &s1, float &s2) __attribute__((always_inline)) {
+        // lanes 0 to 31 hold s1's parts, 32 to 63 s2's
+        const float v = row16_sum(fold_halves(s1, s2, [](float x, float y) { return x + y; }));
         float r[4];
         if constexpr (P > 64) {
             if ((threadIdx.x & 15) == 0)
@@ -466,15 +461,8 @@ __global__ __launch_bounds__(norm_threads(P), OCC) void residual_norm_backward_k
             for (int q = 0; q < 4; ++q)
                 r[q] = lane_value(v, 16 * q);
         }
-        if constexpr (U == 1) {
-            s1[0] = RMS ? 0.0f : (r[0] + r[1]) * a.inv_d;
-            s2[0] = (r[2] + r[3]) * a.inv_d;
-        } else {
-            s1[0] = RMS ? 0.0f : r[0] * a.inv_d;
-            s1[U - 1] = RMS ? 0.0f : r[1] * a.inv_d;
-            s2[0] = r[2] * a.inv_d;
-            s2[U - 1] = r[3] * a.inv_d;
-        }
+        s1 = RMS ? 0.0f : (r[0] + r[1]) * a.inv_d;
+        s2 = (r[2] + r[3]) * a.inv_d;
     };
     // (v - mean) rstd of group i, 0 past the row's end, also where mean rstd is infinite
     auto normed = [&](const Raw8<T> &raw, int i, float mean, float rstd, float (&v)[8]) __attribute__((always_inline)) {
@@ -491,142 +479,123 @@ __global__ __launch_bounds__(norm_threads(P), OCC) void residual_norm_backward_k
         }
     };
 
-    const int step = RPW * U * a.chunks;
+    const int step = RPW * a.chunks;
     for (int grp = blockIdx.x / a.chunks; grp < a.groups; grp += gridDim.x / a.chunks) {
         const int64_t base = (int64_t)grp * a.gate_rows, m1 = base + a.gate_rows;
-        const int64_t m0 = base + (blockIdx.x % a.chunks * RPW + sub) * U;
+        const int64_t m0 = base + blockIdx.x % a.chunks * RPW + sub;
         if (a.gate)
             load_row<T, P, V>((const T *)a.gate + (int64_t)grp * a.ldg, a.D, t, g);
         if (AHEAD && m0 < m1)
-            load(m0, m1);
+            load(m0);
         for (int64_t m = m0; m < m1; m += step) {
             if constexpr (!AHEAD)
-                load(m, m1);
-            Row cur[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                cur[u] = ring[u];
+                load(m);
+            Row cur = ring;
             if (AHEAD && m + step < m1)
-                load(m + step, m1);
-            float s1[U], s2[U], p1[U], p2[U], e[U][V][8];
+                load(m + step);
+            float s1 = 0.0f, s2 = 0.0f, p1 = 0.0f, p2 = 0.0f, e[V][8];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                s1[u] = s2[u] = p1[u] = p2[u] = 0.0f;
-                if (m + u >= m1)
-                    continue;
+            for (int i = 0; i < V; ++i) {
+                float wv[8], dy[8], rh[8];
+                as_in_memory(w[i]);
+                widen_group<TAIL, P>(w[i], a.D, i, t, wv);
+                widen_group<TAIL, P>(cur.dy[i], a.D, i, t, dy);
+                normed(cur.r[i], i, cur.mean, cur.rstd, rh);
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    float wv[8], dy[8], rh[8];
-                    as_in_memory(w[i]);
-                    widen_group<TAIL, P>(w[i], a.D, i, t, wv);
-                    widen_group<TAIL, P>(cur[u].dy[i], a.D, i, t, dy);
-                    normed(cur[u].r[i], i, cur[u].mean, cur[u].rstd, rh);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const float c = dy[k] * wv[k];
-                        s1[u] += c;
-                        s2[u] = __builtin_fmaf(c, rh[k], s2[u]);
-                        sum[0][i][k] = __builtin_fmaf(dy[k], rh[k], sum[0][i][k]);
-                        sum[1][i][k] += dy[k];
-                    }
+                for (int k = 0; k < 8; ++k) {
+                    const float c = dy[k] * wv[k];
+                    s1 += c;
+                    s2 = __builtin_fmaf(c, rh[k], s2);
+                    sum[0][i][k] = __builtin_fmaf(dy[k], rh[k], sum[0][i][k]);
+                    sum[1][i][k] += dy[k];
                 }
             }
             means(s1, s2);
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (m + u >= m1)
+            for (int i = 0; i < V; ++i) {
+                const int at = (i * P + t) * 8, cnt = a.D - at;
+                const bool whole = (i + 1) * P * 8 <= a.D;
+                auto put = [&](void *p, int64_t ld, const float (&o)[8]) __attribute__((always_inline)) {
+                    T *q = (T *)p + m * ld + at;
+                    if (whole || (!TAIL && cnt > 0))
+                        store_all(q, o);
+                    else if constexpr (TAIL)
+                        store_n(q, cnt, o);
+                };
+                float tv[8], o[8], wv[8], rh[8];
+                as_in_memory(w[i]);
+                as_in_memory(cur.r[i]);
+                as_in_memory(cur.dy[i]);
+                widen_group<TAIL, P>(w[i], a.D, i, t, wv);
+                widen_group<TAIL, P>(cur.dy[i], a.D, i, t, tv);
+                normed(cur.r[i], i, cur.mean, cur.rstd, rh);
+                if (a.dr) {
+                    widen_group<TAIL, P>(cur.dr[i], a.D, i, t, o);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        o[k] = 0.0f;
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    tv[k] = __builtin_fmaf(tv[k], wv[k], -s1);
+                    tv[k] = __builtin_fmaf(cur.rstd, __builtin_fmaf(-rh[k], s2, tv[k]), o[k]);
+                    o[k] = a.alpha * tv[k];
+                }
+                put(a.dx, a.lddx, o);
+                if (!a.dh)
                     continue;
+                if (!whole) {  // what mean(c) leaves past the row's end
+                    asm volatile("");
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const int at = (i * P + t) * 8, cnt = a.D - at;
-                    const bool whole = (i + 1) * P * 8 <= a.D;
-                    auto put = [&](void *p, int64_t ld, const float (&o)[8]) __attribute__((always_inline)) {
-                        T *q = (T *)p + (m + u) * ld + at;
-                        if (whole || (!TAIL && cnt > 0))
-                            store_all(q, o);
-                        else if constexpr (TAIL)
-                            store_n(q, cnt, o);
-                    };
-                    float tv[8], o[8], wv[8], rh[8];
-                    as_in_memory(w[i]);
-                    as_in_memory(cur[u].r[i]);
-                    as_in_memory(cur[u].dy[i]);
-                    widen_group<TAIL, P>(w[i], a.D, i, t, wv);
-                    widen_group<TAIL, P>(cur[u].dy[i], a.D, i, t, tv);
-                    normed(cur[u].r[i], i, cur[u].mean, cur[u].rstd, rh);
-                    if (a.dr) {
-                        widen_group<TAIL, P>(cur[u].dr[i], a.D, i, t, o);
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            o[k] = 0.0f;
-                    }
+                    for (int k = 0; k < 8; ++k)
+                        tv[k] = (TAIL ? k < cnt : cnt > 0) ? tv[k] : 0.0f;
+                }
+                float hh[8], gv[8], pv[8];
+                if constexpr (POST) {
+                    normed(cur.h[i], i, cur.post_mean, cur.post_rstd, hh);
+                    as_in_memory(pw[i]);
+                    widen_group<TAIL, P>(pw[i], a.D, i, t, pv);
+                } else if (use_h) {
+                    widen_group<TAIL, P>(cur.h[i], a.D, i, t, hh);
+                }
+                if (a.gate) {
+                    as_in_memory(g[i]);
+                    widen_group<TAIL, P>(g[i], a.D, i, t, gv);
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
-                        tv[k] = __builtin_fmaf(tv[k], wv[k], -s1[u]);
-                        tv[k] = __builtin_fmaf(cur[u].rstd, __builtin_fmaf(-rh[k], s2[u], tv[k]), o[k]);
-                        o[k] = a.alpha * tv[k];
+                        sum[2][i][k] = __builtin_fmaf(tv[k], POST ? hh[k] * pv[k] : hh[k], sum[2][i][k]);
+                        tv[k] *= gv[k];  // u
                     }
-                    put(a.dx, a.lddx, o);
-                    if (!a.dh)
-                        continue;
-                    if (!whole) {  // what mean(c) leaves past the row's end
-                        asm volatile("");
+                }
+                if constexpr (POST) {
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            tv[k] = (TAIL ? k < cnt : cnt > 0) ? tv[k] : 0.0f;
+                    for (int k = 0; k < 8; ++k) {
+                        sum[NS - 1][i][k] = __builtin_fmaf(tv[k], hh[k], sum[NS - 1][i][k]);
+                        e[i][k] = tv[k] * pv[k];
+                        p1 += e[i][k];
+                        p2 = __builtin_fmaf(e[i][k], hh[k], p2);
                     }
-                    float hh[8], gv[8], pv[8];
-                    if constexpr (POST) {
-                        normed(cur[u].h[i], i, cur[u].post_mean, cur[u].post_rstd, hh);
-                        as_in_memory(pw[i]);
-                        widen_group<TAIL, P>(pw[i], a.D, i, t, pv);
-                    } else if (use_h) {
-                        widen_group<TAIL, P>(cur[u].h[i], a.D, i, t, hh);
-                    }
-                    if (a.gate) {
-                        as_in_memory(g[i]);
-                        widen_group<TAIL, P>(g[i], a.D, i, t, gv);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            sum[2][i][k] = __builtin_fmaf(tv[k], POST ? hh[k] * pv[k] : hh[k], sum[2][i][k]);
-                            tv[k] *= gv[k];  // u
-                        }
-                    }
-                    if constexpr (POST) {
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            sum[NS - 1][i][k] = __builtin_fmaf(tv[k], hh[k], sum[NS - 1][i][k]);
-                            e[u][i][k] = tv[k] * pv[k];
-                            p1[u] += e[u][i][k];
-                            p2[u] = __builtin_fmaf(e[u][i][k], hh[k], p2[u]);
-                        }
-                    } else {
-                        put(a.dh, a.lddh, tv);
-                    }
+                } else {
+                    put(a.dh, a.lddh, tv);
                 }
             }
             if constexpr (POST) {
                 means(p1, p2);
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    if (m + u >= m1)
-                        continue;
+                for (int i = 0; i < V; ++i) {
+                    const int at = (i * P + t) * 8;
+                    float o[8], hh[8];
+                    as_in_memory(cur.h[i]);
+                    normed(cur.h[i], i, cur.post_mean, cur.post_rstd, hh);
 #pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        const int at = (i * P + t) * 8;
-                        float o[8], hh[8];
-                        as_in_memory(cur[u].h[i]);
-                        normed(cur[u].h[i], i, cur[u].post_mean, cur[u].post_rstd, hh);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            o[k] = cur[u].post_rstd * (e[u][i][k] - p1[u] - hh[k] * p2[u]);
-                        T *q = (T *)a.dh + (m + u) * a.lddh + at;
-                        if ((i + 1) * P * 8 <= a.D || (!TAIL && at < a.D))
-                            store_all(q, o);
-                        else if constexpr (TAIL)
-                            store_n(q, a.D - at, o);
-                    }
+                    for (int k = 0; k < 8; ++k)
+                        o[k] = cur.post_rstd * (e[i][k] - p1 - hh[k] * p2);
+                    T *q = (T *)a.dh + m * a.lddh + at;
+                    if ((i + 1) * P * 8 <= a.D || (!TAIL && at < a.D))
+                        store_all(q, o);
+                    else if constexpr (TAIL)
+                        store_n(q, a.D - at, o);
                 }
             }
         }

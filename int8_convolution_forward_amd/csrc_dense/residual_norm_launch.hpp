@@ -77,14 +77,14 @@ void launch_residual_norm(const ResNormArgs &a, bool rms, bool q8, hipStream_t s
         q8 ? launch<T, false, true>(a, s) : launch<T, false, false>(a, s);
 }
 
-template <typename T, bool RMS, bool POST, int P, int V, int U, bool AHEAD, int OCC>
+template <typename T, bool RMS, bool POST, int P, int V, bool AHEAD, int OCC>
 void launch_back_rows(const ResNormBackArgs &a, int wgs, hipStream_t s)
 {
     const dim3 grid((unsigned)wgs), block(norm_threads(P));
     if (a.D % 8 == 0)
-        hipLaunchKernelGGL((residual_norm_backward_kernel<T, P, V, U, AHEAD, OCC, false, RMS, POST>), grid, block, 0, s, a);
+        hipLaunchKernelGGL((residual_norm_backward_kernel<T, P, V, AHEAD, OCC, false, RMS, POST>), grid, block, 0, s, a);
     else
-        hipLaunchKernelGGL((residual_norm_backward_kernel<T, P, V, U, AHEAD, OCC, true, RMS, POST>), grid, block, 0, s, a);
+        hipLaunchKernelGGL((residual_norm_backward_kernel<T, P, V, AHEAD, OCC, true, RMS, POST>), grid, block, 0, s, a);
 }
 
 template <typename T, bool RMS, bool POST>
@@ -99,15 +99,15 @@ void launch_back(const ResNormBackArgs &a, int wgs, hipStream_t s)
             hipLaunchKernelGGL((residual_norm_columns_kernel<T, RMS, POST>), dim3((unsigned)ceil_div(a.D, 2048), (unsigned)wgs),
                                dim3(256), 0, s, a);
     } else if (a.D <= 512) {
-        launch_back_rows<T, RMS, POST, 64, 1, 1, true, 2>(a, wgs, s);
+        launch_back_rows<T, RMS, POST, 64, 1, true, 2>(a, wgs, s);
     } else if (a.D <= 1024) {
-        launch_back_rows<T, RMS, POST, 64, 2, 1, true, 1>(a, wgs, s);
+        launch_back_rows<T, RMS, POST, 64, 2, true, 1>(a, wgs, s);
     } else if (a.D <= 2048) {
-        launch_back_rows<T, RMS, POST, 256, 1, 1, true, 2>(a, wgs, s);
+        launch_back_rows<T, RMS, POST, 256, 1, true, 2>(a, wgs, s);
     } else if (a.D <= 4096) {
-        launch_back_rows<T, RMS, POST, 512, 1, 1, true, 2>(a, wgs, s);
+        launch_back_rows<T, RMS, POST, 512, 1, true, 2>(a, wgs, s);
     } else {
-        launch_back_rows<T, RMS, POST, 512, 2, 1, (sizeof(T) == 2 && !POST), 2>(a, wgs, s);
+        launch_back_rows<T, RMS, POST, 512, 2, (sizeof(T) == 2 && !POST), 2>(a, wgs, s);
     }
 }
 

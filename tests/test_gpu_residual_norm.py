@@ -248,3 +248,25 @@ def test_same_bits_again(ci8):
         assert all(torch.equal(p, q) for p, q in zip(a, c))
         c = ci8.residual_norm_backward(t["dr"], t["dy"], a[0], t["h"], a[2], t["weight"], t["gate"], t["post_weight"])
         assert all(torch.equal(p, q) for p, q in zip(b, c))
+
+
+def test_many_long_rows(ci8):
+    """More rows, of more columns than the registers hold, than there are workgroups: each takes several
+    one after the other.  The rows overlap in memory, so that windows of one sum of squares give their norms."""
+    m, d = 65536 + 512, 16392
+    say("many long rows", m, d)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    values = torch.randn(8 * m + d, generator=g, device="cuda")
+    values *= torch.exp2(torch.linspace(-20, 20, values.numel(), device="cuda"))
+    values = values.to(torch.bfloat16)
+    x = values.as_strided((m, d), (8, 1))
+    r, y, stats = ci8.residual_norm(x, None, eps=0.0, norm="rms")
+    total = torch.cat([torch.zeros(1, device="cuda", dtype=torch.float64), values.double().square().cumsum(0)])
+    at = torch.arange(m, device="cuda") * 8
+    rstd = ((total[at + d] - total[at]) / d).rsqrt()
+    # d + 1 roundings of a sum of positive terms in 32 bits, halved by the root, and three of the quotient and the root
+    assert bool(((stats[1].double() / rstd - 1).abs() <= (d / 2 + 4) * 2.0 ** -24).all())
+    for row in (0, 1, 65535, 65536, m - 1):
+        want = x[row].double() * rstd[row]
+        bound = want.abs() * (2.0 ** -8 + (d / 2 + 8) * 2.0 ** -24)
+        assert bool(((y[row].double() - want).abs() <= bound).all())
