@@ -235,11 +235,24 @@ conv_i8_status_t analyze(const dense_linear_fp8_t *args, LinearF8Plan *p)
     DENSE_TRY(forced_tile(&forced));
     DENSE_TRY(plan_bytes(d.x, &p->a));
     DENSE_TRY(plan_bytes(d.w, &p->b));
-    p->skinny = p->M <= 32 && p->N <= ((int64_t)1 << 25) && !p->a.packed && !p->b.packed && !forced.on;
+    // Without a copy, up to 32 rows (us, all of BF16 results; the other side is the best tile and split):
+    //   rows x w         1 x 4096x4096    16 x 4096x4096    17 x 4096x4096    17 x 8192x4096    17 x 16384x4096
+    //   few rows' / tiles   5.9 / 9.8        6.4 / 10.6        8.4 / 10.5       16.5 / 14.1        30.1 / 18.8
+    // Above 16 rows the copies of x leave LDS for one workgroup on a CU, which has half the weights of
+    // that in flight: it pays while each CU has one workgroup in all.  A 32-bit result costs the tiles twice.
+    const bool one_each = ceil_div(p->N, 16) <= kCUs;
+    p->skinny = p->M <= (one_each || d.y.dtype == DENSE_FP32 ? 32 : 16) && p->N <= ((int64_t)1 << 25) && !p->a.packed &&
+                !p->b.packed && !forced.on;
     if (p->skinny) {
+        // A wave for each group of four blocks of K, as far as LDS has room: 1 x 4096x4096 6.5 us with 4
+        // waves, 5.9 with 8, 6.1 with 16; 1 x 1024x8192 7.0, 5.4, 5.2; 1 x 8192x1024 4.4, 4.5, 5.9.  With x
+        // in LDS as well, 8 waves fill it: where CUs have several workgroups, two of 4 waves do more (16 x
+        // 16384x4096: 22.4 us with 8, 18.9 with 4; 16 x 4096x4096: 6.5 and 7.3).
         const int64_t groups = ceil_div(p->K, 4 * kBlock);
-        // as many as LDS has room for
-        p->waves = groups <= 4 || p->M > 16 ? 4 : groups <= 8 || p->M > 4 ? 8 : 16;
+        if (groups <= 4 || p->M > 16 || (p->M > 4 && !one_each))
+            p->waves = 4;
+        else
+            p->waves = groups <= 8 || p->M > 4 ? 8 : 16;
         return CONV_I8_OK;
     }
     p->wide = d.y.dtype == DENSE_FP32;
@@ -248,7 +261,7 @@ conv_i8_status_t analyze(const dense_linear_fp8_t *args, LinearF8Plan *p)
         DENSE_TRY(plan_wide(d.x, &p->a));
         DENSE_TRY(plan_wide(d.w, &p->b));
     }
-    plan_gemm(p->M, p->N, p->K, p->wide ? 2 : 1, forced, &p->gemm);
+    plan_gemm(p->M, p->N, p->K, p->wide ? 2 : 1, forced, &p->gemm, p->wide ? kCost : kCostF8);
     if (!grid_fits(p->gemm, p->M) || !launch_fits(pack_wgs(p->a) + pack_wgs(p->b), 256))
         return CONV_I8_ERR_UNSUPPORTED;
     p->ws_bytes = p->a.pack_bytes + p->b.pack_bytes + p->gemm.part_bytes;
@@ -451,7 +464,7 @@ conv_i8_status_t analyze(const dense_linear_fp8_backward_t *args, BackwardF8Plan
     if (p->want_dx) {
         DENSE_TRY(quantised(M, N, &p->ga, &p->g_bytes, &p->gs_bytes));
         DENSE_TRY(plan_bytes(d.wt, &p->wb));
-        apart += plan_gemm(M, p->K, N, 1, forced, &p->dx);
+        apart += plan_gemm(M, p->K, N, 1, forced, &p->dx, kCostF8);
         if (!grid_fits(p->dx, M))
             return CONV_I8_ERR_UNSUPPORTED;
         p->part_bytes = p->dx.part_bytes;
@@ -459,9 +472,9 @@ conv_i8_status_t analyze(const dense_linear_fp8_backward_t *args, BackwardF8Plan
     if (p->want_dw) {
         DENSE_TRY(quantised(N, M, &p->gt, &p->gt_bytes, &p->gts_bytes));
         DENSE_TRY(plan_bytes(d.xt, &p->xb));
-        apart += plan_gemm(N, p->K, M, 1, forced, &p->dw);
+        apart += plan_gemm(N, p->K, M, 1, forced, &p->dw, kCostF8);
         // apart: a launch more, and the bias gradient's
-        if (p->want_dx && !forced.on && pair_cost(M, N, p->K, 1) < apart + 4.0) {
+        if (p->want_dx && !forced.on && pair_cost(M, N, p->K, 1, kCostF8) < apart + 4.0) {
             set_plan(M, p->K, N, 1, kPairTile, 1, &p->dx);
             set_plan(N, p->K, M, 1, kPairTile, 1, &p->dw);
             p->part_bytes = 0;

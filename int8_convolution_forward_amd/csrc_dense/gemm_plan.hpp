@@ -132,23 +132,34 @@ struct GemmPlan {
 // 64x8192x8192 take 13 to 17 % more.
 struct TileCost {
     double stage;  // us per 64 bytes of the inner dimension of one workgroup
+    double alone;  // the same of the only one on its CU
     double round;  // us per round of workgroups
     double out;    // us per 10^6 outputs
 };
 constexpr TileCost kCost[kTiles] = {
-    {0.536, 8.2, 0.45},
-    {0.259, 4.4, 0.45},
-    {0.089, 3.8, 0.90},
-    {0.194, 4.8, 0.45},
+    {0.536, 0.536, 8.2, 0.45},
+    {0.259, 0.259, 4.4, 0.45},
+    {0.089, 0.089, 3.8, 0.90},
+    {0.194, 0.194, 4.8, 0.45},
+};
+// Of 8-bit floating point, whose stage has twice the products of a 16-bit one and waits for
+// its scales.  Of 22 shapes from 64x1024x1024 to 8192x8192x2048 its choice is within 4 % of the
+// best one for all (128x512x4096: 10.1 us in four parts, 14.7 unsplit as the constants above would
+// have it); of 17 to 100 rows with 8192 to 32768 rows of w it is 2 to 24 % from it.
+constexpr TileCost kCostF8[kTiles] = {
+    {0.550, 0.550, 8.2, 0.45},
+    {0.275, 0.275, 4.4, 0.45},
+    {0.120, 0.155, 3.8, 0.90},
+    {0.290, 0.290, 4.8, 0.45},
 };
 
-double gemm_cost(int tile, int64_t M, int64_t N, int64_t kbytes, int splits)
+double gemm_cost(const TileCost *costs, int tile, int64_t M, int64_t N, int64_t kbytes, int splits)
 {
     const Tile &t = kTile[tile];
-    const TileCost &c = kCost[tile];
+    const TileCost &c = costs[tile];
     const int64_t wgs = ceil_div(M, t.tm) * ceil_div(N, t.tn) * splits;
     const int64_t per_cu = ceil_div(wgs, kCUs);
-    const double stages = (double)(per_cu * ceil_div(kbytes, 64 * splits)) * c.stage;
+    const double stages = (double)(per_cu * ceil_div(kbytes, 64 * splits)) * (per_cu > 1 ? c.stage : c.alone);
     const double rounds = (double)ceil_div(per_cu, t.occ) * c.round;
     const double busy = t.occ == 1 ? stages + rounds : stages + c.round > rounds ? stages + c.round : rounds;
     const double mn = 1.0e-6 * (double)M * (double)N;
@@ -157,14 +168,14 @@ double gemm_cost(int tile, int64_t M, int64_t N, int64_t kbytes, int splits)
 
 // The same of both gradients' products in one launch with tile kPairTile:
 // either all CUs work through both, or the longer reduction lasts longest.
-double pair_cost(int64_t M, int64_t N, int64_t K, int es = 2)
+double pair_cost(int64_t M, int64_t N, int64_t K, int es = 2, const TileCost *costs = kCost)
 {
     const Tile &t = kTile[kPairTile];
-    const TileCost &c = kCost[kPairTile];
+    const TileCost &c = costs[kPairTile];
     const double sx = (double)ceil_div(es * N, 64), sw = (double)ceil_div(es * M, 64);
     const double all = (sx * (double)ceil_div(M, t.tm) + sw * (double)ceil_div(N, t.tm)) * (double)ceil_div(K, t.tn) / kCUs;
     const double longest = sx > sw ? sx : sw;
-    return (all > longest ? all : longest) * c.stage + c.round + c.out * 1.0e-6 * (double)(M + N) * (double)K;
+    return (all > longest ? all : longest) * c.alone + c.round + c.out * 1.0e-6 * (double)(M + N) * (double)K;
 }
 
 // CONV_I8_DENSE_TILE, for tests and sweeps: "128x128" names a tile for every
@@ -217,14 +228,14 @@ void two_terms(int64_t M, GemmPlan *p)
 }
 
 // Returns the microseconds expected.
-double plan_gemm(int64_t M, int64_t N, int64_t K, int es, const Forced &forced, GemmPlan *p)
+double plan_gemm(int64_t M, int64_t N, int64_t K, int es, const Forced &forced, GemmPlan *p, const TileCost *costs = kCost)
 {
     const int64_t nstages = ceil_div(K * es, kStageBytes);
     if (forced.on && forced.split > 0) {
         // of a product with fewer than four stages for each part, as many parts as have four
         const int64_t most = nstages / 4 > 1 ? nstages / 4 : 1;
         set_plan(M, N, K, es, forced.tile, (int)(forced.split < most ? forced.split : most), p);
-        return gemm_cost(forced.tile, M, N, K * es, p->splits);
+        return gemm_cost(costs, forced.tile, M, N, K * es, p->splits);
     }
     int best = 0, best_s = 1;
     double least = 1e30;
@@ -240,7 +251,7 @@ double plan_gemm(int64_t M, int64_t N, int64_t K, int es, const Forced &forced, 
             // 16.3 us, 128x128 14.0)
             if (!forced.on && kTile[t].deep && tiles * s > kCUs)
                 break;
-            const double us = gemm_cost(t, M, N, K * es, s);
+            const double us = gemm_cost(costs, t, M, N, K * es, s);
             if (us < least) {
                 least = us;
                 best = t;

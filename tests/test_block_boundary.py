@@ -350,6 +350,13 @@ def test_plans(monkeypatch):
     big = dict(x=mat(512, 1024, E4), w=mat(256, 1024, E4), y=mat(512, 256, BF16), xs=mat(512, 8, E8), ws=mat(2, 8, E8))
     assert "a=rows b=rows" in plan(linear(**big)) and "stages=8 " in plan(linear(**big))
     assert "b=rows_packed" in plan(linear(**{**big, "w": mat(256, 1024, E4, rs=1, cs=256)}))
+    few = lambda m, n, k, dt=BF16: plan(linear(x=mat(m, k, E4), w=mat(n, k, E4), y=mat(m, n, dt),  # noqa: E731
+                                               xs=mat(m, k // 128, E8), ws=mat(n, k // 128, E8)))
+    for m, n, k, waves in ((1, 4096, 1024, 4), (4, 8192, 4096, 8), (4, 512, 8192, 16), (16, 4096, 8192, 8),
+                           (16, 4112, 8192, 4), (17, 4096, 8192, 4), (32, 4096, 512, 4)):
+        assert few(m, n, k) == few(m, n, k, FP32) == f"kernel=skinny waves={waves}"
+    assert few(17, 4112, 1024).startswith("kernel=gemm tile") and few(17, 4112, 1024, FP32).startswith("kernel=skinny")
+    assert few(33, 512, 1024).startswith("kernel=gemm tile") and few(33, 512, 1024, FP32).startswith("kernel=gemm_bf16")
     for tile, tiles in (("256x256", 2), ("128x128", 8), ("64x64", 32)):
         monkeypatch.setenv("CONV_I8_DENSE_TILE", tile + "/2")
         assert f"tile={tile} tiles={tiles} split=2" in plan(linear(**big))

@@ -139,7 +139,7 @@ def operands(g, m, n, k, xform=E4, tiles=True):
 
 SHAPES = [(1, 1, 1), (1, 48, 128), (3, 130, 272), (1, 2048, 8192), (4, 100, 4096), (5, 64, 640), (16, 256, 2064),
           (17, 33, 1040), (32, 520, 4112), (33, 65, 128), (64, 64, 2176), (7, 40, 333), (130, 257, 1001), (200, 300, 5000),
-          (256, 512, 16), (513, 260, 768)]
+          (256, 512, 16), (513, 260, 768), (9, 4100, 4112), (16, 8208, 2064), (17, 4112, 1040), (32, 4100, 640)]
 
 
 @pytest.mark.parametrize("m,n,k", SHAPES)
