@@ -108,6 +108,44 @@ def test_refusals(ci8):
         ci8.clip_grad_norm([x, p], 100.0)
 
 
+def next_to_the_middle(dtype):
+    """(value, factor) pairs whose product is a little above the middle of two numbers of `dtype`, by more than a
+    rounding to 32 bits takes off, where a factor and a product of 32 bits give the middle or less."""
+    bits = {torch.bfloat16: 8, torch.float16: 11}[dtype]
+    found = []
+    for i in range(1, 9000, 2):
+        value = 1.0 + (i % 2 ** (bits - 1)) * 2.0 ** (1 - bits)
+        middle = 0.5 + (2 * ((7 * i) % 2 ** (bits - 2)) + 0.5) * 2.0 ** -bits  # above an even number
+        factor = middle * (1 + 0.8 * 2.0 ** -23) / value
+        near = torch.tensor(value) * torch.tensor(factor, dtype=torch.float64).float()
+        if value * factor > middle >= float(near) and float(torch.tensor(value * factor, dtype=torch.float64).float()) > middle:
+            found.append((value, factor))
+    return found
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
+def test_products_next_to_the_middle(ci8, dtype):
+    """16-bit values times the factor in 64 bits: the sum of squares is exact here, and so the factor is the same."""
+    pairs = next_to_the_middle(dtype)
+    assert len(pairs) > 20
+    for value, factor in pairs[::max(1, len(pairs) // 20)]:
+        g = [torch.full((9,), value, device="cuda", dtype=dtype), torch.full((40,), -value, device="cuda", dtype=dtype)]
+        limit = factor * (7 * value)  # 49 values: the norm is exact
+        want = [(v.double() * (limit / (7 * value))).float().to(dtype) for v in g]
+        assert float(ci8.clip_grad_norm(g, limit)) == 7 * value
+        assert all(torch.equal(a, b) for a, b in zip(g, want)), (value, factor)
+
+
+def test_factors_far_below_32_bits(ci8):
+    """Factors of 2^-130 to 2^-240, whose products with BF16 values are still numbers of that type: the same rounding."""
+    for up, limit in ((100, 1.7 * 2.0 ** -30), (120, 1.3 * 2.0 ** -70), (120, 1.9 * 2.0 ** -100), (126, 1.1 * 2.0 ** -114)):
+        g = [(torch.arange(1, 129, device="cuda") / 128 * 2.0 ** up).to(torch.bfloat16)]
+        norm = math.sqrt(float(g[0].double().square().sum()))
+        want = (g[0].double() * (limit / norm)).to(torch.bfloat16)
+        ci8.clip_grad_norm(g, limit)
+        assert bool(want.any()) and torch.equal(g[0], want), (up, limit)
+
+
 def test_range(ci8):
     """Squares that 32 bits cannot hold; norms that are not finite change nothing; zeros."""
     big = [torch.full((1000,), 3e38, device="cuda"), torch.full((10,), 1e-38, device="cuda")]
