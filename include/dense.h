@@ -311,11 +311,13 @@ conv_i8_status_t dense_residual_norm_backward(const dense_residual_norm_backward
 
 /*
  * norm = sqrt(sum of squares of all elements of all tensors), summed in 64 bits;
- * out = in min(1, max_norm / norm).  A norm that is not finite leaves the values as they are
- * (the caller sees it in `norm`).  in and out: `count` vectors of BF16, FP16 or
- * FP32; an out is its in itself, or of the same type and size and overlaps
- * no other vector.  No two vectors of `in` overlap where they are written, and
- * `norm` lies in none of them.
+ * out = in min(1, max_norm / norm), a product of 64 bits rounded to 32 and to the
+ * type.  Where an element is infinite or NaN, `norm` is too and all values stay as
+ * they are.  Finite elements always follow the formula, also where their norm is
+ * beyond what 32 bits hold and `norm` reads as infinity.  in and out: `count`
+ * vectors of BF16, FP16 or FP32; an out is its in itself, or of the same type and
+ * size and overlaps no other vector.  No two vectors of `in` overlap where they are
+ * written, and `norm` lies in none of them.
  */
 typedef struct {
     const dense_vec_t *in, *out;

@@ -165,7 +165,7 @@ __global__ __launch_bounds__(kClipThreads) void clip_scale_kernel(const ClipTabl
     const double size = sqrt(group_sum64(s, red));
     if (norm && blockIdx.x == 0 && threadIdx.x == 0)
         *norm = (float)size;
-    // a norm that is not finite changes nothing, nor does one within the limit
+    // a norm that is not finite in 64 bits (an element is not) changes nothing, nor does one within the limit
     const bool clips = size > max_norm && size < INFINITY;
     const double factor = clips ? max_norm / size : 1.0;
     clip_walk(t, [&](int i, int64_t at) {

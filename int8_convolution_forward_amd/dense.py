@@ -471,7 +471,9 @@ def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, out: Optional
                    stream=None) -> torch.Tensor:
     """The 2-norm of all values of `grads` together (fp32, on their device, summed
     in 64 bits); they are multiplied by min(1, max_norm / norm), in place or into
-    `out`.  A norm that is not finite leaves the values as they are.
+    `out`.  An infinity or NaN among the values makes the norm infinite or NaN and
+    leaves all of them as they are.  Finite values are scaled also where their norm
+    is beyond fp32 and reads as infinity.
 
     grads: bf16, fp16 or fp32 tensors on one GPU, of any number and shapes, each
     without gaps in memory (in any order of its dims); out: as many, of the same types, shapes and

@@ -146,6 +146,21 @@ def test_factors_far_below_32_bits(ci8):
         assert bool(want.any()) and torch.equal(g[0], want), (up, limit)
 
 
+def test_norms_that_32_bits_do_not_hold(ci8):
+    """Finite values whose norm reads as infinity are scaled by it all the same, in place and into `out`; only values
+    that are not finite stay as they are."""
+    for dtype in (torch.bfloat16, torch.float32):
+        grads = [torch.full((5000,), 3e38, device="cuda", dtype=dtype), make([33], 2, dtype)[0]]
+        norm, want = expected(grads, 8.0)
+        assert norm > torch.finfo(torch.float32).max
+        out = [torch.empty_like(g) for g in grads]
+        assert float(ci8.clip_grad_norm(grads, 8.0, out=out)) == math.inf
+        assert float(ci8.clip_grad_norm(grads, 8.0)) == math.inf
+        for a, b, c in zip(grads, out, want):
+            assert torch.equal(a, b)
+            close(a, c)
+
+
 def test_range(ci8):
     """Squares that 32 bits cannot hold; norms that are not finite change nothing; zeros."""
     big = [torch.full((1000,), 3e38, device="cuda"), torch.full((10,), 1e-38, device="cuda")]
