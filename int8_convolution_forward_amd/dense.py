@@ -337,7 +337,8 @@ def quantize_fp8(x: torch.Tensor, block: str = "rows", transposed: bool = False,
 
 def dequantize_fp8(q: torch.Tensor, scale: torch.Tensor, dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
     """q * scale in bf16, fp16 or fp32, of what quantize_fp8 gave (either kind of
-    block).  bf16 and fp32 hold such values exactly."""
+    block): exact where the value is in the type's range, else rounded to its
+    smallest steps (bf16's are 2^-133) or to infinity (3.4e38 is 2^128 in 8 bits)."""
     x = _call(_native.dequantize, stream, q, scale, dtype)
     if type(x) is int:
         _refuse(x, 2, q=q, scale=scale)
@@ -352,9 +353,19 @@ def linear_fp8(x: torch.Tensor, w: torch.Tensor, x_scale: torch.Tensor, w_scale:
 
     x [..., K]: float8_e4m3fn or float8_e5m2, x_scale [..., ceil(K / 128)]; w [N,
     K]: float8_e4m3fn, w_scale [N, ceil(K / 128)] or [ceil(N / 128), ceil(K /
-    128)]; scales in float8_e8m0fnu, as quantize_fp8 gives them.  Products and
-    sums are those of 32 bits.  The result [..., N] is bf16 by default, or fp16
-    or fp32; bias, residual, preact and out as in linear.
+    128)]; scales in float8_e8m0fnu, as quantize_fp8 gives them.  The result [...,
+    N] is bf16 by default, or fp16 or fp32; bias, residual, preact and out as in
+    linear.
+
+    With out_dtype fp32, products and sums are those of 32 bits (of scaled operands
+    of 2^-126 and more, which BF16 holds).  So are those of
+    a 16-bit result of up to 32 rows (16 where N > 4096) whose x and w can be read
+    in place (K and the strides of their rows multiples of 16, 16-byte aligned
+    memory).  Any other 16-bit result is the matrix unit's on 8-bit operands: of
+    the products of eight consecutive k, what lies more than 13 bits below the
+    largest is cut off before they are summed in 32 bits.  That is below the
+    rounding to 16 bits unless a sum cancels; the same row may differ by it between
+    calls of few and of many rows.
     """
     y = _call(_native.linear_fp8, stream, x, w, x_scale, w_scale, bias, _activation(activation), residual, out_dtype, preact,
               out)
@@ -385,7 +396,10 @@ def linear_fp8_backward(dy: torch.Tensor, xt: Optional[torch.Tensor], xt_scale: 
     for dw.  xt [K, rows] and wt [K, N] with their scales are the transposed
     copies that quantize_fp8 gives (float8_e4m3fn, either kind of block); xt is
     not needed without dw, wt not without dx.  The gradient of linear_fp8's
-    residual is dy.
+    residual is dy.  Both products are the matrix unit's on 8-bit operands: of the
+    products of eight consecutive inner elements, what lies more than 13 bits below
+    the largest is cut off before they are summed in 32 bits; dbias sums g in 32
+    bits.
     """
     r = _call(_native.linear_fp8_backward, stream, dy, xt, xt_scale, wt, wt_scale, preact, _activation(activation),
               bool(need_dx), bool(need_dw), bool(need_dbias), g_dtype)
