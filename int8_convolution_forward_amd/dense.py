@@ -471,9 +471,10 @@ def residual_norm_backward(dr: Optional[torch.Tensor], dy: torch.Tensor, r: torc
                            need_params: bool = True, stream=None) -> Tuple[Optional[torch.Tensor], ...]:
     """(dx, dh, dweight, dbias, dgate, dpost_weight) of residual_norm, from the
     gradients of r (None: zero) and y, and what the forward pass gave.  None
-    stands for the gradient of what is absent and, without need_params, for the
-    last four.  dgate has gate's shape, each of its rows summed over the rows that
-    shared it."""
+    stands for dh, dgate and dpost_weight where h, gate and post_weight are absent
+    and, without need_params, for the last four; dweight and dbias are given also
+    where there was no weight or bias.  dgate has gate's shape, each of its rows
+    summed over the rows that shared it."""
     g = _call(_native.residual_norm_backward, stream, dr, dy, r, h, stats, weight, gate, post_weight, scale,
               _norm_kind(norm), bool(need_params))
     if type(g) is int:
