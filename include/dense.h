@@ -141,7 +141,9 @@ conv_i8_status_t dense_linear_backward_plan(const dense_linear_backward_t *args,
  * Layer norm over the columns of x [M, D] (BF16, FP16 or FP32, col_stride 1,
  * D >= 1).  weight and bias: D of x's type.  y [M, D] has x's type, or INT8:
  * then row m holds round(y / s) with s = max |y| / 127 in scale[m] (a row of
- * zeros has scale 0).  mean and rstd (M of FP32) may be absent.
+ * zeros has scale 0).  mean and rstd (M of FP32) may be absent.  Squares are summed
+ * in 32 bits: a row whose squared distances from its mean add up to 2^128 or more
+ * has rstd 0 and becomes its bias.
  */
 typedef struct {
     dense_mat_t x, y;
@@ -266,6 +268,11 @@ conv_i8_status_t dense_linear_fp8_backward_plan(const dense_linear_fp8_backward_
  * Without h, gate, post_weight and r are absent as well.  r may be x or h
  * itself.  y may be E4M3, with a scale for each 128 of a row in y_scale
  * [M, ceil(D/128)], as dense_quantize gives of the unrounded y.
+ *
+ * Squares are summed in 32 bits, where they have to stay below 2^128 (a deviation of
+ * 2^64 / sqrt(D), which FP16 does not reach): beyond, and with an infinity or NaN in it, a
+ * row's rstd is NaN and with it the normed row.  Squares below 2^-126 lose digits, which
+ * shows with an eps below 1e-22 only; eps is taken in 32 bits.
  */
 typedef enum { DENSE_LAYER_NORM = 0, DENSE_RMS_NORM = 1 } dense_norm_t;
 

@@ -61,6 +61,16 @@ __device__ __forceinline__ void moments(float (&v)[V][8], int D, int t, float co
     }
 }
 
+// 1 / deviation from the sum of squares m2 of d columns.  NaN where 32 bits do not hold
+// m2: by the formula that row, finite as its values may be, would become its
+// bias with no gradient, and nobody would see it.  (Taking such a row again, divided by a
+// power of two, costs the registers of the usual ones: 8192 x 4096 BF16 with both norms
+// and gates 62.3 us instead of 57.5, 4096 x 8192 54.0 instead of 49.3.)
+__device__ __forceinline__ float inverse_deviation(float m2, float d, float eps)
+{
+    return m2 < INFINITY ? 1.0f / sqrtf(m2 / d + eps) : __builtin_nanf("");
+}
+
 template <typename T, int P, int V, bool HOLD, bool TAIL, bool RMS, bool Q8>
 __global__ __launch_bounds__(norm_threads(P)) void residual_norm_kernel(const ResNormArgs a)
 {
@@ -109,7 +119,7 @@ __global__ __launch_bounds__(norm_threads(P)) void residual_norm_kernel(const Re
             if (a.post_weight) {
                 moments<P, V, RMS>(n, a.D, t, cols, a.d, red[set], mean, m2);
                 set ^= 1;  // the other set: a slow wave may still read this one
-                const float rstd = 1.0f / sqrtf(m2 / a.d + a.eps);
+                const float rstd = inverse_deviation(m2, a.d, a.eps);
                 if (t == 0) {
                     if (a.post_mean)
                         a.post_mean[m] = mean;
@@ -154,7 +164,7 @@ __global__ __launch_bounds__(norm_threads(P)) void residual_norm_kernel(const Re
         }
         moments<P, V, RMS>(v, a.D, t, cols, a.d, red[set], mean, m2);
         set ^= 1;
-        const float rstd = 1.0f / sqrtf(m2 / a.d + a.eps);
+        const float rstd = inverse_deviation(m2, a.d, a.eps);
         if (t == 0) {
             if (a.mean)
                 a.mean[m] = mean;
@@ -237,7 +247,7 @@ __global__ __launch_bounds__(P) void residual_norm_any_kernel(const ResNormArgs 
                 for (int k = 0; k < 8; ++k)
                     s = __builtin_fmaf(v[k] - mean, v[k] - mean, s);
             }
-            rstd = 1.0f / sqrtf(sum(s) / a.d + a.eps);
+            rstd = inverse_deviation(sum(s), a.d, a.eps);
         };
         float mean, rstd;
         const T *src = x;

@@ -445,6 +445,10 @@ def residual_norm(x: torch.Tensor, h: Optional[torch.Tensor], weight: Optional[t
     other (a gate for each sequence of a batch).  stats, which
     residual_norm_backward takes, holds mean and rstd of r and, with
     post_weight, of h: fp32, [2 or 4, *x's leading shape] (means of "rms" are 0).
+
+    A row whose squares add up to more than fp32 holds (a deviation of 2^64 /
+    sqrt(D), 2.9e17 for D = 4096) has NaN for rstd and is NaN where it is normed,
+    as one with an infinity or NaN is.
     """
     r = _call(_native.residual_norm, stream, x, h, weight, bias, gate, post_weight, scale, _norm_kind(norm), eps, False)
     if type(r) is int:

@@ -208,6 +208,37 @@ def test_edges_of_the_range(ci8):
             check_forward(ci8, keep, 1.0, kind, (d, kind))
 
 
+@pytest.mark.parametrize("d", [5, 40, 1000, 2048, 5000, 9000, 17000])
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_rows_whose_squares_32_bits_do_not_hold(ci8, d, kind, dtype):
+    """They are NaN, by either norm and in the gradients, and stay in their row; right up to there."""
+    t = inputs(8, d, DTYPES[dtype], None, True)
+    usual = ci8.residual_norm(t["x"], t["h"], t["weight"], t["bias"], post_weight=t["post_weight"], norm=kind)
+    for name, row in (("x", 2), ("h", 5)):
+        for big in (1e25, 3e30):
+            v = {**t, name: t[name].clone()}
+            v[name][row] = (v[name][row].float() * big).to(DTYPES[dtype])
+            args = (v["x"], v["h"], t["weight"], t["bias"])
+            say("residual_norm", d, kind, dtype, name, big)
+            r, y, stats = ci8.residual_norm(*args, post_weight=t["post_weight"], norm=kind)
+            _, q, s = ci8.residual_norm_fp8(*args, post_weight=t["post_weight"], norm=kind)
+            others = [i for i in range(8) if i != row]
+            assert bool(torch.isnan(y[row]).all()) and bool(torch.isnan(stats[1, row]))
+            assert bool(torch.isnan(ref.values(q, s)[row]).all())
+            assert bool(torch.isfinite(r[row]).all()) == (name == "x") and bool(torch.isnan(stats[3, row])) == (name == "h")
+            assert all(torch.equal(a[..., others] if a is stats else a[others], b[..., others] if a is stats else b[others])
+                       for a, b in zip((r, y, stats), usual))
+            dx, dh, *_ = ci8.residual_norm_backward(t["dr"], t["dy"], r, v["h"], stats, t["weight"], post_weight=t["post_weight"],
+                                                    norm=kind)
+            assert bool(torch.isnan(dx[row]).all()) and bool(torch.isfinite(dx[others]).all()) and bool(torch.isfinite(dh[others]).all())
+    # 2^60 / sqrt(d), with the values of `inputs` up to 2^4 of it
+    fits = inputs(8, d, DTYPES[dtype], None, True)
+    up = 2.0 ** math.floor(60 - 0.5 * math.log2(d))
+    fits["x"], fits["h"] = (fits["x"] * up), (fits["h"] * up)
+    check_forward(ci8, fits, 0.75, kind, (d, dtype, kind))
+
+
 @pytest.mark.parametrize("d", [70, 1100, 9000])
 @pytest.mark.parametrize("kind", ["layer", "rms"])
 def test_gradients_against_differences(ci8, d, kind):
