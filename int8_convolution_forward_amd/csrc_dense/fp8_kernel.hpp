@@ -86,7 +86,8 @@ struct QuantArgs {
 // Rows of 1 x 128 blocks: a wave takes 512 columns of four rows, eight a lane, so
 // that sixteen lanes hold a block.  Four rows' loads are in flight at once.  Without
 // a transposed copy or tiles nothing passes between waves, so this takes the place
-// of the kernel below, with its barriers and LDS.
+// of the kernel below, with its barriers and LDS.  8192 x 8192 BF16: 36 us (202 MB, 5.6 TB/s);
+// 16 x 4096, 64 x 8192 and 777 x 1032 3.9 to 4.4, a launch.
 template <typename T>
 __global__ __launch_bounds__(256) void quantize_rows_kernel(const QuantArgs a)
 {

@@ -9,8 +9,11 @@
 // taken: the backward pass, which reads it back, then works on the same values.
 //
 // A thread group walks over rows and has the next one's loads in flight while it
-// works on the present one (HOLD; workgroups of 1024 threads have 128 registers
-// each and do neither that nor keep the weights).
+// works on the present one (HOLD).  Workgroups of 1024 threads, for rows of more than
+// 8192 columns, have 128 registers each and do neither that nor keep the weights;
+// layer norm spills all the same, 16 to 37 registers of BF16 and 45 to 72 of FP32 (rms
+// none and up to 8), which shows: r and y of 4096 x 16384 BF16 106 us as rms (537 MB,
+// 5.1 TB/s), 157 as layer norm, 4096 x 12288 82 and 146.
 #pragma once
 
 #include "colsum.hpp"
@@ -744,7 +747,9 @@ __global__ __launch_bounds__(P) void residual_norm_backward_any_kernel(const Res
 }
 
 // ... and the columns' sums of the rows of workgroup blockIdx.y of the kernel above,
-// 2048 columns a workgroup here.
+// 2048 columns a workgroup here.  Both read every operand, so that a call with a norm
+// of h takes 410 us for 4096 x 12288 BF16 (its 604 MB once: 112 at a copy's rate) and
+// 486 for 4096 x 16384.
 template <typename T, bool RMS, bool POST>
 __global__ __launch_bounds__(256) void residual_norm_columns_kernel(const ResNormBackArgs a)
 {

@@ -43,8 +43,8 @@ void launch_rows(const ResNormArgs &a, hipStream_t s)
 }
 
 // Two rows or more for each thread group, as layer norm's kernel takes them.  16384 x
-// 4096 BF16 with both norms and a gate: 107 to 111 us with 256 threads for a row (537 MB,
-// 5.0 TB/s), 132 with 512, which wait twice as long at its four reductions.
+// 4096 BF16 with both norms and a gate: 108 to 118 us with 256 threads for a row, by where its
+// memory lies (537 MB, 4.6 to 5.0 TB/s), 132 with 512, which wait twice as long at its four reductions.
 template <typename T, bool RMS, bool Q8>
 void launch(const ResNormArgs &a, hipStream_t s)
 {
@@ -109,6 +109,7 @@ void launch_back(const ResNormBackArgs &a, int wgs, hipStream_t s)
     } else if (a.D <= 4096) {
         launch_back_rows<T, RMS, POST, 512, 1, true, 2>(a, wgs, s);
     } else {
+        // FP32 with a norm of h spills 30 (rms) to 86 registers (4096x8192: 207 us as rms, 251 as layer norm, 805 MB)
         launch_back_rows<T, RMS, POST, 512, 2, (sizeof(T) == 2 && !POST), 2>(a, wgs, s);
     }
 }
