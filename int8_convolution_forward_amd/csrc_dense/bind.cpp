@@ -704,8 +704,9 @@ PyObject *clip_grad_norm(PyObject *, PyObject *const *o, Py_ssize_t n)
                 to[i] = outs ? in.get(PySequence_Fast_GET_ITEM(outs, i), true, true) : g;
                 if (to[i]->sizes() != g->sizes())
                     throw Stop{CONV_I8_ERR_OUT_DIMS};
-                if (to[i]->strides() != g->strides() && g->numel() > 1)
-                    throw Stop{CONV_I8_ERR_STRIDES};
+                for (int64_t d = 0; d < g->dim(); ++d)  // strides of dims of one mean nothing
+                    if (g->size(d) > 1 && g->numel() > 0 && to[i]->stride(d) != g->stride(d))
+                        throw Stop{CONV_I8_ERR_STRIDES};
                 a[i] = flat(*g);
                 b[i] = flat(*to[i]);
             }

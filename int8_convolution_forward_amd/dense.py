@@ -495,8 +495,8 @@ def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, out: Optional
     is beyond fp32 and reads as infinity.
 
     grads: bf16, fp16 or fp32 tensors on one GPU, of any number and shapes, each
-    without gaps in memory (in any order of its dims); out: as many, of the same types, shapes and
-    strides.  Memory that is written may belong to one tensor only.
+    without gaps in memory (in any order of its dims); out: as many, of the same
+    types, shapes and strides (of dims longer than one).  Memory that is written may belong to one tensor only.
     """
     grads = list(grads)
     out = None if out is None else list(out)

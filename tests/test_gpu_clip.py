@@ -88,6 +88,17 @@ def test_shapes_and_strides(ci8):
         close(a, b.double() / 2)
 
 
+def test_out_with_other_strides_along_dims_of_one(ci8):
+    """They say nothing about where the values lie: a gradient of a column as its transpose leaves it."""
+    base = torch.arange(1.0, 41, device="cuda")
+    for g, out in ((base.reshape(1, 40).t(), torch.zeros(40, 1, device="cuda")),
+                   (base.as_strided((1, 5, 8), (3, 8, 1)), torch.zeros(1, 5, 8, device="cuda")),
+                   (base[:1].as_strided((1, 1), (7, 9)), torch.zeros(1, 1, device="cuda"))):
+        norm = reference([g])
+        ci8.clip_grad_norm([g], norm / 2, out=[out])
+        close(out, g.double() / 2)
+
+
 def test_refusals(ci8):
     x = torch.ones(8, 8, device="cuda")
     for grads, out, status in (([x[:, ::2]], None, "STRIDES"), ([x[:, :4]], None, "STRIDES"), ([x[:1].expand(4, 8)], None, "STRIDES"),
